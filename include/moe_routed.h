@@ -70,7 +70,8 @@ typedef enum {
     MOE_ERR_SCRATCH = -7    /* moe_fused_decode_noalloc: the step needs more than its fixed scratch */
 } moe_status;
 
-typedef enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_F16 = 2 } moe_dtype;
+/* MOE_E4M3 (codes with 1x128 scales) is taken by moe_b16_grouped_wgrad's saved operand only. */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_F16 = 2, MOE_E4M3 = 3 } moe_dtype;
 /* Gated activations h = act(gate) * up: the five GLU variants (SwiGLU, GEGLU with the exact GELU,
  * ReGLU, GLU, bilinear); IDENTITY quantizes its input as is. */
 typedef enum {
@@ -439,6 +440,125 @@ int moe_fused_decode_noalloc(const uint16_t* x_bf16, int64_t T, int64_t H, int64
                              const uint8_t* w13_q, const float* w13_s,
                              const uint8_t* w2_q, const float* w2_s,
                              uint16_t* out_bf16, void* stream);
+
+/*
+ * 16-bit experts and the backward pass
+ *   The entry points from here to moe_route_prep_backward are not steps of the pages' method: they serve
+ *   expert banks that are not block-quantized, and training.  A step of the routed experts is, with W13
+ *   [E][2I][H] and W2 [E][H][I] in bf16 or fp16:
+ *     forward   c1 = moe_b16_grouped_gemm(x rows, W13);  h = moe_act_checkpoint(c1), which also saves c1 in
+ *               8 bits;  y = moe_b16_grouped_gemm(h, W2);  out = moe_topk_reduce(y)
+ *     backward  dy, dw = moe_topk_reduce_backward(dout, y);  dlogits = moe_route_prep_backward(dw);
+ *               dh = moe_b16_grouped_gemm(dy, W2, w_trans);  dc1, h = moe_gated_act_backward(dh, saved c1);
+ *               dW2 = moe_b16_grouped_wgrad(dy, h);  dW13 = moe_b16_grouped_wgrad(dc1, x rows, 16 bits or
+ *               saved in 8);  dx rows = moe_b16_grouped_gemm(dc1, W13, w_trans), then moe_topk_reduce with
+ *               unit weights sums each token's rows.
+ */
+
+/*
+ * moe_b16_grouped_gemm  -- the expert GEMMs with 16-bit operands, and their data gradient
+ *   out[r, n] = sum_k A[ar, k] * W(e, n, k), products and sums in fp32 (the MFMA's accumulator in grouped
+ *   mode), one rounding to out_dt.
+ *   a    [*][a_stride] of dt (MOE_BF16 or MOE_F16), K used
+ *   w    of dt.  w_trans = 0: element (e, n, k) at e*w_stride_e + n*w_stride_r + k (rows of K: the forward).
+ *        w_trans = 1: element (e, n, k) at e*w_stride_e + k*w_stride_r + n (rows of N): out = A W[e] of the
+ *        bank [E][K][N], i.e. the gradient of the input of a layer whose forward used it as [E][N'=K][K'=N].
+ *   out  [m_rows][out_stride] of out_dt (MOE_BF16, MOE_F16 or MOE_F32)
+ *   mode, expert_offsets, slot_ids, m_rows, a_row_div: as moe_bf8_grouped_gemm.  Grouped: rows
+ *        [expert_offsets[e], expert_offsets[e+1]) use expert e and A row r, offsets are clamped to [0, m_rows],
+ *        rows beyond the last are left untouched, any number of rows per expert (none included).  Slot:
+ *        w_trans = 0 only; a slot outside [0, n_experts) writes a +0 row and reads nothing of that row.
+ *   An infinity or NaN in a row of A or W reaches exactly the outputs whose sums hold it.
+ *   Requirements: N % 8 == 0, K % 8 == 0, 8 <= N, K <= 2^20, m_rows <= 2^31 - 1, 1 <= n_experts <= 1024 in
+ *   grouped mode (0 allowed in slot mode, with NULL a and w); a, w and their strides 16-byte aligned; out
+ *   aligned to its type (16-byte aligned rows are stored faster).  m_rows == 0 launches nothing.
+ */
+int moe_b16_grouped_gemm(const void* a, int64_t a_stride, const void* w, int64_t w_stride_e, int64_t w_stride_r,
+                         int64_t n_experts, int64_t N, int64_t K, int dt, int w_trans, int mode,
+                         const int32_t* expert_offsets, const int32_t* slot_ids, int64_t m_rows, int64_t a_row_div,
+                         void* out, int out_dt, int64_t out_stride, void* stream);
+
+/*
+ * moe_b16_grouped_wgrad  -- weight gradient of the grouped products
+ *   dw[e, n, k] = (accumulate ? dw[e, n, k] : 0) + sum_{r in rows of e} dY[r, n] * A[r, k], in fp32, rounded
+ *   once to dw_dt.  An expert without rows gets zeros (accumulate: keeps its gradient).
+ *   dy   [m_rows][dy_stride] of dt (MOE_BF16 or MOE_F16), N used
+ *   a    [m_rows][a_stride] of a_dt: dt, or MOE_E4M3 for rows saved in 8 bits: codes, and a_s
+ *        [m_rows][a_s_stride] fp32 scales (ceil(K/128) used).  A saved operand is round_dt(code * scale);
+ *        with moe_act_checkpoint's power-of-two scales that product is exact in bf16 (and in fp16 within its
+ *        range), with moe_act_quant's it is rounded once to dt.  a_s is ignored otherwise.
+ *   dw   element (e, n, k) at e*dw_stride_e + n*dw_stride_n + k, of dw_dt (MOE_BF16, MOE_F16 or MOE_F32)
+ *   expert_offsets as moe_b16_grouped_gemm; rows beyond the last are not read.
+ *   workspace: moe_b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K) bytes, 16-byte aligned, no
+ *   initialization; 0 bytes (NULL allowed) unless the gradient has few tiles and long row ranges, which are
+ *   then cut and their fp32 parts summed in order.  Scratch within one call: overlapping calls need their own.
+ *   Requirements: 1 <= n_experts <= 1024, N % 8 == 0, K % 8 == 0 (MOE_E4M3: K % 16 == 0), 8 <= N, K <= 2^20;
+ *   dy, a and their strides 16-byte aligned; dw aligned to its type.
+ *   m_rows == 0 still writes the zeros (dy and a may be NULL).
+ */
+size_t moe_b16_grouped_wgrad_workspace_size(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K);
+int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void* a, int64_t a_stride, int a_dt,
+                          const float* a_s, int64_t a_s_stride, const int32_t* expert_offsets, int64_t n_experts,
+                          int64_t N, int64_t K, int64_t m_rows, void* dw, int dw_dt, int64_t dw_stride_e,
+                          int64_t dw_stride_n, int accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_act_checkpoint  -- activations saved in 8 bits for the backward pass
+ *   Codes and scales laid out as moe_act_quant's, with power-of-two scales: per group of 128 columns
+ *     s = the smallest power of two with max|v| / s <= 448, at least 2^-126 (0 for a group of zeros)
+ *     q = e4m3_rne(v / s), the quotient exact; an infinity or NaN becomes the NaN code.
+ *   act = MOE_ACT_IDENTITY: rows of n columns; h must be NULL.
+ *   act = moe_act 1..5: in row is [gate(0:n) | up(n:2n)]; both halves are saved (codes at 0 and n, scales at
+ *   0 and ceil(n/128)), and h[r, c] = act(gate) * up in fp32 of the unrounded inputs, rounded to dt, is
+ *   written unless h is NULL.
+ *   in    [rows][in_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32);  h [rows][h_stride] of dt
+ *   out_q [rows][q_stride] bytes, out_s [rows][s_stride] fp32
+ *   Pointers aligned to their types; 16-byte aligned rows with n % 8 == 0 take the vector path.
+ */
+int moe_act_checkpoint(const void* in, int dt, int64_t in_stride, int64_t rows, int64_t n, int act, uint8_t* out_q,
+                       int64_t q_stride, float* out_s, int64_t s_stride, void* h, int64_t h_stride, void* stream);
+
+/*
+ * moe_gated_act_backward  -- backward of h = act(gate) * up from the saved gate and up
+ *   With g, u = code * scale of the two halves (moe_act_checkpoint's layout, any finite scales):
+ *     dx[r, c] = dh * u * act'(g),  dx[r, n + c] = dh * act(g),  h[r, c] = act(g) * u (unless h is NULL)
+ *   in fp32, rounded to dt.  ReLU's slope at 0 is 0.
+ *   dh [rows][dh_stride], dx [rows][dx_stride] (2n used), h [rows][h_stride], all of dt (MOE_BF16, MOE_F16 or
+ *   MOE_F32); act: moe_act 1..5.  Alignment as moe_act_checkpoint.  An infinity or NaN in dh stays in its dx.
+ */
+int moe_gated_act_backward(const void* dh, int dt, int64_t dh_stride, const uint8_t* q, int64_t q_stride,
+                           const float* s, int64_t s_stride, int64_t rows, int64_t n, int act, void* dx,
+                           int64_t dx_stride, void* h, int64_t h_stride, void* stream);
+
+/*
+ * moe_topk_reduce_backward  -- backward of moe_topk_reduce
+ *   For every route (t, j) with slot_ids[t, j] >= 0 and row(t, j) in [0, y_rows):
+ *     dy[row, 0:H] = weights[t, j] * dout[t, 0:H] (fp32, rounded to y_dt)
+ *     dweights[t, j] = sum_h dout[t, h] * y[row, h] (fp32, in a fixed order)
+ *   Any other route gets dweights = +0 and reads neither its weight nor y; its dy row is +0 when route_rows is
+ *   NULL (the row t*topk + j exists), and with route_rows it has no row.  Rows that no route names are left as
+ *   they were; active routes name distinct rows.
+ *   dout [T][dout_stride] bf16;  y [y_rows][y_stride] and dy [y_rows][dy_stride] of y_dt;  slot_ids, weights,
+ *   dweights [T][topk];  route_rows as moe_topk_reduce (DEVICE int32 [T*topk] or NULL).
+ *   dweights may be NULL (a router that is not trained); y is then not read and may be NULL.
+ *   topk <= 1024, T * topk < 2^31; pointers aligned to their types, 16-byte aligned rows with H % 8 == 0 are
+ *   faster.  T == 0 or topk == 0 launches nothing.
+ */
+int moe_topk_reduce_backward(const uint16_t* dout_bf16, int64_t dout_stride, const void* y, int y_dt, int64_t y_stride,
+                             int64_t y_rows, const int32_t* slot_ids, const int32_t* route_rows, const float* weights,
+                             int64_t T, int64_t topk, int64_t H, void* dy, int64_t dy_stride, float* dweights,
+                             void* stream);
+
+/*
+ * moe_route_prep_backward  -- gradient of the router logits from the routing weights'
+ *   dlogits[t, expert_ids[t, j]] = w_j * (dw_j - sum_i w_i dw_i), the softmax over the selected logits that
+ *   moe_route_prep's weights are; every other entry +0.  An id outside [0, E) is skipped (its weight still
+ *   counts in the sum); an id named twice gets the sum.
+ *   expert_ids, weights, dweights [T][topk];  dlogits [T][dlogits_stride] fp32, E written.
+ *   Requirements: 1 <= E <= 1024, 1 <= topk <= 64.  T == 0 launches nothing.
+ */
+int moe_route_prep_backward(const int32_t* expert_ids, const float* weights, const float* dweights, int64_t T,
+                            int64_t E, int64_t topk, float* dlogits, int64_t dlogits_stride, void* stream);
 
 #ifdef __cplusplus
 }

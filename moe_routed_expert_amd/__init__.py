@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_routed.so")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_ALIGN, MOE_ERR_HIP = 0, -1, -2, -3, -4, -5, -6
 MOE_ERR_SCRATCH = -7
-MOE_BF16, MOE_F32, MOE_F16 = 0, 1, 2
+MOE_BF16, MOE_F32, MOE_F16, MOE_E4M3 = 0, 1, 2, 3
 MOE_ACT_IDENTITY, MOE_ACT_SILU_MUL, MOE_ACT_GELU_MUL, MOE_ACT_RELU_MUL, MOE_ACT_SIGMOID_MUL, MOE_ACT_MUL = 0, 1, 2, 3, 4, 5
 MOE_MODE_GROUPED, MOE_MODE_SLOT = 0, 1
 MOE_W_PACKED = -1
@@ -33,7 +33,8 @@ EXPORTS = (
     "moe_fused_decode_workspace_layout", "moe_fused_decode_workspace_init", "moe_fused_decode",
     "moe_route_prep_workspace_size", "moe_route_prep", "moe_bf8_grouped_gemm_act_quant",
     "moe_mxfp4_grouped_gemm", "moe_mxfp4_grouped_gemm_act_quant", "moe_fused_decode_noalloc", "moe_pack_weights",
-    "moe_grouped_block_m",
+    "moe_grouped_block_m", "moe_b16_grouped_gemm", "moe_b16_grouped_wgrad", "moe_b16_grouped_wgrad_workspace_size",
+    "moe_act_checkpoint", "moe_gated_act_backward", "moe_topk_reduce_backward", "moe_route_prep_backward",
 )
 
 _lib = None
@@ -83,6 +84,15 @@ def lib():
             "moe_mxfp4_grouped_gemm_act_quant": ([P, I64, P, I64, P, I64, I64, P, I64, I64, I64, I64, I64, P,
                                                   I64, I32, I32, P, I64, P, I64, P], I32),
             "moe_pack_weights": ([P, I64, I64, I64, I64, I64, I64, P, I64, P], I32),
+            "moe_b16_grouped_gemm": ([P, I64, P, I64, I64, I64, I64, I64, I32, I32, I32, P, P, I64, I64, P, I32, I64,
+                                      P], I32),
+            "moe_b16_grouped_wgrad_workspace_size": ([I64, I64, I64, I64], SZ),
+            "moe_b16_grouped_wgrad": ([P, I64, I32, P, I64, I32, P, I64, P, I64, I64, I64, I64, P, I32, I64, I64, I32,
+                                       P, SZ, P], I32),
+            "moe_act_checkpoint": ([P, I32, I64, I64, I64, I32, P, I64, P, I64, P, I64, P], I32),
+            "moe_gated_act_backward": ([P, I32, I64, P, I64, P, I64, I64, I64, I32, P, I64, P, I64, P], I32),
+            "moe_topk_reduce_backward": ([P, I64, P, I32, I64, I64, P, P, P, I64, I64, I64, P, I64, P, P], I32),
+            "moe_route_prep_backward": ([P, P, P, I64, I64, I64, P, I64, P], I32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -314,3 +324,142 @@ def route_prep(logits, topk, stream=None):
         _ptr(logits), _rowstride(logits), T, E, topk, _ptr(ids) if T else None, _ptr(w) if T else None,
         _ptr(d2s) if T else None, _ptr(rr) if T else None, _ptr(offs), _ptr(ws), size, _stream(stream)))
     return ids, w, d2s, rr, offs
+
+
+# ---------------------------------------------------------------------------
+# 16-bit experts and the backward pass
+
+def _call(fn, tensors, args, stream):
+    """Calls C entry point fn(*args, stream) for tensors of one GPU, with that GPU current; stream None is its
+    current stream."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None:
+            assert t.device == dev and t.is_cuda, "tensors of one GPU expected"
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            s = stream if stream is not None else torch.cuda.current_stream(dev)
+            _check(fn, getattr(lib(), fn)(*args, s.cuda_stream))
+        return
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    _check(fn, getattr(lib(), fn)(*args, s.cuda_stream))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _i32(t, n, what):
+    assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n, "%s: %d contiguous int32 expected" % (what, n)
+
+
+def b16_grouped_gemm(a, w, out, *, mode, expert_offsets=None, slot_ids=None, m_rows=None, a_row_div=1,
+                     w_trans=False, stream=None):
+    """16-bit grouped GEMM: out[r] = a[r] @ w[e].T with w [E, N, K], or a[r] @ w[e] with w [E, K, N] when w_trans
+    (the data gradient of a layer whose forward used the same bank).  a [rows, K] and w bf16 or fp16, out
+    [rows, N] bf16, fp16 or fp32; rows by expert_offsets [E+1] (grouped) or slot_ids [m_rows] (slot mode)."""
+    E, K, N = w.shape if w_trans else (w.shape[0], w.shape[2], w.shape[1])
+    rows = out.shape[0] if m_rows is None else m_rows
+    assert a.dtype == w.dtype and a.shape[1] == K and out.shape[1] == N and w.stride(2) == 1, "operands do not match"
+    assert 0 <= rows <= out.shape[0], "m_rows exceeds out"
+    if mode == MOE_MODE_SLOT:
+        _i32(slot_ids, rows, "slot_ids")
+        assert a.shape[0] * a_row_div >= rows, "a has too few rows"
+    else:
+        _i32(expert_offsets, E + 1, "expert_offsets")
+        assert a.shape[0] >= rows, "a has too few rows"
+    _call("moe_b16_grouped_gemm", (a, w, out, expert_offsets, slot_ids), (
+        a.data_ptr(), _rowstride(a), w.data_ptr(), w.stride(0), w.stride(1), E, N, K, _dt(a), int(w_trans), mode,
+        _addr(expert_offsets), _addr(slot_ids), rows, a_row_div, out.data_ptr(), _dt(out), _rowstride(out)), stream)
+
+
+def b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K) -> int:
+    """Bytes of workspace b16_grouped_wgrad needs (0: none)."""
+    return lib().moe_b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K)
+
+
+def b16_grouped_wgrad(dy, a, expert_offsets, dw, *, a_s=None, m_rows=None, accumulate=False, workspace=None,
+                      stream=None):
+    """Weight gradient dw[e] = dy[rows of e].T @ a[rows of e] (+ dw[e] when accumulate).  dy [rows, N] bf16 or
+    fp16; a [rows, K] of dy's type, or uint8 e4m3 codes with scales a_s [rows, ceil(K/128)]; dw [E, N, K] bf16,
+    fp16 or fp32.  workspace: uint8 tensor of b16_grouped_wgrad_workspace_size bytes, allocated here when None."""
+    E, N, K = dw.shape
+    rows = dy.shape[0] if m_rows is None else m_rows
+    saved = a.dtype == torch.uint8
+    assert saved == (a_s is not None), "scales go with saved (uint8) rows"
+    assert dy.shape[1] == N and a.shape[1] == K and dw.stride(2) == 1, "operands do not match"
+    assert 0 <= rows <= min(dy.shape[0], a.shape[0]), "m_rows exceeds dy or a"
+    if saved:
+        assert a_s.dtype == torch.float32 and a_s.shape[0] >= rows and a_s.shape[1] >= (K + 127) // 128, "scales do not match"
+    _i32(expert_offsets, E + 1, "expert_offsets")
+    size = b16_grouped_wgrad_workspace_size(rows, E, N, K)
+    if size and workspace is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(dy.device)):
+            workspace = torch.empty(size, dtype=torch.uint8, device=dy.device)
+    if workspace is not None:
+        assert workspace.is_contiguous() and workspace.element_size() == 1, "workspace: contiguous bytes"
+    _call("moe_b16_grouped_wgrad", (dy, a, a_s, expert_offsets, dw, workspace), (
+        dy.data_ptr(), _rowstride(dy), _dt(dy), a.data_ptr(), _rowstride(a), MOE_E4M3 if saved else _dt(a), _addr(a_s),
+        _rowstride(a_s) if saved else 0, expert_offsets.data_ptr(), E, N, K, rows, dw.data_ptr(), _dt(dw), dw.stride(0),
+        dw.stride(1), int(accumulate), _addr(workspace), workspace.numel() if workspace is not None else 0), stream)
+
+
+def act_checkpoint(x, out_q, out_s, act=MOE_ACT_IDENTITY, h=None, stream=None):
+    """Saves rows x in 8 bits (e4m3 codes out_q, power-of-two scales out_s per 1x128 group).  With a gated act, x =
+    [gate | up]: both halves are saved and h = act(gate) * up (x's type) is written when given."""
+    rows, width = x.shape
+    n = width if act == MOE_ACT_IDENTITY else width // 2
+    both = 1 if act == MOE_ACT_IDENTITY else 2
+    assert width == both * n, "gate and up of one width expected"
+    assert out_q.dtype == torch.uint8 and out_s.dtype == torch.float32, "codes are uint8, scales float32"
+    assert tuple(out_q.shape) == (rows, width) and tuple(out_s.shape) == (rows, both * ((n + 127) // 128)), "outputs do not match"
+    assert h is None or (h.dtype == x.dtype and tuple(h.shape) == (rows, n)), "h does not match"
+    _call("moe_act_checkpoint", (x, out_q, out_s, h), (
+        x.data_ptr(), _dt(x), _rowstride(x), rows, n, act, out_q.data_ptr(), _rowstride(out_q), out_s.data_ptr(),
+        _rowstride(out_s), _addr(h), _rowstride(h) if h is not None else 0), stream)
+
+
+def gated_act_backward(dh, q, s, dx, act=MOE_ACT_SILU_MUL, h=None, stream=None):
+    """Backward of h = act(gate) * up from saved codes q [rows, 2n] and scales s: dx [rows, 2n] = [d gate | d up],
+    and h [rows, n] again when given.  dh, dx, h of one type."""
+    rows, n = dh.shape
+    assert q.dtype == torch.uint8 and s.dtype == torch.float32, "codes are uint8, scales float32"
+    assert tuple(q.shape) == (rows, 2 * n) and tuple(s.shape) == (rows, 2 * ((n + 127) // 128)), "saved rows do not match"
+    assert dx.dtype == dh.dtype and tuple(dx.shape) == (rows, 2 * n), "dx does not match"
+    assert h is None or (h.dtype == dh.dtype and tuple(h.shape) == (rows, n)), "h does not match"
+    _call("moe_gated_act_backward", (dh, q, s, dx, h), (
+        dh.data_ptr(), _dt(dh), _rowstride(dh), q.data_ptr(), _rowstride(q), s.data_ptr(), _rowstride(s), rows, n, act,
+        dx.data_ptr(), _rowstride(dx), _addr(h), _rowstride(h) if h is not None else 0), stream)
+
+
+def topk_reduce_backward(dout, y, slot_ids, weights, dy, dweights=None, route_rows=None, stream=None):
+    """Backward of topk_reduce: dy[row(t,j)] = weights[t,j] * dout[t], dweights[t,j] = <dout[t], y[row(t,j)]>.
+    dout [T, H] bf16; y (None when dweights is None) and dy [rows, H] of one type."""
+    T, topk = slot_ids.shape
+    rows, H = dy.shape
+    _i32(slot_ids, T * topk, "slot_ids")
+    assert dout.dtype == torch.bfloat16 and tuple(dout.shape) == (T, H), "dout: [T, H] bfloat16"
+    assert weights.dtype == torch.float32 and weights.is_contiguous() and weights.shape == slot_ids.shape, "weights do not match"
+    assert dweights is None or (dweights.dtype == torch.float32 and dweights.is_contiguous() and
+                                dweights.shape == slot_ids.shape), "dweights do not match"
+    assert y is None or (y.dtype == dy.dtype and y.shape == dy.shape), "y does not match dy"
+    if route_rows is not None:
+        _i32(route_rows, T * topk, "route_rows")
+    else:
+        assert rows >= T * topk, "a row for every route expected"
+    _call("moe_topk_reduce_backward", (dout, y if y is not None else dout, slot_ids, route_rows, weights, dy, dweights), (
+        dout.data_ptr(), _rowstride(dout), _addr(y), _dt(dy), _rowstride(y) if y is not None else 0, rows,
+        slot_ids.data_ptr(), _addr(route_rows), weights.data_ptr(), T, topk, H, dy.data_ptr(), _rowstride(dy),
+        _addr(dweights)), stream)
+
+
+def route_prep_backward(expert_ids, weights, dweights, dlogits, stream=None):
+    """Router gradient: dlogits [T, E] from route_prep's expert_ids and weights and the weights' gradient."""
+    T, topk = expert_ids.shape
+    _i32(expert_ids, T * topk, "expert_ids")
+    for t in (weights, dweights):
+        assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == expert_ids.shape, "weights do not match"
+    assert dlogits.dtype == torch.float32 and dlogits.shape[0] == T, "dlogits: [T, E] float32"
+    _call("moe_route_prep_backward", (expert_ids, weights, dweights, dlogits), (
+        expert_ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), T, dlogits.shape[1], topk, dlogits.data_ptr(),
+        _rowstride(dlogits)), stream)

@@ -1,0 +1,350 @@
+// Grouped products with 16-bit operands: the expert GEMMs of banks that are not block-quantized, and their
+// data gradient.  Rows are sorted by expert; out[r, n] = sum_k A[r, k] W[e(r)](n, k) with W held [N][K] (the
+// forward) or [K][N] (the data gradient, which reduces over the rows of the bank as the forward holds it).
+// Slot mode is the decode form: every row streams its own expert.
+//
+// MI355X design of the grouped mode (the tile engine is b16_tile.h).
+//  * Persistent workgroups of 8 waves (one per CU: a tile's LDS ring takes most of the CU's 160 KB).  Each
+//    reads the device offsets once into an LDS table of every expert's first M tile and walks its tiles; the
+//    load pipeline runs on across tiles, so a tile's first steps are in flight while the tile before it is
+//    multiplied and stored.
+//  * Tiles are numbered in panels of kPanel M tiles, M fastest, and tile t of round s goes to workgroup t % G
+//    with the workgroups of one XCD next to each other: the tiles that an XCD works on at one time form a
+//    patch whose A rows and weight columns meet in its L2.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "b16_tile.h"
+
+namespace moe {
+namespace b16 {
+
+
+struct GemmArgs {
+    const char* a;
+    int64_t a_stride;                 // bytes
+    const char* w;
+    int64_t w_stride_e, w_stride_r;   // bytes: expert, row of the bank
+    int n_experts;
+    int64_t N, K;
+    const int32_t* offsets;
+    int m_rows;
+    int n_tiles;                      // N tiles
+    void* out;
+    int out_dt;
+    int64_t out_stride;               // elements
+};
+
+template <class C, bool QT, bool F16>
+__global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(const GemmArgs g) {
+    using P = KMajor<C::BP, C::NW>;
+    using Q = std::conditional_t<QT, TMajor<C::BQ, C::NW>, KMajor<C::BQ, C::NW>>;
+    constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
+    __shared__ int first_tile[kMaxExperts + 1];       // M tiles before expert e; [n_experts] is the total
+    __shared__ int first_row[kMaxExperts + 1];        // rows of expert e: [first_row[e], first_row[e] + count)
+    __shared__ int wave_sum[C::NW];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int E = g.n_experts;
+
+    // the tile table: EPT consecutive experts per thread, a scan over the block
+    {
+        constexpr int EPT = kMaxExperts / C::THREADS;
+        int n[EPT], sum = 0;
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            n[i] = 0;
+            if (e < E) {
+                const int lo = min(max(g.offsets[e], 0), g.m_rows), hi = min(max(g.offsets[e + 1], lo), g.m_rows);
+                first_row[e] = lo;
+                if (e == E - 1) first_row[E] = hi;
+                n[i] = (hi - lo + C::BP - 1) / C::BP;
+            }
+            sum += n[i];
+        }
+        int x = sum;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int y = __shfl_up(x, d, kWave);
+            if (lane >= d) x += y;
+        }
+        if (lane == kWave - 1) wave_sum[wave] = x;
+        __syncthreads();
+        int before = x - sum;
+        for (int w = 0; w < wave; w++) before += wave_sum[w];
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            if (e < E) first_tile[e] = before;
+            before += n[i];
+            if (e == E - 1) first_tile[E] = before;
+        }
+        __syncthreads();
+    }
+    const int m_tiles = __builtin_amdgcn_readfirstlane(first_tile[E]);
+    const int tiles = m_tiles * g.n_tiles;
+    const int G = gridDim.x;
+    const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
+
+    struct Tile {
+        int expert, row0, rows, n0;
+    };
+    auto locate = [&](int t) {
+        const int per = kPanel * g.n_tiles;
+        const int panel = t / per, r = t - panel * per;
+        const int height = min(kPanel, m_tiles - panel * kPanel);
+        const int nt = r / height, mt = panel * kPanel + r - nt * height;
+        int lo = 0, hi = E - 1;                        // last expert whose first tile is <= mt
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (__builtin_amdgcn_readfirstlane(first_tile[mid]) <= mt) lo = mid;
+            else hi = mid - 1;
+        }
+        Tile ti;
+        ti.expert = lo;
+        const int skip = (mt - __builtin_amdgcn_readfirstlane(first_tile[lo])) * C::BP;
+        ti.row0 = __builtin_amdgcn_readfirstlane(first_row[lo]) + skip;
+        ti.rows = __builtin_amdgcn_readfirstlane(first_row[lo + 1]) - ti.row0;
+        ti.n0 = nt * C::BQ;
+        return ti;
+    };
+
+    const uint32_t lds = lds_offset(ring);
+    const int steps = (int)((g.K + kStep - 1) / kStep);
+
+    // producer: the ring stage, tile and step that are requested next
+    P p;
+    Q q;
+    int prod_t = start, prod_kt = 0, prod_stage = 0, issued = 0;
+    auto aim = [&]() {
+        if (prod_t >= tiles) return;
+        const Tile ti = locate(prod_t);
+        p.set(g.a + ti.row0 * g.a_stride, g.a_stride, ti.rows, wave, lane);
+        const char* w = g.w + ti.expert * g.w_stride_e;
+        const int valid = (int)min(g.N - ti.n0, (int64_t)C::BQ);
+        if constexpr (QT) q.set(w + (int64_t)ti.n0 * 2, g.w_stride_r, valid, wave, lane);
+        else q.set(w + ti.n0 * g.w_stride_r, g.w_stride_r, valid, wave, lane);
+    };
+    auto produce = [&]() {
+        if (prod_t >= tiles) return;
+        const uint32_t dst = lds + prod_stage * STAGE;
+        p.issue(dst, prod_kt, g.K, wave, lane);
+        q.issue(dst + P::BYTES, prod_kt, g.K, wave, lane);
+        issued++;
+        prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
+        if (++prod_kt == steps) {
+            prod_kt = 0;
+            prod_t += G;
+            aim();
+        }
+    };
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < S - 1; i++) produce();
+
+    typename P::Frag fp;
+    typename Q::Frag fq;
+    const int wp = wave / C::WQ, wq = wave % C::WQ;
+    fp.set(wp * C::MP, lane);
+    fq.set(wq * C::MQ, lane);
+
+    int stage = 0, consumed = 0, ready = 0;
+#pragma unroll 1
+    for (int t = start; t < tiles; t += G) {
+        v4f acc[C::MP][C::MQ];
+#pragma unroll
+        for (int m = 0; m < C::MP; m++)
+#pragma unroll
+            for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int kt = 0; kt < steps; kt++) {
+            // this step's stage: `ready` stages were already waited for at the end of the tile before; else
+            // wait until only the stages after it are in flight (all of them once the last are requested)
+            if (ready > 0) ready--;
+            else if (issued - consumed >= S - 1) wait_loads<(S - 2) * LPS>();
+            else wait_loads<0>();
+            block_barrier();
+            produce();                                 // into the stage that the step before this one read
+            const uint32_t at = lds + stage * STAGE;
+            step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
+            consumed++;
+            stage = stage + 1 == S ? 0 : stage + 1;
+        }
+        // Stores count as vector memory operations too: the stages in flight are waited for here, before the
+        // stores join them, so the next tile's first steps wait for no store.
+        wait_loads<0>();
+        ready = issued - consumed;
+        const Tile ti = locate(t);
+        const int rows = min(ti.rows, C::BP) - wp * C::MP * 16;
+        const int64_t c0 = ti.n0 + wq * C::MQ * 16;
+        const int cols = (int)min(g.N - c0, (int64_t)(C::MQ * 16));
+        if (rows > 0 && cols > 0) {
+            const int64_t o = (ti.row0 + wp * C::MP * 16) * g.out_stride + c0;
+            if (g.out_dt == MOE_F32) store_wave<kF32>((float*)g.out + o, g.out_stride, rows, cols, acc, lane);
+            else if (g.out_dt == MOE_BF16) store_wave<kBF16>((uint16_t*)g.out + o, g.out_stride, rows, cols, acc, lane);
+            else store_wave<kF16>((uint16_t*)g.out + o, g.out_stride, rows, cols, acc, lane);
+        }
+    }
+}
+
+template <class C, bool QT, bool F16>
+int resident_blocks() {
+    static std::atomic<int> cached[64];   // concurrent first calls may both fill it, with the same value
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+    int c = cached[dev].load(std::memory_order_relaxed);
+    if (c == 0) {
+        int per_cu = 0, cus = 0;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, b16_gemm_kernel<C, QT, F16>, C::THREADS, 0) != hipSuccess ||
+            hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            return 0;
+        c = per_cu * cus;
+        if (c > 0) cached[dev].store(c, std::memory_order_relaxed);
+    }
+    return c;
+}
+
+template <class C, bool QT, bool F16>
+int launch_cfg(hipStream_t st, GemmArgs g) {
+    const int64_t n_tiles = ceil_div(g.N, C::BQ);
+    const int64_t most = (g.m_rows / C::BP + std::min<int64_t>(g.n_experts, g.m_rows)) * n_tiles;
+    if (most > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
+    int wgs = resident_blocks<C, QT, F16>() / kXcds * kXcds;
+    if (wgs < kXcds) return MOE_ERR_HIP;
+    wgs = (int)std::min<int64_t>(wgs, ceil_div(most, kXcds) * kXcds);
+    g.n_tiles = (int)n_tiles;
+    hipLaunchKernelGGL((b16_gemm_kernel<C, QT, F16>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
+    return launch_status();
+}
+
+using Tile256 = Cfg<256, 256, 2, 4, 2, 1>;
+using Tile128 = Cfg<128, 256, 2, 4, 3, 1>;
+using Tile64 = Cfg<64, 256, 2, 4, 3, 1>;
+using Tile16 = Cfg<16, 256, 1, 8, 4, 1>;
+
+template <class C>
+int launch_form(hipStream_t st, bool trans, bool f16, const GemmArgs& g) {
+    if (trans) return f16 ? launch_cfg<C, true, true>(st, g) : launch_cfg<C, true, false>(st, g);
+    return f16 ? launch_cfg<C, false, true>(st, g) : launch_cfg<C, false, false>(st, g);
+}
+
+
+// The tile by rows per expert.
+int grouped_launch(hipStream_t st, bool trans, bool f16, const GemmArgs& g) {
+    const int64_t r = ceil_div(g.m_rows, g.n_experts);
+    if (r <= 16) return launch_form<Tile16>(st, trans, f16, g);
+    if (r <= 64) return launch_form<Tile64>(st, trans, f16, g);
+    if (r <= 256) return launch_form<Tile128>(st, trans, f16, g);
+    return launch_form<Tile256>(st, trans, f16, g);
+}
+
+// ------------------------------------------------------------------ slot mode
+// One wave holds kSlotCols columns of one row: its lanes take 8 consecutive k each (512 a pass), products and
+// sums in fp32, and the lanes' sums meet in six shuffles.  Bound by streaming the row's expert.
+constexpr int kSlotCols = 4;
+constexpr int kSlotWaves = 4;
+
+template <bool F16>
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint16_t lo = (uint16_t)(w[i] & 0xFFFFu), hi = (uint16_t)(w[i] >> 16);
+        x[2 * i] = F16 ? f16_to_f32(lo) : bf16_to_f32(lo);
+        x[2 * i + 1] = F16 ? f16_to_f32(hi) : bf16_to_f32(hi);
+    }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(64 * kSlotWaves)
+b16_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_row_div, int col_groups) {
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t r = blockIdx.x / (unsigned)col_groups;
+    const int64_t n0 = ((int64_t)(blockIdx.x % (unsigned)col_groups) * kSlotWaves + wave) * kSlotCols;
+    if (n0 >= g.N) return;
+    const int slot = slots[r];
+    float sum[kSlotCols];
+#pragma unroll
+    for (int c = 0; c < kSlotCols; c++) sum[c] = 0.0f;
+    if (slot >= 0 && slot < g.n_experts) {
+        const char* x = g.a + (r / a_row_div) * g.a_stride;
+        const char* w = g.w + slot * g.w_stride_e + n0 * g.w_stride_r;
+#pragma unroll 4
+        for (int64_t k = lane * 8; k < g.K; k += kWave * 8) {
+            float xv[8];
+            unpack8<F16>(*reinterpret_cast<const uint4*>(x + k * 2), xv);
+#pragma unroll
+            for (int c = 0; c < kSlotCols; c++) {
+                float wv[8];
+                unpack8<F16>(*reinterpret_cast<const uint4*>(w + c * g.w_stride_r + k * 2), wv);
+#pragma unroll
+                for (int i = 0; i < 8; i++) sum[c] = __builtin_fmaf(wv[i], xv[i], sum[c]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kSlotCols; c++)
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) sum[c] += __shfl_xor(sum[c], d, kWave);
+    }
+    if (lane < kSlotCols) {
+        float v = sum[0];
+#pragma unroll
+        for (int c = 1; c < kSlotCols; c++) v = lane == c ? sum[c] : v;
+        const int64_t o = r * g.out_stride + n0 + lane;
+        if (g.out_dt == MOE_F32) store_from_f32<kF32>(g.out, o, v);
+        else if (g.out_dt == MOE_BF16) store_from_f32<kBF16>(g.out, o, v);
+        else store_from_f32<kF16>(g.out, o, v);
+    }
+}
+
+int slot_launch(hipStream_t st, bool f16, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
+    const int64_t groups = ceil_div(g.N, kSlotCols * kSlotWaves);
+    if (groups * g.m_rows > 0x7FFFFFFF) return MOE_ERR_SHAPE;
+    const dim3 grid((unsigned)(groups * g.m_rows)), block(64 * kSlotWaves);
+    if (f16) hipLaunchKernelGGL((b16_slot_kernel<true>), grid, block, 0, st, g, slots, a_row_div, (int)groups);
+    else hipLaunchKernelGGL((b16_slot_kernel<false>), grid, block, 0, st, g, slots, a_row_div, (int)groups);
+    return launch_status();
+}
+
+}  // namespace b16
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_b16_grouped_gemm(const void* a, int64_t a_stride, const void* w, int64_t w_stride_e,
+                                    int64_t w_stride_r, int64_t n_experts, int64_t N, int64_t K, int dt, int w_trans,
+                                    int mode, const int32_t* expert_offsets, const int32_t* slot_ids, int64_t m_rows,
+                                    int64_t a_row_div, void* out, int out_dt, int64_t out_stride, void* stream) {
+    if (mode != MOE_MODE_GROUPED && mode != MOE_MODE_SLOT) return MOE_ERR_SHAPE;
+    if (w_trans != 0 && (w_trans != 1 || mode == MOE_MODE_SLOT)) return MOE_ERR_SHAPE;
+    if ((dt != MOE_BF16 && dt != MOE_F16) || !dtype_ok(out_dt)) return MOE_ERR_DTYPE;
+    if (m_rows < 0 || m_rows > 0x7FFFFFFF || n_experts < 0 || n_experts > 0x7FFFFFFF) return MOE_ERR_SHAPE;
+    if (N < 8 || N > b16::kMaxWidth || N % 8 || K < 8 || K > b16::kMaxWidth || K % 8) return MOE_ERR_SHAPE;
+    if (m_rows == 0) return MOE_OK;
+    if (!out) return MOE_ERR_NULL;
+    if (out_stride < N) return MOE_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(out) % (out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_ALIGN;
+    if (n_experts > 0) {
+        if (!a || !w) return MOE_ERR_NULL;
+        const int64_t rows = w_trans ? K : N, width = w_trans ? N : K;
+        if (a_stride < K || w_stride_r < width || (n_experts > 1 && w_stride_e / w_stride_r < rows)) return MOE_ERR_SHAPE;
+        if (!aligned16(a) || !aligned16(w) || a_stride % 8 || w_stride_r % 8 || w_stride_e % 8) return MOE_ERR_ALIGN;
+    }
+    b16::GemmArgs g{};
+    g.a = (const char*)a; g.a_stride = a_stride * 2;
+    g.w = (const char*)w; g.w_stride_e = w_stride_e * 2; g.w_stride_r = w_stride_r * 2;
+    g.n_experts = (int)n_experts; g.N = N; g.K = K; g.offsets = expert_offsets; g.m_rows = (int)m_rows;
+    g.out = out; g.out_dt = out_dt; g.out_stride = out_stride;
+    if (mode == MOE_MODE_SLOT) {
+        if (!slot_ids) return MOE_ERR_NULL;
+        if (a_row_div < 1) return MOE_ERR_SHAPE;
+        return b16::slot_launch(as_stream(stream), dt == MOE_F16, g, slot_ids, a_row_div);
+    }
+    if (n_experts < 1 || n_experts > b16::kMaxExperts) return MOE_ERR_SHAPE;
+    if (!expert_offsets) return MOE_ERR_NULL;
+    return b16::grouped_launch(as_stream(stream), w_trans == 1, dt == MOE_F16, g);
+}

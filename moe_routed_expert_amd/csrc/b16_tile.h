@@ -1,0 +1,260 @@
+// Tile engine of the 16-bit grouped products (b16_gemm.hip, b16_wgrad.hip): C[p, q] = sum_k P[p, k] Q[q, k]
+// on v_mfma_f32_16x16x32 with bf16 or fp16 operands and fp32 accumulators.
+//
+// A workgroup owns a BP x BQ tile of C and walks k in steps of 64.  Each step's operands go from global memory
+// straight into one stage of an LDS ring (global_load_lds_dwordx4: no registers, S - 1 steps in flight), and
+// the waves read MFMA fragments from there.  An operand lies in memory in one of two ways:
+//   KMajor  k is contiguous (P[p][k]): a stage holds T rows of 64 k, 128 bytes a row, and a fragment (8
+//           consecutive k of one row per lane) is one ds_read_b128;
+//   TMajor  the tile's own index is contiguous (P[k][p]): a stage holds 64 k rows of T elements, and a
+//           fragment is two ds_read_b64_tr_b16, each of which hands a group of 16 lanes 4 k of 16 columns
+//           transposed (lane i gets column i), so no operand is ever transposed in memory or in registers.
+// The DMA writes 64 consecutive 16-byte slots per wave instruction, so the bank swizzle is applied to the
+// address each lane reads: slot `pos` of a row holds 16-byte piece pos ^ f(row), with f chosen below so that
+// the lanes an LDS cycle serves fall into different banks.
+// A step's pieces past the end of k (the last step of a K that is no multiple of 64, or an expert's last rows
+// in the weight gradient) come from a 16-byte page of zeros, on both operands: a zero on one side alone would
+// not silence an infinity or NaN that follows in memory on the other.
+#pragma once
+
+#include "device.h"
+#include "host.h"
+
+namespace moe {
+namespace b16 {
+
+constexpr int kStep = 64;                     // k per ring stage
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+#define MOE_LDS __attribute__((address_space(3)))
+
+constexpr int kXcds = 8;
+constexpr int kMaxExperts = 1024;                   // experts of the tables in LDS
+constexpr int kPanel = 4;                           // tiles of a panel (the walks below)
+constexpr int64_t kMaxWidth = 1 << 20;              // widths: tile coordinates are held as int
+
+// BP x BQ tile, WP x WQ waves, S ring stages, WGS workgroups resident on a CU.
+template <int BP_, int BQ_, int WP_, int WQ_, int S_, int WGS_>
+struct Cfg {
+    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, S = S_;
+    static constexpr int NW = WP * WQ, THREADS = 64 * NW;
+    static constexpr int MP = BP / 16 / WP, MQ = BQ / 16 / WQ;
+    static constexpr int WAVES_PER_EU = NW * WGS_ / 4;
+};
+
+static __device__ const uint4 kZeroPiece = {0u, 0u, 0u, 0u};
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(const MOE_LDS char*)p;
+}
+
+// 64 lanes x 16 bytes from each lane's src to the LDS bytes [dst, dst + 1024) in lane order.  The instruction
+// writes no register, so nothing the compiler allocates can be overwritten by it; its completion is waited for
+// with wait_loads before the barrier that publishes the stage.  m0 holds the LDS address and nothing else in
+// these kernels uses it; the s_nop is the wait state between an m0 write and an LDS-direct load.
+__device__ __forceinline__ void dma16(const void* src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+}
+
+// Waits until at most N of this wave's vector memory operations are in flight (they retire in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A workgroup barrier that leaves vector memory operations in flight; LDS accesses before it are complete.
+__device__ __forceinline__ void block_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ v4f mfma16x16x32(v8s a, v8s b, v4f c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// T rows of an operand whose k is contiguous, staged by NW waves.  Row r's 16-byte piece c sits at slot
+// c ^ ((r >> 1) & 7): 16 consecutive rows of one piece cover 256 bytes, all 64 banks.
+template <int T, int NW>
+struct KMajor {
+    static constexpr int BYTES = T * kStep * 2;
+    static constexpr int GROUPS = T / 8;                                    // 8-row groups, one DMA each
+    static constexpr int LOADS = (GROUPS + NW - 1) / NW;                    // per wave and step
+    static_assert(GROUPS % NW == 0 || NW % GROUPS == 0, "waves cover the rows evenly");
+    const char* p[LOADS];
+    int k0;                                                                 // first k of this lane's pieces
+
+    // With fewer groups than waves the waves repeat each other's groups (the same bytes to the same place), so
+    // every wave has the same number of loads in flight.
+    __device__ __forceinline__ static int group(int j, int wave) { return GROUPS < NW ? wave % GROUPS : j * NW + wave; }
+
+    // Rows base + r * stride (bytes); rows from `valid` on repeat the last one (their results are dropped).
+    __device__ __forceinline__ void set(const void* base, int64_t stride, int valid, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) {
+            const int r = group(j, wave) * 8 + lane / 8;
+            const int c = (lane % 8) ^ ((r >> 1) & 7);                      // the same for every j
+            p[j] = (const char*)base + (int64_t)(r < valid ? r : valid - 1) * stride + c * 16;
+            k0 = c * 8;
+        }
+    }
+    // Step kt of a reduction over klen into the stage at LDS byte dst.
+    __device__ __forceinline__ void issue(uint32_t dst, int kt, int64_t klen, int wave, int lane) const {
+        const bool in = k0 < klen - (int64_t)kt * kStep;
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) {
+            const char* src = p[j] + (int64_t)kt * (kStep * 2);
+            dma16(in ? src : (const char*)&kZeroPiece, dst + group(j, wave) * 1024);
+        }
+    }
+
+    // This lane's fragment addresses in a stage: sub-tile m of 16 rows from row 16 * sub0, k half ks.
+    struct Frag {
+        uint32_t a0, a1;
+        __device__ __forceinline__ void set(int sub0, int lane) {
+            const int r = lane & 15;
+            a0 = (uint32_t)(sub0 * 2048 + r * 128 + (((lane >> 4) ^ (r >> 1)) << 4));
+            a1 = a0 ^ 64;
+        }
+        __device__ __forceinline__ v8s read(uint32_t stage, int m, int ks) const {
+            return *(const MOE_LDS v8s*)(uintptr_t)(stage + (ks ? a1 : a0) + m * 2048);
+        }
+    };
+};
+
+// 64 k rows of T elements of an operand whose own index is contiguous.  Row k's 32-byte column pair c sits at
+// c ^ g(k), g(k) = (k & 3) | ((k >> 3) & 1) << 2: the eight rows that two groups of 16 lanes read for one
+// sub-tile (8q .. 8q+3 and 8(q+1) .. 8(q+1)+3) fall into the eight 32-byte parts of 256 bytes.
+template <int T, int NW>
+struct TMajor {
+    static constexpr int BYTES = T * kStep * 2;
+    static constexpr int PIECES = T / 8;                                    // 16-byte pieces of a row
+    static constexpr int ROWS = 64 / PIECES;                                // rows of one DMA
+    static constexpr int LOADS = kStep / (ROWS * NW);
+    static_assert(T % 128 == 0 && LOADS * ROWS * NW == kStep, "whole swizzle groups");
+    const char* p[LOADS];
+    int64_t stride;
+
+    __device__ __forceinline__ static int row(int j, int wave, int lane) { return (j * NW + wave) * ROWS + lane / PIECES; }
+    __device__ __forceinline__ static int swizzle(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+
+    // k rows base + k * stride (bytes); column pieces from `valid` elements on repeat the last one.
+    __device__ __forceinline__ void set(const void* base, int64_t stride_bytes, int valid, int wave, int lane) {
+        stride = stride_bytes;
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) {
+            const int k = row(j, wave, lane);
+            const int c = (lane % PIECES) ^ (swizzle(k) << 1);
+            const int last = valid / 8 - 1;
+            p[j] = (const char*)base + k * stride + (c < last ? c : last) * 16;
+        }
+    }
+    __device__ __forceinline__ void issue(uint32_t dst, int kt, int64_t klen, int wave, int lane) const {
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) {
+            const bool in = row(j, wave, lane) < klen - (int64_t)kt * kStep;
+            const char* src = p[j] + (int64_t)kt * kStep * stride;
+            dma16(in ? src : (const char*)&kZeroPiece, dst + (j * NW + wave) * 1024);
+        }
+    }
+
+    struct Frag {
+        uint32_t a;
+        __device__ __forceinline__ void set(int sub0, int lane) {
+            const int q = lane >> 4, r = (lane >> 2) & 3;
+            const int g = r | ((q & 1) << 2);
+            a = (uint32_t)((8 * q + r) * (T * 2) + (sub0 >> 3) * 256 + (((sub0 & 7) ^ g) << 5) + (lane & 3) * 8);
+        }
+        __device__ __forceinline__ v8s read(uint32_t stage, int m, int ks) const {
+            const uint32_t at = stage + (a ^ ((m & 7) << 5)) + (m >> 3) * 256 + ks * (32 * T * 2);
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS v4s*)(uintptr_t)at);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS v4s*)(uintptr_t)(at + 4 * T * 2));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+};
+
+// One k step of a wave's MP x MQ sub-tiles of 16 x 16.  Q is the MFMA's row operand, so lane l holds of
+// sub-tile (m, n) the element p = 16m + l % 16, q = 16n + 4 (l / 16) + 0..3: four consecutive q.
+template <int MP, int MQ, bool F16, class FP, class FQ>
+__device__ __forceinline__ void step_mfma(v4f (&acc)[MP][MQ], const FP& fp, const FQ& fq, uint32_t p_stage,
+                                          uint32_t q_stage) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ks++) {
+        v8s q[MQ];
+#pragma unroll
+        for (int n = 0; n < MQ; n++) q[n] = fq.read(q_stage, n, ks);
+#pragma unroll
+        for (int m = 0; m < MP; m++) {
+            const v8s p = fp.read(p_stage, m, ks);
+#pragma unroll
+            for (int n = 0; n < MQ; n++) acc[m][n] = mfma16x16x32<F16>(q[n], p, acc[m][n]);
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if constexpr (DT == kBF16) return (uint32_t)f32_to_bf16(x) | ((uint32_t)f32_to_bf16(y) << 16);
+    else return (uint32_t)f32_to_f16(x) | ((uint32_t)f32_to_f16(y) << 16);
+}
+
+// A wave's sub-tiles to out[p][q] (row stride in elements; `out` at the wave's element (0, 0)), rows below
+// `rows`, columns below `cols` (a multiple of 8).  A 2-byte type's sub-tiles n and n + 1 leave together: a
+// permlane32 and a permlane16 swap of the packed words hand lane 16q + r the eight columns 8q .. 8q+7 of row
+// r, so a store writes 64 bytes of each of 16 rows.  The swaps run in every lane, outside the bounds.
+template <int DT, int MP, int MQ>
+__device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, int cols, const v4f (&acc)[MP][MQ],
+                                           int lane) {
+    const int esz = DT == kF32 ? 4 : 2;
+    const bool vec = stride % (16 / esz) == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    const int r0 = lane & 15, q4 = 4 * (lane >> 4);
+    if constexpr (DT != kF32 && MQ % 2 == 0) {
+        if (vec) {
+#pragma unroll
+            for (int m = 0; m < MP; m++) {
+                if (m * 16 >= rows) break;                                   // wave-uniform
+#pragma unroll
+                for (int n = 0; n < MQ; n += 2) {
+                    const v4f x = acc[m][n], y = acc[m][n + 1];
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(pack2<DT>(x[0], x[1]), pack2<DT>(y[0], y[1]), false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(pack2<DT>(x[2], x[3]), pack2<DT>(y[2], y[3]), false, false);
+                    const auto t0 = __builtin_amdgcn_permlane16_swap(s0[0], s0[1], false, false);
+                    const auto t1 = __builtin_amdgcn_permlane16_swap(s1[0], s1[1], false, false);
+                    const int r = m * 16 + r0, c = n * 16 + 2 * q4;
+                    if (r < rows && c < cols)
+                        *reinterpret_cast<uint4*>((uint16_t*)out + r * stride + c) = make_uint4(t0[0], t1[0], t0[1], t1[1]);
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MP; m++) {
+        const int r = m * 16 + r0;
+        if (r < rows) {
+#pragma unroll
+            for (int n = 0; n < MQ; n++) {
+                const int c = n * 16 + q4;
+                if (c < cols) {
+                    if (vec) {
+                        store4_from_f32<DT>(out, r * stride + c, acc[m][n]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) store_from_f32<DT>(out, r * stride + c + i, acc[m][n][i]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+}  // namespace b16
+}  // namespace moe

@@ -1,0 +1,408 @@
+// Weight gradient of the grouped products: dW[e][n][k] = sum over the rows r of expert e of dY[r][n] A[r][k].
+// Both operands lie with the reduction as their slow dimension, so both are read through the transposing LDS
+// loads of b16_tile.h and nothing is transposed in memory.  A may be the 8-bit checkpoint of a forward pass:
+// its e4m3 codes and 1 x 128 scales are read (half the bytes), and each 16-bit operand value
+// round(code * scale) is formed once per workgroup on its way into LDS.  With power-of-two scales
+// (moe_act_checkpoint) that product is exact in bf16 and no rounding is added.
+//
+// Persistent workgroups walk the tiles of every expert, expert by expert, so experts of unequal length are
+// shared by all of them; an expert without rows gets zeros.  Where the gradient has few tiles and many rows
+// (small matrices, long sequences), an expert's rows are cut into `splits` ranges whose fp32 partial
+// gradients go to a workspace and are summed in range order: no atomics, so results do not depend on timing.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "b16_tile.h"
+
+namespace moe {
+namespace b16 {
+
+constexpr int kMaxSplits = 16;
+
+struct WgradArgs {
+    const char* dy;
+    int64_t dy_stride;                // bytes
+    const char* a;
+    int64_t a_stride;                 // bytes
+    const float* a_s;                 // e4m3: scales
+    int64_t a_s_stride;
+    const int32_t* offsets;
+    int m_rows;
+    int n_experts;
+    int64_t N, K;
+    int n_tiles, k_tiles, splits;
+    char* out;                        // dW, or the fp32 partials when splits > 1
+    int out_dt;
+    int64_t stride_e, stride_n;       // elements
+    int accumulate;
+};
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2_op(float x, float y) {
+    if constexpr (F16) {
+        return (uint32_t)f32_to_f16(x) | ((uint32_t)f32_to_f16(y) << 16);
+    } else {
+        typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+        const v2bf b = {(__bf16)x, (__bf16)y};
+        return __builtin_bit_cast(uint32_t, b);
+    }
+}
+
+// 64 rows of T e4m3 columns with a scale per row and 128 columns, staged through registers into the layout of
+// TMajor: a thread's piece is 16 columns of one row (one scale), two 16-byte pieces of the stage.
+template <int T, int NW, bool F16>
+struct TSaved {
+    static constexpr int BYTES = T * kStep * 2;
+    static constexpr int PIECES = T / 16;
+    static constexpr int PER = T * kStep / 16 / (64 * NW);                  // pieces of a thread
+    static constexpr int LOADS = 0;                                         // none that wait_loads counts
+    static_assert(PER >= 1, "every thread has a piece");
+    const char* p[PER];
+    const float* s[PER];
+    int64_t stride, s_stride;
+    uint4 code[PER];
+    float scale[PER];
+
+    __device__ __forceinline__ static int row(int j, int tid) { return (j * 64 * NW + tid) / PIECES; }
+
+    __device__ __forceinline__ void set(const char* base, int64_t stride_bytes, const float* scales, int64_t scale_stride,
+                                        int valid, int col0, int tid) {
+        stride = stride_bytes;
+        s_stride = scale_stride;
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+            const int c = (j * 64 * NW + tid) % PIECES, last = valid / 16 - 1;
+            const int cc = c < last ? c : last;
+            p[j] = base + row(j, tid) * stride + cc * 16;
+            s[j] = scales + row(j, tid) * s_stride + (col0 + cc * 16) / 128;
+        }
+    }
+    // Requests step kt; rows past klen read as code 0, scale 0.
+    __device__ __forceinline__ void load(int kt, int64_t klen, int tid) {
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+            const bool in = row(j, tid) < klen - (int64_t)kt * kStep;
+            const char* src = p[j] + (int64_t)kt * kStep * stride;
+            const float* ss = s[j] + (int64_t)kt * kStep * s_stride;
+            code[j] = *reinterpret_cast<const uint4*>(in ? src : (const char*)&kZeroPiece);
+            scale[j] = *(in ? ss : (const float*)&kZeroPiece);
+        }
+    }
+    __device__ __forceinline__ void commit(uint32_t dst, int tid) const {
+#pragma unroll
+        for (int j = 0; j < PER; j++) {
+            const int k = row(j, tid), c = (j * 64 * NW + tid) % PIECES;
+            const uint32_t at = dst + k * (T * 2) + ((c ^ TMajor<T, NW>::swizzle(k)) << 5);
+            const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+                const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+                o[2 * i] = pack2_op<F16>(lo[0] * scale[j], lo[1] * scale[j]);
+                o[2 * i + 1] = pack2_op<F16>(hi[0] * scale[j], hi[1] * scale[j]);
+            }
+            *(MOE_LDS v4i*)(uintptr_t)at = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+            *(MOE_LDS v4i*)(uintptr_t)(at + 16) = v4i{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
+        }
+    }
+};
+
+// acc += the gradient that is there (accumulate), before store_wave writes the sum.
+template <int DT, int MP, int MQ>
+__device__ __forceinline__ void add_wave(const void* out, int64_t stride, int rows, int cols, v4f (&acc)[MP][MQ], int lane) {
+#pragma unroll
+    for (int m = 0; m < MP; m++) {
+        const int r = m * 16 + (lane & 15);
+#pragma unroll
+        for (int n = 0; n < MQ; n++) {
+            const int c = n * 16 + 4 * (lane >> 4);
+            if (r < rows && c < cols) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[m][n][i] += load_as_f32<DT>(out, r * stride + c + i);
+            }
+        }
+    }
+}
+
+template <class C, bool SAVED, bool F16>
+__global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(const WgradArgs g) {
+    using P = TMajor<C::BP, C::NW>;
+    using QD = TMajor<C::BQ, C::NW>;
+    using Q = std::conditional_t<SAVED, TSaved<C::BQ, C::NW, F16>, QD>;
+    constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
+    __shared__ int first_row[kMaxExperts + 1];         // device offsets, clamped to [0, m_rows]
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int per = g.n_tiles * g.k_tiles, per_expert = per * g.splits;
+    const int tiles = per_expert * g.n_experts;
+    const int G = gridDim.x;
+    const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
+
+    for (int e = tid; e <= g.n_experts; e += C::THREADS) first_row[e] = min(max(g.offsets[e], 0), g.m_rows);
+    __syncthreads();
+
+    struct Tile {
+        int expert, split, row0, rows, n0, k0;
+    };
+    auto locate = [&](int t) {
+        Tile ti;
+        ti.expert = t / per_expert;
+        t -= ti.expert * per_expert;
+        ti.split = t / per;
+        t -= ti.split * per;
+        const int panel = t / (kPanel * g.k_tiles);
+        t -= panel * kPanel * g.k_tiles;
+        const int height = min(kPanel, g.n_tiles - panel * kPanel);
+        const int kt = t / height;
+        ti.k0 = kt * C::BQ;
+        ti.n0 = (panel * kPanel + t - kt * height) * C::BP;
+        const int lo = __builtin_amdgcn_readfirstlane(first_row[ti.expert]);
+        const int hi = max(__builtin_amdgcn_readfirstlane(first_row[ti.expert + 1]), lo);
+        const int len = ((hi - lo + kStep - 1) / kStep + g.splits - 1) / g.splits * kStep;   // rows of a split
+        const int64_t from = lo + (int64_t)ti.split * len;
+        ti.row0 = (int)(from < hi ? from : hi);
+        ti.rows = (int)(from + len < hi ? from + len : hi) - ti.row0;
+        return ti;
+    };
+    // a range without rows still takes one step, of zeros, so that every tile is stored
+    auto steps_of = [&](const Tile& ti) { return max(1, (ti.rows + kStep - 1) / kStep); };
+
+    const uint32_t lds = lds_offset(ring);
+    P p;
+    Q q;
+    int prod_t = start, prod_kt = 0, prod_steps = 0, prod_rows = 0, prod_stage = 0, issued = 0;
+    bool pending = false;                              // SAVED: a step is in registers, not yet in LDS
+    uint32_t pending_dst = 0;
+    auto aim = [&]() {
+        if (prod_t >= tiles) return;
+        const Tile ti = locate(prod_t);
+        prod_steps = steps_of(ti);
+        prod_rows = ti.rows;
+        p.set(g.dy + ti.row0 * g.dy_stride + (int64_t)ti.n0 * 2, g.dy_stride, (int)min(g.N - ti.n0, (int64_t)C::BP), wave, lane);
+        const int valid = (int)min(g.K - ti.k0, (int64_t)C::BQ);
+        if constexpr (SAVED)
+            q.set(g.a + ti.row0 * g.a_stride + ti.k0, g.a_stride, g.a_s + ti.row0 * g.a_s_stride, g.a_s_stride, valid, ti.k0, tid);
+        else
+            q.set(g.a + ti.row0 * g.a_stride + (int64_t)ti.k0 * 2, g.a_stride, valid, wave, lane);
+    };
+    auto produce = [&]() {
+        if (prod_t >= tiles) return;
+        const uint32_t dst = lds + prod_stage * STAGE;
+        p.issue(dst, prod_kt, prod_rows, wave, lane);
+        if constexpr (SAVED) {
+            q.load(prod_kt, prod_rows, tid);
+            pending = true;
+            pending_dst = dst + P::BYTES;
+        } else {
+            q.issue(dst + P::BYTES, prod_kt, prod_rows, wave, lane);
+        }
+        issued++;
+        prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
+        if (++prod_kt == prod_steps) {
+            prod_kt = 0;
+            prod_t += G;
+            aim();
+        }
+    };
+    auto commit = [&]() {
+        if constexpr (SAVED) {
+            if (pending) q.commit(pending_dst, tid);
+            pending = false;
+        }
+    };
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < S - 1; i++) {
+        produce();
+        commit();
+    }
+
+    typename P::Frag fp;
+    typename QD::Frag fq;
+    const int wp = wave / C::WQ, wq = wave % C::WQ;
+    fp.set(wp * C::MP, lane);
+    fq.set(wq * C::MQ, lane);
+
+    int stage = 0, consumed = 0, ready = 0;
+#pragma unroll 1
+    for (int t = start; t < tiles; t += G) {
+        const Tile ti = locate(t);
+        const int steps = steps_of(ti);
+        v4f acc[C::MP][C::MQ];
+#pragma unroll
+        for (int m = 0; m < C::MP; m++)
+#pragma unroll
+            for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int kt = 0; kt < steps; kt++) {
+            if (ready > 0) ready--;
+            else if (issued - consumed >= S - 1) wait_loads<(S - 2) * LPS>();
+            else wait_loads<0>();
+            block_barrier();
+            produce();
+            const uint32_t at = lds + stage * STAGE;
+            step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
+            commit();
+            consumed++;
+            stage = stage + 1 == S ? 0 : stage + 1;
+        }
+        wait_loads<0>();
+        ready = issued - consumed;
+        const int rows = (int)min(g.N - ti.n0, (int64_t)C::BP) - wp * C::MP * 16;
+        const int64_t c0 = ti.k0 + wq * C::MQ * 16;
+        const int cols = (int)min(g.K - c0, (int64_t)(C::MQ * 16));
+        if (rows > 0 && cols > 0) {
+            const int64_t o = ((int64_t)ti.split * g.n_experts + ti.expert) * g.stride_e + (int64_t)(ti.n0 + wp * C::MP * 16) * g.stride_n + c0;
+            if (g.out_dt == MOE_F32) {
+                if (g.accumulate) add_wave<kF32>((float*)g.out + o, g.stride_n, rows, cols, acc, lane);
+                store_wave<kF32>((float*)g.out + o, g.stride_n, rows, cols, acc, lane);
+            } else if (g.out_dt == MOE_BF16) {
+                if (g.accumulate) add_wave<kBF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
+                store_wave<kBF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
+            } else {
+                if (g.accumulate) add_wave<kF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
+                store_wave<kF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
+            }
+        }
+    }
+}
+
+// The partial gradients of `splits` row ranges, [split][e][n][k] in fp32, summed in range order (onto what is
+// there, when accumulating) and rounded once.  Four consecutive k a thread.
+template <int DT>
+__global__ void __launch_bounds__(256)
+wgrad_join_kernel(const float* __restrict__ part, int splits, int64_t E, int64_t N, int64_t K, void* __restrict__ out,
+                  int64_t stride_e, int64_t stride_n, int accumulate) {
+    const int64_t total = E * N * K / 4;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t k4 = K / 4, row = i / k4;
+    const int64_t k = (i - row * k4) * 4, e = row / N, n = row - e * N;
+    v4f sum = *reinterpret_cast<const v4f*>(part + i * 4);
+    for (int s = 1; s < splits; s++) sum += *reinterpret_cast<const v4f*>(part + s * E * N * K + i * 4);
+    const int64_t o = e * stride_e + n * stride_n + k;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        float v = sum[j];
+        if (accumulate) v += load_as_f32<DT>(out, o + j);
+        store_from_f32<DT>(out, o + j, v);
+    }
+}
+
+template <class C, bool SAVED, bool F16>
+int wgrad_resident() {
+    static std::atomic<int> cached[64];   // concurrent first calls may both fill it, with the same value
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+    int c = cached[dev].load(std::memory_order_relaxed);
+    if (c == 0) {
+        int per_cu = 0, cus = 0;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, b16_wgrad_kernel<C, SAVED, F16>, C::THREADS, 0) != hipSuccess ||
+            hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            return 0;
+        c = per_cu * cus;
+        if (c > 0) cached[dev].store(c, std::memory_order_relaxed);
+    }
+    return c;
+}
+
+template <class C, bool SAVED, bool F16>
+int wgrad_launch_cfg(hipStream_t st, WgradArgs g) {
+    const int64_t nt = ceil_div(g.N, C::BP), kt = ceil_div(g.K, C::BQ);
+    const int64_t tiles = nt * kt * g.n_experts * g.splits;
+    if (nt * kt > 0x7FFFFFFF / 64 || tiles > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
+    g.n_tiles = (int)nt;
+    g.k_tiles = (int)kt;
+    int wgs = wgrad_resident<C, SAVED, F16>() / kXcds * kXcds;
+    if (wgs < kXcds) return MOE_ERR_HIP;
+    wgs = (int)std::min<int64_t>(wgs, ceil_div(tiles, kXcds) * kXcds);
+    hipLaunchKernelGGL((b16_wgrad_kernel<C, SAVED, F16>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
+    return launch_status();
+}
+
+using Tile256 = Cfg<256, 256, 2, 4, 2, 1>;
+using Tile128 = Cfg<128, 128, 2, 2, 2, 2>;
+
+template <class C>
+int wgrad_launch(hipStream_t st, bool saved, bool f16, const WgradArgs& g) {
+    if (saved) return f16 ? wgrad_launch_cfg<C, true, true>(st, g) : wgrad_launch_cfg<C, true, false>(st, g);
+    return f16 ? wgrad_launch_cfg<C, false, true>(st, g) : wgrad_launch_cfg<C, false, false>(st, g);
+}
+
+bool wgrad_shape_ok(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
+    return m_rows >= 0 && m_rows <= 0x7FFFFFFF && E >= 1 && E <= kMaxExperts && N >= 8 && N <= kMaxWidth && N % 8 == 0 &&
+           K >= 8 && K <= kMaxWidth && K % 8 == 0;
+}
+
+// The large tile needs enough tiles for the device's 256 CUs.
+bool wgrad_large(int64_t E, int64_t N, int64_t K) { return ceil_div(N, 256) * ceil_div(K, 256) * E >= 512; }
+
+// Row ranges per expert: enough for two workgroups a CU, none shorter than 256 rows on average.
+int wgrad_splits(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
+    if (wgrad_large(E, N, K)) return 1;
+    const int64_t tiles = ceil_div(N, 128) * ceil_div(K, 128) * E;
+    const int64_t want = std::min<int64_t>({512 / tiles, m_rows / E / 256, kMaxSplits});
+    return want < 2 ? 1 : (int)want;
+}
+
+}  // namespace b16
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_b16_grouped_wgrad_workspace_size(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
+    if (!b16::wgrad_shape_ok(m_rows, n_experts, N, K)) return 0;
+    const int s = b16::wgrad_splits(m_rows, n_experts, N, K);
+    return s > 1 ? (size_t)s * n_experts * N * K * 4 : 0;
+}
+
+extern "C" int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void* a, int64_t a_stride,
+                                     int a_dt, const float* a_s, int64_t a_s_stride, const int32_t* expert_offsets,
+                                     int64_t n_experts, int64_t N, int64_t K, int64_t m_rows, void* dw, int dw_dt,
+                                     int64_t dw_stride_e, int64_t dw_stride_n, int accumulate, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+    if ((dt != MOE_BF16 && dt != MOE_F16) || !dtype_ok(dw_dt)) return MOE_ERR_DTYPE;
+    const bool saved = a_dt == MOE_E4M3;
+    if (!saved && a_dt != dt) return MOE_ERR_DTYPE;
+    if (!b16::wgrad_shape_ok(m_rows, n_experts, N, K) || (saved && K % 16)) return MOE_ERR_SHAPE;
+    if (accumulate != 0 && accumulate != 1) return MOE_ERR_SHAPE;
+    if (!dw || !expert_offsets) return MOE_ERR_NULL;
+    if (dw_stride_n < K || (n_experts > 1 && dw_stride_e / dw_stride_n < N)) return MOE_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(dw) % (dw_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_ALIGN;
+    if (m_rows > 0) {
+        if (!dy || !a || (saved && !a_s)) return MOE_ERR_NULL;
+        if (dy_stride < N || a_stride < K || (saved && a_s_stride < ceil_div(K, 128))) return MOE_ERR_SHAPE;
+        if (!aligned16(dy) || !aligned16(a) || dy_stride % 8 || a_stride % (saved ? 16 : 8)) return MOE_ERR_ALIGN;
+    }
+    b16::WgradArgs g{};
+    g.dy = (const char*)dy; g.dy_stride = dy_stride * 2;
+    g.a = (const char*)a; g.a_stride = saved ? a_stride : a_stride * 2;
+    g.a_s = a_s; g.a_s_stride = a_s_stride;
+    g.offsets = expert_offsets; g.m_rows = (int)m_rows; g.n_experts = (int)n_experts; g.N = N; g.K = K;
+    g.splits = b16::wgrad_splits(m_rows, n_experts, N, K);
+    g.out = (char*)dw; g.out_dt = dw_dt; g.stride_e = dw_stride_e; g.stride_n = dw_stride_n;
+    g.accumulate = accumulate;
+    auto st = as_stream(stream);
+    if (g.splits > 1) {
+        if (!workspace) return MOE_ERR_NULL;
+        if (ws_bytes < (size_t)g.splits * n_experts * N * K * 4) return MOE_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return MOE_ERR_ALIGN;
+        g.out = (char*)workspace; g.out_dt = MOE_F32; g.stride_e = N * K; g.stride_n = K; g.accumulate = 0;
+    }
+    const int rc = b16::wgrad_large(n_experts, N, K) ? b16::wgrad_launch<b16::Tile256>(st, saved, dt == MOE_F16, g)
+                                                     : b16::wgrad_launch<b16::Tile128>(st, saved, dt == MOE_F16, g);
+    if (rc != MOE_OK || g.splits == 1) return rc;
+    const dim3 grid((unsigned)ceil_div(n_experts * N * K / 4, 256)), block(256);
+    const float* part = (const float*)workspace;
+    if (dw_dt == MOE_F32)
+        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF32>), grid, block, 0, st, part, g.splits, n_experts, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+    else if (dw_dt == MOE_BF16)
+        hipLaunchKernelGGL((b16::wgrad_join_kernel<kBF16>), grid, block, 0, st, part, g.splits, n_experts, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+    else
+        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF16>), grid, block, 0, st, part, g.splits, n_experts, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+    return launch_status();
+}
