@@ -116,33 +116,43 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     const uint32_t lds = lds_offset(ring);
     const int steps = (int)((g.K + kStep - 1) / kStep);
 
-    // producer: the ring stage, tile and step that are requested next
+    // Producer: the ring stage, tile and step that are requested next.  Past the last tile it goes on with zeros
+    // (prod_k = 0) into stages that nobody reads, so the loads in flight can be counted the same way to the end.
     P p;
     Q q;
-    int prod_t = start, prod_kt = 0, prod_stage = 0, issued = 0;
+    int prod_t = start, prod_kt = 0, prod_stage = 0;
+    int64_t prod_k = 0;
     auto aim = [&]() {
+        prod_k = prod_t < tiles ? g.K : 0;
         if (prod_t >= tiles) return;
         const Tile ti = locate(prod_t);
-        p.set(g.a + ti.row0 * g.a_stride, g.a_stride, ti.rows, wave, lane);
+        const int l = fresh(lane);
+        p.set(g.a + ti.row0 * g.a_stride, g.a_stride, ti.rows, wave, l);
         const char* w = g.w + ti.expert * g.w_stride_e;
         const int valid = (int)min(g.N - ti.n0, (int64_t)C::BQ);
-        if constexpr (QT) q.set(w + (int64_t)ti.n0 * 2, g.w_stride_r, valid, wave, lane);
-        else q.set(w + ti.n0 * g.w_stride_r, g.w_stride_r, valid, wave, lane);
+        if constexpr (QT) q.set(w + (int64_t)ti.n0 * 2, g.w_stride_r, valid, wave, l);
+        else q.set(w + ti.n0 * g.w_stride_r, g.w_stride_r, valid, wave, l);
     };
-    auto produce = [&]() {
-        if (prod_t >= tiles) return;
+    auto part = [&](int j) {
         const uint32_t dst = lds + prod_stage * STAGE;
-        p.issue(dst, prod_kt, g.K, wave, lane);
-        q.issue(dst + P::BYTES, prod_kt, g.K, wave, lane);
-        issued++;
-        prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
-        if (++prod_kt == steps) {
-            prod_kt = 0;
-            prod_t += G;
-            aim();
+        if (j < P::LOADS) p.issue(j, dst, prod_kt, prod_k, wave, lane);
+        else q.issue(j - P::LOADS, dst + P::BYTES, prod_kt, prod_k, wave, lane);
+        if (j == LPS - 1) {
+            prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
+            if (++prod_kt == steps) {
+                prod_kt = 0;
+                prod_t += G;
+                aim();
+            }
         }
     };
+    auto produce = [&]() {
+#pragma unroll
+        for (int j = 0; j < LPS; j++) part(j);
+    };
+    if (start >= tiles) return;
     aim();
+    constexpr bool PIPED = C::MP >= 4;                 // a wave's MFMAs are worth the software pipeline
 #pragma unroll 1
     for (int i = 0; i < S - 1; i++) produce();
 
@@ -152,7 +162,23 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     fp.set(wp * C::MP, lane);
     fq.set(wq * C::MQ, lane);
 
-    int stage = 0, consumed = 0, ready = 0;
+    // The next stage has landed for every wave: `ready` stages were waited for already, else all but the S - 2
+    // stages after it have to be in.
+    int stage = 0, ready = 0;
+    auto arrive = [&]() {
+        if (ready > 0) ready--;
+        else wait_loads<(S - 2) * LPS>();
+        block_barrier();
+    };
+    Frags<C::MP, C::MQ> f;
+    if constexpr (PIPED) {
+        wait_loads<0>();
+        ready = S - 2;
+        block_barrier();
+        f.first(fp, fq, lds, lds + P::BYTES);
+#pragma unroll
+        for (int j = 0; j < parts_after_meet<C::MP, LPS>(); j++) part(j);
+    }
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
         v4f acc[C::MP][C::MQ];
@@ -162,33 +188,31 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int kt = 0; kt < steps; kt++) {
-            // this step's stage: `ready` stages were already waited for at the end of the tile before; else
-            // wait until only the stages after it are in flight (all of them once the last are requested)
-            if (ready > 0) ready--;
-            else if (issued - consumed >= S - 1) wait_loads<(S - 2) * LPS>();
-            else wait_loads<0>();
-            block_barrier();
-            produce();                                 // into the stage that the step before this one read
             const uint32_t at = lds + stage * STAGE;
-            step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
-            consumed++;
             stage = stage + 1 == S ? 0 : stage + 1;
+            if constexpr (PIPED) {
+                const uint32_t next = lds + stage * STAGE;
+                step_pipelined<C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
+            } else {
+                arrive();
+                produce();                             // into the stage that the step before this one read
+                step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
+            }
         }
         // Stores count as vector memory operations too: the stages in flight are waited for here, before the
         // stores join them, so the next tile's first steps wait for no store.
-        wait_loads<0>();
-        ready = issued - consumed;
+        if constexpr (!PIPED || S > 2) {
+            wait_loads<0>();
+            ready = PIPED ? S - 2 : S - 1;
+        }
         const Tile ti = locate(t);
         const int rows = min(ti.rows, C::BP) - wp * C::MP * 16;
         const int64_t c0 = ti.n0 + wq * C::MQ * 16;
         const int cols = (int)min(g.N - c0, (int64_t)(C::MQ * 16));
-        if (rows > 0 && cols > 0) {
-            const int64_t o = (ti.row0 + wp * C::MP * 16) * g.out_stride + c0;
-            if (g.out_dt == MOE_F32) store_wave<kF32>((float*)g.out + o, g.out_stride, rows, cols, acc, lane);
-            else if (g.out_dt == MOE_BF16) store_wave<kBF16>((uint16_t*)g.out + o, g.out_stride, rows, cols, acc, lane);
-            else store_wave<kF16>((uint16_t*)g.out + o, g.out_stride, rows, cols, acc, lane);
-        }
+        if (rows > 0 && cols > 0)
+            store_wave_dt(g.out, g.out_dt, false, (ti.row0 + wp * C::MP * 16) * g.out_stride + c0, g.out_stride, rows, cols, acc, fresh(lane));
     }
+    wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
 template <class C, bool QT, bool F16>

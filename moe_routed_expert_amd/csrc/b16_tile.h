@@ -72,6 +72,13 @@ __device__ __forceinline__ void block_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// A copy of v that the compiler takes for a new value: what is computed from it (a tile's addresses) is not
+// hoisted out of the tile loop, where it would hold registers through the k loop.
+__device__ __forceinline__ int fresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 template <bool F16>
 __device__ __forceinline__ v4f mfma16x16x32(v8s a, v8s b, v4f c) {
     if constexpr (F16)
@@ -105,14 +112,11 @@ struct KMajor {
             k0 = c * 8;
         }
     }
-    // Step kt of a reduction over klen into the stage at LDS byte dst.
-    __device__ __forceinline__ void issue(uint32_t dst, int kt, int64_t klen, int wave, int lane) const {
+    // Load j of step kt of a reduction over klen, into the stage at LDS byte dst.
+    __device__ __forceinline__ void issue(int j, uint32_t dst, int kt, int64_t klen, int wave, int lane) const {
         const bool in = k0 < klen - (int64_t)kt * kStep;
-#pragma unroll
-        for (int j = 0; j < LOADS; j++) {
-            const char* src = p[j] + (int64_t)kt * (kStep * 2);
-            dma16(in ? src : (const char*)&kZeroPiece, dst + group(j, wave) * 1024);
-        }
+        const char* src = p[j] + (int64_t)kt * (kStep * 2);
+        dma16(in ? src : (const char*)&kZeroPiece, dst + group(j, wave) * 1024);
     }
 
     // This lane's fragment addresses in a stage: sub-tile m of 16 rows from row 16 * sub0, k half ks.
@@ -156,13 +160,10 @@ struct TMajor {
             p[j] = (const char*)base + k * stride + (c < last ? c : last) * 16;
         }
     }
-    __device__ __forceinline__ void issue(uint32_t dst, int kt, int64_t klen, int wave, int lane) const {
-#pragma unroll
-        for (int j = 0; j < LOADS; j++) {
-            const bool in = row(j, wave, lane) < klen - (int64_t)kt * kStep;
-            const char* src = p[j] + (int64_t)kt * kStep * stride;
-            dma16(in ? src : (const char*)&kZeroPiece, dst + (j * NW + wave) * 1024);
-        }
+    __device__ __forceinline__ void issue(int j, uint32_t dst, int kt, int64_t klen, int wave, int lane) const {
+        const bool in = row(j, wave, lane) < klen - (int64_t)kt * kStep;
+        const char* src = p[j] + (int64_t)kt * kStep * stride;
+        dma16(in ? src : (const char*)&kZeroPiece, dst + (j * NW + wave) * 1024);
     }
 
     struct Frag {
@@ -200,6 +201,72 @@ __device__ __forceinline__ void step_mfma(v4f (&acc)[MP][MQ], const FP& fp, cons
     }
 }
 
+// The same step as a software pipeline, for tiles whose MFMAs are the bound.  Its 2 MP groups of MQ MFMAs take
+// their P fragments from a ring that is read kAhead groups ahead.  When the last fragments of this stage are in
+// registers the workgroup meets (`meet`: the next stage has landed for every wave, and this one is free), and the
+// groups that are left cover the first reads of the next stage, so no MFMA waits for LDS at a stage's start.  The
+// parts of the stage that `meet` begins to request (`part(j)`, one DMA each) are spread over the groups that
+// follow, into the next step: requested at once they fill the CU's address queue and the waves stall on it.
+constexpr int kAhead = 3;
+
+// Parts of PARTS that a pipelined step of 2 MP groups requests after its meeting; the next step requests the rest.
+template <int MP, int PARTS>
+constexpr int parts_after_meet() {
+    const int n = kAhead * ((PARTS + 2 * MP - 1) / (2 * MP));
+    return n < PARTS ? n : PARTS;
+}
+
+template <int MP, int MQ>
+struct Frags {
+    v8s p[kAhead + 1];
+    v8s q[2][MQ];
+    template <class FP, class FQ>
+    __device__ __forceinline__ void first(const FP& fp, const FQ& fq, uint32_t p_stage, uint32_t q_stage) {
+#pragma unroll
+        for (int n = 0; n < MQ; n++) q[0][n] = fq.read(q_stage, n, 0);
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) p[i] = fp.read(p_stage, i % MP, i / MP);
+    }
+};
+
+template <int MP, int MQ, bool F16, int PARTS, class FP, class FQ, class Meet, class Part>
+__device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>& f, const FP& fp, const FQ& fq,
+                                               uint32_t p_stage, uint32_t q_stage, uint32_t p_next, uint32_t q_next,
+                                               const Meet& meet, const Part& part) {
+    constexpr int G = 2 * MP, MEET = G - kAhead;
+    static_assert(MP >= 4 && G % (kAhead + 1) == 0, "the ring's phase is the same in every step");
+    constexpr int PER = (PARTS + G - 1) / G;              // parts a group
+#pragma unroll
+    for (int i = 0; i < G; i++) {
+        if (i == MEET) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            meet();
+        }
+        // the part whose turn it is, counted in groups since the meeting
+#pragma unroll
+        for (int u = 0; u < PER; u++) {
+            const int j = ((i - MEET + G) % G) * PER + u;
+            if (j < PARTS) part(j);
+        }
+        // this stage's fragments kAhead groups ahead, the second half's Q in time for group MP
+        const int r = i + kAhead;
+        if (i < MEET) {
+            const int n = i - (MP - 1 - MQ > 0 ? MP - 1 - MQ : 0);
+            if (n >= 0 && n < MQ) f.q[1][n] = fq.read(q_stage, n, 1);
+            f.p[r % (kAhead + 1)] = fp.read(p_stage, r % MP, r / MP);
+        } else {                                          // the next stage's first
+#pragma unroll
+            for (int n = (i - MEET) * 2; n < MQ && n < (i - MEET) * 2 + 2; n++) f.q[0][n] = fq.read(q_next, n, 0);
+            f.p[r % (kAhead + 1)] = fp.read(p_next, r - G, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < MQ; n++)
+            acc[i % MP][n] = mfma16x16x32<F16>(f.q[i / MP][n], f.p[i % (kAhead + 1)], acc[i % MP][n]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     if constexpr (DT == kBF16) return (uint32_t)f32_to_bf16(x) | ((uint32_t)f32_to_bf16(y) << 16);
@@ -207,20 +274,24 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 
 // A wave's sub-tiles to out[p][q] (row stride in elements; `out` at the wave's element (0, 0)), rows below
-// `rows`, columns below `cols` (a multiple of 8).  A 2-byte type's sub-tiles n and n + 1 leave together: a
-// permlane32 and a permlane16 swap of the packed words hand lane 16q + r the eight columns 8q .. 8q+7 of row
-// r, so a store writes 64 bytes of each of 16 rows.  The swaps run in every lane, outside the bounds.
-template <int DT, int MP, int MQ>
+// `rows`, columns below `cols` (a multiple of 8); ADD: onto what is there, in fp32 before the rounding.  A 2-byte
+// type's sub-tiles n and n + 1 leave together: a permlane32 and a permlane16 swap of the packed words hand lane
+// 16q + r the eight columns 8q .. 8q+7 of row r, so a store writes 64 bytes of each of 16 rows.  The swaps run in
+// every lane, outside the bounds.
+template <int DT, bool ADD, int MP, int MQ>
 __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, int cols, const v4f (&acc)[MP][MQ],
                                            int lane) {
-    const int esz = DT == kF32 ? 4 : 2;
-    const bool vec = stride % (16 / esz) == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    constexpr int ESZ = DT == kF32 ? 4 : 2;
+    const bool vec = stride % (16 / ESZ) == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
     const int r0 = lane & 15, q4 = 4 * (lane >> 4);
-    if constexpr (DT != kF32 && MQ % 2 == 0) {
-        if (vec) {
+    char* row = (char*)out + r0 * (stride * ESZ);
 #pragma unroll
-            for (int m = 0; m < MP; m++) {
-                if (m * 16 >= rows) break;                                   // wave-uniform
+    for (int m = 0; m < MP; m++) {
+        if (m * 16 >= rows) break;                                           // wave-uniform
+        asm volatile("" ::: "memory");         // row by row: the accumulators leave few registers for addresses
+        const bool in = m * 16 + r0 < rows;
+        if constexpr (DT != kF32 && MQ % 2 == 0 && !ADD) {
+            if (vec) {
 #pragma unroll
                 for (int n = 0; n < MQ; n += 2) {
                     const v4f x = acc[m][n], y = acc[m][n + 1];
@@ -228,32 +299,42 @@ __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, 
                     const auto s1 = __builtin_amdgcn_permlane32_swap(pack2<DT>(x[2], x[3]), pack2<DT>(y[2], y[3]), false, false);
                     const auto t0 = __builtin_amdgcn_permlane16_swap(s0[0], s0[1], false, false);
                     const auto t1 = __builtin_amdgcn_permlane16_swap(s1[0], s1[1], false, false);
-                    const int r = m * 16 + r0, c = n * 16 + 2 * q4;
-                    if (r < rows && c < cols)
-                        *reinterpret_cast<uint4*>((uint16_t*)out + r * stride + c) = make_uint4(t0[0], t1[0], t0[1], t1[1]);
+                    const int c = n * 16 + 2 * q4;
+                    if (in && c < cols) *reinterpret_cast<uint4*>(row + c * 2) = make_uint4(t0[0], t1[0], t0[1], t1[1]);
                 }
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < MP; m++) {
-        const int r = m * 16 + r0;
-        if (r < rows) {
-#pragma unroll
-            for (int n = 0; n < MQ; n++) {
-                const int c = n * 16 + q4;
-                if (c < cols) {
-                    if (vec) {
-                        store4_from_f32<DT>(out, r * stride + c, acc[m][n]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) store_from_f32<DT>(out, r * stride + c + i, acc[m][n][i]);
-                    }
-                }
+                row += 16 * stride * ESZ;
+                continue;
             }
         }
+#pragma unroll
+        for (int n = 0; n < MQ; n++) {
+            const int c = n * 16 + q4;
+            if (in && c < cols) {
+                v4f v = acc[m][n];
+                if constexpr (ADD) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) v[i] += load_as_f32<DT>(row, c + i);
+                }
+                if (vec) {
+                    store4_from_f32<DT>(row, c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) store_from_f32<DT>(row, c + i, v[i]);
+                }
+            }
+        }
+        row += 16 * stride * ESZ;
     }
+}
+
+// The same for a run-time type; `at` is the wave's first element of out, in elements.
+template <int MP, int MQ>
+__device__ __forceinline__ void store_wave_dt(void* out, int out_dt, bool add, int64_t at, int64_t stride, int rows, int cols,
+                                              const v4f (&acc)[MP][MQ], int lane) {
+    char* p = (char*)out + at * (out_dt == MOE_F32 ? 4 : 2);
+    if (out_dt == MOE_F32) add ? store_wave<kF32, true>(p, stride, rows, cols, acc, lane) : store_wave<kF32, false>(p, stride, rows, cols, acc, lane);
+    else if (out_dt == MOE_BF16) add ? store_wave<kBF16, true>(p, stride, rows, cols, acc, lane) : store_wave<kBF16, false>(p, stride, rows, cols, acc, lane);
+    else add ? store_wave<kF16, true>(p, stride, rows, cols, acc, lane) : store_wave<kF16, false>(p, stride, rows, cols, acc, lane);
 }
 
 }  // namespace b16

@@ -109,23 +109,6 @@ struct TSaved {
     }
 };
 
-// acc += the gradient that is there (accumulate), before store_wave writes the sum.
-template <int DT, int MP, int MQ>
-__device__ __forceinline__ void add_wave(const void* out, int64_t stride, int rows, int cols, v4f (&acc)[MP][MQ], int lane) {
-#pragma unroll
-    for (int m = 0; m < MP; m++) {
-        const int r = m * 16 + (lane & 15);
-#pragma unroll
-        for (int n = 0; n < MQ; n++) {
-            const int c = n * 16 + 4 * (lane >> 4);
-            if (r < rows && c < cols) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) acc[m][n][i] += load_as_f32<DT>(out, r * stride + c + i);
-            }
-        }
-    }
-}
-
 template <class C, bool SAVED, bool F16>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(const WgradArgs g) {
     using P = TMajor<C::BP, C::NW>;
@@ -171,54 +154,54 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     // a range without rows still takes one step, of zeros, so that every tile is stored
     auto steps_of = [&](const Tile& ti) { return max(1, (ti.rows + kStep - 1) / kStep); };
 
+    // Producer, as in b16_gemm_kernel: past the last tile it goes on with zeros (prod_rows = 0).
     const uint32_t lds = lds_offset(ring);
     P p;
     Q q;
-    int prod_t = start, prod_kt = 0, prod_steps = 0, prod_rows = 0, prod_stage = 0, issued = 0;
-    bool pending = false;                              // SAVED: a step is in registers, not yet in LDS
-    uint32_t pending_dst = 0;
+    int prod_t = start, prod_kt = 0, prod_steps = 1, prod_rows = 0, prod_stage = 0;
+    uint32_t saved_dst = 0;                            // SAVED: where the step that is in registers goes
     auto aim = [&]() {
+        prod_rows = 0;
         if (prod_t >= tiles) return;
         const Tile ti = locate(prod_t);
         prod_steps = steps_of(ti);
         prod_rows = ti.rows;
-        p.set(g.dy + ti.row0 * g.dy_stride + (int64_t)ti.n0 * 2, g.dy_stride, (int)min(g.N - ti.n0, (int64_t)C::BP), wave, lane);
+        const int l = fresh(lane);
+        p.set(g.dy + ti.row0 * g.dy_stride + (int64_t)ti.n0 * 2, g.dy_stride, (int)min(g.N - ti.n0, (int64_t)C::BP), wave, l);
         const int valid = (int)min(g.K - ti.k0, (int64_t)C::BQ);
         if constexpr (SAVED)
-            q.set(g.a + ti.row0 * g.a_stride + ti.k0, g.a_stride, g.a_s + ti.row0 * g.a_s_stride, g.a_s_stride, valid, ti.k0, tid);
+            q.set(g.a + ti.row0 * g.a_stride + ti.k0, g.a_stride, g.a_s + ti.row0 * g.a_s_stride, g.a_s_stride, valid, ti.k0, wave * kWave + l);
         else
-            q.set(g.a + ti.row0 * g.a_stride + (int64_t)ti.k0 * 2, g.a_stride, valid, wave, lane);
+            q.set(g.a + ti.row0 * g.a_stride + (int64_t)ti.k0 * 2, g.a_stride, valid, wave, l);
+    };
+    auto part = [&](int j) {
+        const uint32_t dst = lds + prod_stage * STAGE;
+        if (j < P::LOADS) p.issue(j, dst, prod_kt, prod_rows, wave, lane);
+        else if constexpr (!SAVED) q.issue(j - P::LOADS, dst + P::BYTES, prod_kt, prod_rows, wave, lane);
+        if (j == LPS - 1) {
+            if constexpr (SAVED) {
+                q.load(prod_kt, prod_rows, tid);
+                saved_dst = dst + P::BYTES;
+            }
+            prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
+            if (++prod_kt == prod_steps) {
+                prod_kt = 0;
+                prod_t += G;
+                aim();
+            }
+        }
     };
     auto produce = [&]() {
-        if (prod_t >= tiles) return;
-        const uint32_t dst = lds + prod_stage * STAGE;
-        p.issue(dst, prod_kt, prod_rows, wave, lane);
-        if constexpr (SAVED) {
-            q.load(prod_kt, prod_rows, tid);
-            pending = true;
-            pending_dst = dst + P::BYTES;
-        } else {
-            q.issue(dst + P::BYTES, prod_kt, prod_rows, wave, lane);
-        }
-        issued++;
-        prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
-        if (++prod_kt == prod_steps) {
-            prod_kt = 0;
-            prod_t += G;
-            aim();
-        }
+#pragma unroll
+        for (int j = 0; j < LPS; j++) part(j);
     };
-    auto commit = [&]() {
-        if constexpr (SAVED) {
-            if (pending) q.commit(pending_dst, tid);
-            pending = false;
-        }
-    };
+    if (start >= tiles) return;
     aim();
+    constexpr bool PIPED = C::MP >= 4 && !SAVED;
 #pragma unroll 1
     for (int i = 0; i < S - 1; i++) {
         produce();
-        commit();
+        if constexpr (SAVED) q.commit(saved_dst, tid);
     }
 
     typename P::Frag fp;
@@ -227,7 +210,21 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     fp.set(wp * C::MP, lane);
     fq.set(wq * C::MQ, lane);
 
-    int stage = 0, consumed = 0, ready = 0;
+    int stage = 0, ready = 0;
+    auto arrive = [&]() {
+        if (ready > 0) ready--;
+        else wait_loads<(S - 2) * LPS>();
+        block_barrier();
+    };
+    Frags<C::MP, C::MQ> f;
+    if constexpr (PIPED) {
+        wait_loads<0>();
+        ready = S - 2;
+        block_barrier();
+        f.first(fp, fq, lds, lds + P::BYTES);
+#pragma unroll
+        for (int j = 0; j < parts_after_meet<C::MP, LPS>(); j++) part(j);
+    }
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
         const Tile ti = locate(t);
@@ -239,36 +236,31 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int kt = 0; kt < steps; kt++) {
-            if (ready > 0) ready--;
-            else if (issued - consumed >= S - 1) wait_loads<(S - 2) * LPS>();
-            else wait_loads<0>();
-            block_barrier();
-            produce();
             const uint32_t at = lds + stage * STAGE;
-            step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
-            commit();
-            consumed++;
             stage = stage + 1 == S ? 0 : stage + 1;
+            if constexpr (PIPED) {
+                const uint32_t next = lds + stage * STAGE;
+                step_pipelined<C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
+            } else {
+                arrive();
+                produce();
+                step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
+                if constexpr (SAVED) q.commit(saved_dst, tid);
+            }
         }
-        wait_loads<0>();
-        ready = issued - consumed;
+        if constexpr (!PIPED || S > 2) {               // before the stores join the loads in flight
+            wait_loads<0>();
+            ready = PIPED ? S - 2 : S - 1;
+        }
         const int rows = (int)min(g.N - ti.n0, (int64_t)C::BP) - wp * C::MP * 16;
         const int64_t c0 = ti.k0 + wq * C::MQ * 16;
         const int cols = (int)min(g.K - c0, (int64_t)(C::MQ * 16));
         if (rows > 0 && cols > 0) {
             const int64_t o = ((int64_t)ti.split * g.n_experts + ti.expert) * g.stride_e + (int64_t)(ti.n0 + wp * C::MP * 16) * g.stride_n + c0;
-            if (g.out_dt == MOE_F32) {
-                if (g.accumulate) add_wave<kF32>((float*)g.out + o, g.stride_n, rows, cols, acc, lane);
-                store_wave<kF32>((float*)g.out + o, g.stride_n, rows, cols, acc, lane);
-            } else if (g.out_dt == MOE_BF16) {
-                if (g.accumulate) add_wave<kBF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
-                store_wave<kBF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
-            } else {
-                if (g.accumulate) add_wave<kF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
-                store_wave<kF16>((uint16_t*)g.out + o, g.stride_n, rows, cols, acc, lane);
-            }
+            store_wave_dt(g.out, g.out_dt, g.accumulate != 0, o, g.stride_n, rows, cols, acc, fresh(lane));
         }
     }
+    wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
 // The partial gradients of `splits` row ranges, [split][e][n][k] in fp32, summed in range order (onto what is
