@@ -206,7 +206,9 @@ __device__ __forceinline__ void step_mfma(v4f (&acc)[MP][MQ], const FP& fp, cons
 // registers the workgroup meets (`meet`: the next stage has landed for every wave, and this one is free), and the
 // groups that are left cover the first reads of the next stage, so no MFMA waits for LDS at a stage's start.  The
 // parts of the stage that `meet` begins to request (`part(j)`, one DMA each) are spread over the groups that
-// follow, into the next step: requested at once they fill the CU's address queue and the waves stall on it.
+// follow, into the next step: requested at once they fill the CU's address queue and the waves stall on it (dense
+// products ran 5 % slower).  REST: the parts left over from the step before are requested here; a tile's first step
+// has none, since they went out before the stores of the tile before it (see Arrival).
 constexpr int kAhead = 3;
 
 // Parts of PARTS that a pipelined step of 2 MP groups requests after its meeting; the next step requests the rest.
@@ -215,6 +217,34 @@ constexpr int parts_after_meet() {
     const int n = kAhead * ((PARTS + 2 * MP - 1) / (2 * MP));
     return n < PARTS ? n : PARTS;
 }
+
+// The wait and the barrier that make the next stage readable: all but the S - 2 stages after it (LPS loads each) have
+// to be in.  Vector memory operations retire in order and stores are among them, so the first S - 1 waits after a
+// tile's stores, all for stages that were requested before them, let that many more operations stay in flight;
+// otherwise a tile's first steps would wait for its predecessor's stores to reach memory.  Only stores that the
+// wave is sure to have issued may be counted: one for each 16-row sub-tile row and 32 (16-bit) or 16 (fp32)
+// columns that hold an element, which is what `stored` gets; the count is rounded down to a level of E.
+template <int S, int LPS, int E>
+struct Arrival {
+    int grace = 0, level = 0;
+    __device__ __forceinline__ void stored(int count) {
+        grace = S - 1;
+        level = count >= 2 * E ? 3 : count >= E ? 2 : count >= E / 2 ? 1 : 0;
+    }
+    __device__ __forceinline__ void operator()() {
+        constexpr int N = (S - 2) * LPS;
+        static_assert(N + 2 * E < 64, "vmcnt counts to 63");
+        if (grace > 0 && level > 0) {
+            grace--;
+            if (level == 3) wait_loads<N + 2 * E>();
+            else if (level == 2) wait_loads<N + E>();
+            else wait_loads<N + E / 2>();
+        } else {
+            wait_loads<N>();
+        }
+        block_barrier();
+    }
+};
 
 template <int MP, int MQ>
 struct Frags {
@@ -229,10 +259,10 @@ struct Frags {
     }
 };
 
-template <int MP, int MQ, bool F16, int PARTS, class FP, class FQ, class Meet, class Part>
+template <bool REST, int MP, int MQ, bool F16, int PARTS, class FP, class FQ, class Meet, class Part>
 __device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>& f, const FP& fp, const FQ& fq,
                                                uint32_t p_stage, uint32_t q_stage, uint32_t p_next, uint32_t q_next,
-                                               const Meet& meet, const Part& part) {
+                                               Meet& meet, const Part& part) {
     constexpr int G = 2 * MP, MEET = G - kAhead;
     static_assert(MP >= 4 && G % (kAhead + 1) == 0, "the ring's phase is the same in every step");
     constexpr int PER = (PARTS + G - 1) / G;              // parts a group
@@ -246,7 +276,7 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>
 #pragma unroll
         for (int u = 0; u < PER; u++) {
             const int j = ((i - MEET + G) % G) * PER + u;
-            if (j < PARTS) part(j);
+            if (j < PARTS && (i >= MEET || REST)) part(j);
         }
         // this stage's fragments kAhead groups ahead, the second half's Q in time for group MP
         const int r = i + kAhead;
@@ -265,12 +295,6 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>
             acc[i % MP][n] = mfma16x16x32<F16>(f.q[i / MP][n], f.p[i % (kAhead + 1)], acc[i % MP][n]);
         __builtin_amdgcn_sched_barrier(0);
     }
-}
-
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-    if constexpr (DT == kBF16) return (uint32_t)f32_to_bf16(x) | ((uint32_t)f32_to_bf16(y) << 16);
-    else return (uint32_t)f32_to_f16(x) | ((uint32_t)f32_to_f16(y) << 16);
 }
 
 // A wave's sub-tiles to out[p][q] (row stride in elements; `out` at the wave's element (0, 0)), rows below
@@ -295,8 +319,8 @@ __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, 
 #pragma unroll
                 for (int n = 0; n < MQ; n += 2) {
                     const v4f x = acc[m][n], y = acc[m][n + 1];
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(pack2<DT>(x[0], x[1]), pack2<DT>(y[0], y[1]), false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(pack2<DT>(x[2], x[3]), pack2<DT>(y[2], y[3]), false, false);
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(pk16<DT>(x[0], x[1]), pk16<DT>(y[0], y[1]), false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(pk16<DT>(x[2], x[3]), pk16<DT>(y[2], y[3]), false, false);
                     const auto t0 = __builtin_amdgcn_permlane16_swap(s0[0], s0[1], false, false);
                     const auto t1 = __builtin_amdgcn_permlane16_swap(s1[0], s1[1], false, false);
                     const int c = n * 16 + 2 * q4;
@@ -316,7 +340,8 @@ __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, 
                     for (int i = 0; i < 4; i++) v[i] += load_as_f32<DT>(row, c + i);
                 }
                 if (vec) {
-                    store4_from_f32<DT>(row, c, v);
+                    if constexpr (DT == kF32) *reinterpret_cast<v4f*>(row + c * 4) = v;
+                    else *reinterpret_cast<uint2*>(row + c * 2) = make_uint2(pk16<DT>(v[0], v[1]), pk16<DT>(v[2], v[3]));
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; i++) store_from_f32<DT>(row, c + i, v[i]);
@@ -327,14 +352,17 @@ __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, 
     }
 }
 
-// The same for a run-time type; `at` is the wave's first element of out, in elements.
+// The same for a run-time type; `at` is the wave's first element of out, in elements.  Returns the store
+// instructions that the wave has issued at least (Arrival::stored).
 template <int MP, int MQ>
-__device__ __forceinline__ void store_wave_dt(void* out, int out_dt, bool add, int64_t at, int64_t stride, int rows, int cols,
+__device__ __forceinline__ int store_wave_dt(void* out, int out_dt, bool add, int64_t at, int64_t stride, int rows, int cols,
                                               const v4f (&acc)[MP][MQ], int lane) {
     char* p = (char*)out + at * (out_dt == MOE_F32 ? 4 : 2);
     if (out_dt == MOE_F32) add ? store_wave<kF32, true>(p, stride, rows, cols, acc, lane) : store_wave<kF32, false>(p, stride, rows, cols, acc, lane);
     else if (out_dt == MOE_BF16) add ? store_wave<kBF16, true>(p, stride, rows, cols, acc, lane) : store_wave<kBF16, false>(p, stride, rows, cols, acc, lane);
     else add ? store_wave<kF16, true>(p, stride, rows, cols, acc, lane) : store_wave<kF16, false>(p, stride, rows, cols, acc, lane);
+    const int width = out_dt == MOE_F32 || MQ == 1 ? 16 : 32;
+    return (min(rows, MP * 16) + 15) / 16 * ((cols + width - 1) / width);
 }
 
 }  // namespace b16

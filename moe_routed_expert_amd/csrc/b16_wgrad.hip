@@ -38,17 +38,6 @@ struct WgradArgs {
     int accumulate;
 };
 
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2_op(float x, float y) {
-    if constexpr (F16) {
-        return (uint32_t)f32_to_f16(x) | ((uint32_t)f32_to_f16(y) << 16);
-    } else {
-        typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-        const v2bf b = {(__bf16)x, (__bf16)y};
-        return __builtin_bit_cast(uint32_t, b);
-    }
-}
-
 // 64 rows of T e4m3 columns with a scale per row and 128 columns, staged through registers into the layout of
 // TMajor: a thread's piece is 16 columns of one row (one scale), two 16-byte pieces of the stage.
 template <int T, int NW, bool F16>
@@ -100,8 +89,8 @@ struct TSaved {
             for (int i = 0; i < 4; i++) {
                 const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
                 const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-                o[2 * i] = pack2_op<F16>(lo[0] * scale[j], lo[1] * scale[j]);
-                o[2 * i + 1] = pack2_op<F16>(hi[0] * scale[j], hi[1] * scale[j]);
+                o[2 * i] = pk16<F16 ? kF16 : kBF16>(lo[0] * scale[j], lo[1] * scale[j]);
+                o[2 * i + 1] = pk16<F16 ? kF16 : kBF16>(hi[0] * scale[j], hi[1] * scale[j]);
             }
             *(MOE_LDS v4i*)(uintptr_t)at = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
             *(MOE_LDS v4i*)(uintptr_t)(at + 16) = v4i{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
@@ -210,20 +199,15 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     fp.set(wp * C::MP, lane);
     fq.set(wq * C::MQ, lane);
 
-    int stage = 0, ready = 0;
-    auto arrive = [&]() {
-        if (ready > 0) ready--;
-        else wait_loads<(S - 2) * LPS>();
-        block_barrier();
-    };
+    int stage = 0;
+    constexpr int AFTER = parts_after_meet<C::MP, LPS>();
+    Arrival<S, LPS, C::MP * C::MQ / 2> arrive;
     Frags<C::MP, C::MQ> f;
     if constexpr (PIPED) {
-        wait_loads<0>();
-        ready = S - 2;
-        block_barrier();
+        arrive();
         f.first(fp, fq, lds, lds + P::BYTES);
 #pragma unroll
-        for (int j = 0; j < parts_after_meet<C::MP, LPS>(); j++) part(j);
+        for (int j = 0; j < LPS; j++) part(j);
     }
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
@@ -234,31 +218,44 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
         for (int m = 0; m < C::MP; m++)
 #pragma unroll
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-        for (int kt = 0; kt < steps; kt++) {
-            const uint32_t at = lds + stage * STAGE;
+        if constexpr (PIPED) {
+            // (one body after the other: as two branches of a loop they would keep two sets of accumulators)
+            uint32_t at = lds + stage * STAGE;
             stage = stage + 1 == S ? 0 : stage + 1;
-            if constexpr (PIPED) {
-                const uint32_t next = lds + stage * STAGE;
-                step_pipelined<C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
-            } else {
+            uint32_t next = lds + stage * STAGE;
+            step_pipelined<false, C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
+#pragma unroll 1
+            for (int kt = 1; kt < steps; kt++) {
+                at = next;
+                stage = stage + 1 == S ? 0 : stage + 1;
+                next = lds + stage * STAGE;
+                step_pipelined<true, C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
+            }
+        } else {
+#pragma unroll 1
+            for (int kt = 0; kt < steps; kt++) {
+                const uint32_t at = lds + stage * STAGE;
+                stage = stage + 1 == S ? 0 : stage + 1;
                 arrive();
-                produce();
+                produce();                             // into the stage that the step before this one read
                 step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
                 if constexpr (SAVED) q.commit(saved_dst, tid);
             }
         }
-        if constexpr (!PIPED || S > 2) {               // before the stores join the loads in flight
-            wait_loads<0>();
-            ready = PIPED ? S - 2 : S - 1;
+        // the rest of the stage that is being requested goes out before the stores (see Arrival)
+        if constexpr (PIPED) {
+#pragma unroll
+            for (int j = AFTER; j < LPS; j++) part(j);
         }
         const int rows = (int)min(g.N - ti.n0, (int64_t)C::BP) - wp * C::MP * 16;
         const int64_t c0 = ti.k0 + wq * C::MQ * 16;
         const int cols = (int)min(g.K - c0, (int64_t)(C::MQ * 16));
+        int stores = 0;
         if (rows > 0 && cols > 0) {
             const int64_t o = ((int64_t)ti.split * g.n_experts + ti.expert) * g.stride_e + (int64_t)(ti.n0 + wp * C::MP * 16) * g.stride_n + c0;
-            store_wave_dt(g.out, g.out_dt, g.accumulate != 0, o, g.stride_n, rows, cols, acc, fresh(lane));
+            stores = store_wave_dt(g.out, g.out_dt, g.accumulate != 0, o, g.stride_n, rows, cols, acc, fresh(lane));
         }
+        arrive.stored(stores);
     }
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }

@@ -39,8 +39,7 @@ __device__ __forceinline__ void store_cols(void* __restrict__ base, int64_t off,
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            w[i] = DT == kBF16 ? (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16)
-                               : (uint32_t)f32_to_f16(v[2 * i]) | ((uint32_t)f32_to_f16(v[2 * i + 1]) << 16);
+            w[i] = pk16<DT>(v[2 * i], v[2 * i + 1]);
         *reinterpret_cast<uint4*>((uint16_t*)base + off) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll

@@ -81,6 +81,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float v) {
     return (uint16_t)(x >> 16);
 }
 
+// Two values to bf16 in one word (x low) with v_cvt_pk_bf16_f32: round-to-nearest-even, NaN stays NaN; one
+// instruction where f32_to_bf16 takes six a value.
+__device__ __forceinline__ uint32_t pk_bf16(float x, float y) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2bf b = {(__bf16)x, (__bf16)y};
+    return __builtin_bit_cast(uint32_t, b);
+}
+
 __device__ __forceinline__ uint16_t f32_to_f16(float v) {
     _Float16 h = (_Float16)v;
     return __builtin_bit_cast(uint16_t, h);
@@ -105,6 +113,13 @@ __device__ __forceinline__ void store_from_f32(void* p, int64_t i, float v) {
     if constexpr (DT == kF32) ((float*)p)[i] = v;
     else if constexpr (DT == kBF16) ((uint16_t*)p)[i] = f32_to_bf16(v);
     else ((uint16_t*)p)[i] = f32_to_f16(v);
+}
+
+// Two values of a 2-byte type (kBF16 or kF16) in one word, x low.
+template <int DT>
+__device__ __forceinline__ uint32_t pk16(float x, float y) {
+    if constexpr (DT == kBF16) return pk_bf16(x, y);
+    else return (uint32_t)f32_to_f16(x) | ((uint32_t)f32_to_f16(y) << 16);
 }
 
 // sigmoid(g) = 1 / (1 + e^-g) from the hardware exp2 (v_exp_f32) of -g*log2(e) and the hardware reciprocal
