@@ -171,14 +171,12 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     fq.set(wq * C::MQ, lane);
 
     int stage = 0;
-    constexpr int AFTER = parts_after_meet<C::MP, LPS>();
-    Arrival<S, LPS, C::MP * C::MQ / 2> arrive;
     Frags<C::MP, C::MQ> f;
     if constexpr (PIPED) {
-        arrive();
+        arrive<S, LPS>();
         f.first(fp, fq, lds, lds + P::BYTES);
 #pragma unroll
-        for (int j = 0; j < LPS; j++) part(j);
+        for (int j = 0; j < parts_after_meet<C::MP, LPS>(); j++) part(j);
     }
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
@@ -188,41 +186,29 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
 #pragma unroll
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (PIPED) {
-            // (one body after the other: as two branches of a loop they would keep two sets of accumulators)
-            uint32_t at = lds + stage * STAGE;
-            stage = stage + 1 == S ? 0 : stage + 1;
-            uint32_t next = lds + stage * STAGE;
-            step_pipelined<false, C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
 #pragma unroll 1
-            for (int kt = 1; kt < steps; kt++) {
-                at = next;
+            for (int kt = 0; kt < steps; kt++) {
+                const uint32_t at = lds + stage * STAGE;
                 stage = stage + 1 == S ? 0 : stage + 1;
-                next = lds + stage * STAGE;
-                step_pipelined<true, C::MP, C::MQ, F16, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, arrive, part);
+                const uint32_t next = lds + stage * STAGE;
+                step_pipelined<C::MP, C::MQ, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
             }
         } else {
 #pragma unroll 1
             for (int kt = 0; kt < steps; kt++) {
                 const uint32_t at = lds + stage * STAGE;
                 stage = stage + 1 == S ? 0 : stage + 1;
-                arrive();
+                arrive<S, LPS>();
                 produce();                             // into the stage that the step before this one read
                 step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
             }
-        }
-        // the rest of the stage that is being requested goes out before the stores (see Arrival)
-        if constexpr (PIPED) {
-#pragma unroll
-            for (int j = AFTER; j < LPS; j++) part(j);
         }
         const Tile ti = locate(t);
         const int rows = min(ti.rows, C::BP) - wp * C::MP * 16;
         const int64_t c0 = ti.n0 + wq * C::MQ * 16;
         const int cols = (int)min(g.N - c0, (int64_t)(C::MQ * 16));
-        int stores = 0;
         if (rows > 0 && cols > 0)
-            stores = store_wave_dt(g.out, g.out_dt, false, (ti.row0 + wp * C::MP * 16) * g.out_stride + c0, g.out_stride, rows, cols, acc, fresh(lane));
-        arrive.stored(stores);
+            store_wave_dt(g.out, g.out_dt, false, (ti.row0 + wp * C::MP * 16) * g.out_stride + c0, g.out_stride, rows, cols, acc, fresh(lane));
     }
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }

@@ -203,12 +203,11 @@ __device__ __forceinline__ void step_mfma(v4f (&acc)[MP][MQ], const FP& fp, cons
 
 // The same step as a software pipeline, for tiles whose MFMAs are the bound.  Its 2 MP groups of MQ MFMAs take
 // their P fragments from a ring that is read kAhead groups ahead.  When the last fragments of this stage are in
-// registers the workgroup meets (`meet`: the next stage has landed for every wave, and this one is free), and the
+// registers the workgroup meets (the next stage has landed for every wave, and this one is free), and the
 // groups that are left cover the first reads of the next stage, so no MFMA waits for LDS at a stage's start.  The
-// parts of the stage that `meet` begins to request (`part(j)`, one DMA each) are spread over the groups that
+// parts of the stage that is requested then (`part(j)`, one DMA each) are spread over the groups that
 // follow, into the next step: requested at once they fill the CU's address queue and the waves stall on it (dense
-// products ran 5 % slower).  REST: the parts left over from the step before are requested here; a tile's first step
-// has none, since they went out before the stores of the tile before it (see Arrival).
+// products ran 5 % slower).
 constexpr int kAhead = 3;
 
 // Parts of PARTS that a pipelined step of 2 MP groups requests after its meeting; the next step requests the rest.
@@ -218,33 +217,15 @@ constexpr int parts_after_meet() {
     return n < PARTS ? n : PARTS;
 }
 
-// The wait and the barrier that make the next stage readable: all but the S - 2 stages after it (LPS loads each) have
-// to be in.  Vector memory operations retire in order and stores are among them, so the first S - 1 waits after a
-// tile's stores, all for stages that were requested before them, let that many more operations stay in flight;
-// otherwise a tile's first steps would wait for its predecessor's stores to reach memory.  Only stores that the
-// wave is sure to have issued may be counted: one for each 16-row sub-tile row and 32 (16-bit) or 16 (fp32)
-// columns that hold an element, which is what `stored` gets; the count is rounded down to a level of E.
-template <int S, int LPS, int E>
-struct Arrival {
-    int grace = 0, level = 0;
-    __device__ __forceinline__ void stored(int count) {
-        grace = S - 1;
-        level = count >= 2 * E ? 3 : count >= E ? 2 : count >= E / 2 ? 1 : 0;
-    }
-    __device__ __forceinline__ void operator()() {
-        constexpr int N = (S - 2) * LPS;
-        static_assert(N + 2 * E < 64, "vmcnt counts to 63");
-        if (grace > 0 && level > 0) {
-            grace--;
-            if (level == 3) wait_loads<N + 2 * E>();
-            else if (level == 2) wait_loads<N + E>();
-            else wait_loads<N + E / 2>();
-        } else {
-            wait_loads<N>();
-        }
-        block_barrier();
-    }
-};
+// The wait and the barrier that make the next stage readable: all but the S - 2 stages after it (LPS loads each)
+// have to be in.  (Stores retire in the same order, so a tile's first wait covers its predecessor's stores as well.
+// Counting them out of it, with the stage's last parts requested before the stores, gained nothing once the stores
+// bypass the caches' order, and its registers cost more.)
+template <int S, int LPS>
+__device__ __forceinline__ void arrive() {
+    wait_loads<(S - 2) * LPS>();
+    block_barrier();
+}
 
 template <int MP, int MQ>
 struct Frags {
@@ -259,10 +240,10 @@ struct Frags {
     }
 };
 
-template <bool REST, int MP, int MQ, bool F16, int PARTS, class FP, class FQ, class Meet, class Part>
+template <int MP, int MQ, bool F16, int S, int PARTS, class FP, class FQ, class Part>
 __device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>& f, const FP& fp, const FQ& fq,
                                                uint32_t p_stage, uint32_t q_stage, uint32_t p_next, uint32_t q_next,
-                                               Meet& meet, const Part& part) {
+                                               const Part& part) {
     constexpr int G = 2 * MP, MEET = G - kAhead;
     static_assert(MP >= 4 && G % (kAhead + 1) == 0, "the ring's phase is the same in every step");
     constexpr int PER = (PARTS + G - 1) / G;              // parts a group
@@ -270,13 +251,13 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>
     for (int i = 0; i < G; i++) {
         if (i == MEET) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            meet();
+            arrive<S, PARTS>();
         }
         // the part whose turn it is, counted in groups since the meeting
 #pragma unroll
         for (int u = 0; u < PER; u++) {
             const int j = ((i - MEET + G) % G) * PER + u;
-            if (j < PARTS && (i >= MEET || REST)) part(j);
+            if (j < PARTS) part(j);
         }
         // this stage's fragments kAhead groups ahead, the second half's Q in time for group MP
         const int r = i + kAhead;
@@ -297,36 +278,69 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>
     }
 }
 
+// Lanes r and r + 8 of each 16 exchange halves: a holds 16 bytes of row r at one place, b 16 bytes of the same row 64
+// bytes further on.  After it a holds row r % 8 and b row 8 + r % 8, lanes below 8 the first place and the others the
+// second, so each of two stores writes 128 bytes (a whole cache line) of eight rows instead of half lines of sixteen.
+__device__ __forceinline__ void line_exchange(v4i& a, v4i& b, bool low) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int give = low ? b[i] : a[i];
+        const int got = __builtin_amdgcn_update_dpp(give, give, 0x128, 0xF, 0xF, false);     // row_ror:8
+        a[i] = low ? a[i] : got;
+        b[i] = low ? got : b[i];
+    }
+}
+
 // A wave's sub-tiles to out[p][q] (row stride in elements; `out` at the wave's element (0, 0)), rows below
 // `rows`, columns below `cols` (a multiple of 8); ADD: onto what is there, in fp32 before the rounding.  A 2-byte
-// type's sub-tiles n and n + 1 leave together: a permlane32 and a permlane16 swap of the packed words hand lane
-// 16q + r the eight columns 8q .. 8q+7 of row r, so a store writes 64 bytes of each of 16 rows.  The swaps run in
-// every lane, outside the bounds.
+// type's sub-tiles n and n + 1 are first joined: a permlane32 and a permlane16 swap of the packed words hand lane
+// 16q + r the eight columns 8q .. 8q+7 of row r.  Two such pieces (or two fp32 sub-tiles) then leave as whole lines
+// (line_exchange), past the caches' usual order: kept as ordinary dirty lines they pushed the operands out of L2
+// and were written back only when the next tile's loads needed their place.  The moves run in every lane, outside
+// the bounds.
 template <int DT, bool ADD, int MP, int MQ>
 __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, int cols, const v4f (&acc)[MP][MQ],
                                            int lane) {
     constexpr int ESZ = DT == kF32 ? 4 : 2;
+    constexpr int JOIN = DT == kF32 ? 1 : 2;             // sub-tiles of a 16-byte piece per lane
     const bool vec = stride % (16 / ESZ) == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
     const int r0 = lane & 15, q4 = 4 * (lane >> 4);
+    const bool low = r0 < 8;
     char* row = (char*)out + r0 * (stride * ESZ);
+    const int64_t step = 16 * stride * ESZ;
 #pragma unroll
     for (int m = 0; m < MP; m++) {
         if (m * 16 >= rows) break;                                           // wave-uniform
         asm volatile("" ::: "memory");         // row by row: the accumulators leave few registers for addresses
         const bool in = m * 16 + r0 < rows;
-        if constexpr (DT != kF32 && MQ % 2 == 0 && !ADD) {
+        if constexpr (MQ % (2 * JOIN) == 0 && !ADD) {
             if (vec) {
+                char* line = row - (low ? 0 : 8 * stride * ESZ);             // row r % 8 of the sixteen
+                const bool in_a = m * 16 + (r0 & 7) < rows, in_b = m * 16 + 8 + (r0 & 7) < rows;
 #pragma unroll
-                for (int n = 0; n < MQ; n += 2) {
-                    const v4f x = acc[m][n], y = acc[m][n + 1];
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(pk16<DT>(x[0], x[1]), pk16<DT>(y[0], y[1]), false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(pk16<DT>(x[2], x[3]), pk16<DT>(y[2], y[3]), false, false);
-                    const auto t0 = __builtin_amdgcn_permlane16_swap(s0[0], s0[1], false, false);
-                    const auto t1 = __builtin_amdgcn_permlane16_swap(s1[0], s1[1], false, false);
-                    const int c = n * 16 + 2 * q4;
-                    if (in && c < cols) *reinterpret_cast<uint4*>(row + c * 2) = make_uint4(t0[0], t1[0], t0[1], t1[1]);
+                for (int n = 0; n < MQ; n += 2 * JOIN) {
+                    v4i piece[2];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const v4f x = acc[m][n + h * JOIN];
+                        if constexpr (DT == kF32) {
+                            piece[h] = __builtin_bit_cast(v4i, x);
+                        } else {
+                            const v4f y = acc[m][n + h * JOIN + 1];
+                            const auto s0 = __builtin_amdgcn_permlane32_swap(pk16<DT>(x[0], x[1]), pk16<DT>(y[0], y[1]), false, false);
+                            const auto s1 = __builtin_amdgcn_permlane32_swap(pk16<DT>(x[2], x[3]), pk16<DT>(y[2], y[3]), false, false);
+                            const auto t0 = __builtin_amdgcn_permlane16_swap(s0[0], s0[1], false, false);
+                            const auto t1 = __builtin_amdgcn_permlane16_swap(s1[0], s1[1], false, false);
+                            piece[h] = v4i{(int)t0[0], (int)t1[0], (int)t0[1], (int)t1[1]};
+                        }
+                    }
+                    line_exchange(piece[0], piece[1], low);
+                    const int c = n * 16 + (low ? 0 : 16 * JOIN) + q4 * JOIN;
+                    if (in_a && c < cols) __builtin_nontemporal_store(piece[0], reinterpret_cast<v4i*>(line + c * ESZ));
+                    if (in_b && c < cols)
+                        __builtin_nontemporal_store(piece[1], reinterpret_cast<v4i*>(line + 8 * stride * ESZ + c * ESZ));
                 }
-                row += 16 * stride * ESZ;
+                row += step;
                 continue;
             }
         }
@@ -348,21 +362,18 @@ __device__ __forceinline__ void store_wave(void* out, int64_t stride, int rows, 
                 }
             }
         }
-        row += 16 * stride * ESZ;
+        row += step;
     }
 }
 
-// The same for a run-time type; `at` is the wave's first element of out, in elements.  Returns the store
-// instructions that the wave has issued at least (Arrival::stored).
+// The same for a run-time type; `at` is the wave's first element of out, in elements.
 template <int MP, int MQ>
-__device__ __forceinline__ int store_wave_dt(void* out, int out_dt, bool add, int64_t at, int64_t stride, int rows, int cols,
+__device__ __forceinline__ void store_wave_dt(void* out, int out_dt, bool add, int64_t at, int64_t stride, int rows, int cols,
                                               const v4f (&acc)[MP][MQ], int lane) {
     char* p = (char*)out + at * (out_dt == MOE_F32 ? 4 : 2);
     if (out_dt == MOE_F32) add ? store_wave<kF32, true>(p, stride, rows, cols, acc, lane) : store_wave<kF32, false>(p, stride, rows, cols, acc, lane);
     else if (out_dt == MOE_BF16) add ? store_wave<kBF16, true>(p, stride, rows, cols, acc, lane) : store_wave<kBF16, false>(p, stride, rows, cols, acc, lane);
     else add ? store_wave<kF16, true>(p, stride, rows, cols, acc, lane) : store_wave<kF16, false>(p, stride, rows, cols, acc, lane);
-    const int width = out_dt == MOE_F32 || MQ == 1 ? 16 : 32;
-    return (min(rows, MP * 16) + 15) / 16 * ((cols + width - 1) / width);
 }
 
 }  // namespace b16
