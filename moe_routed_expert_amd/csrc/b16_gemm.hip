@@ -48,53 +48,84 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     using Q = std::conditional_t<QT, TMajor<C::BQ, C::NW>, KMajor<C::BQ, C::NW>>;
     constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
-    __shared__ int first_tile[kMaxExperts + 1];       // M tiles before expert e; [n_experts] is the total
-    __shared__ int first_row[kMaxExperts + 1];        // rows of expert e: [first_row[e], first_row[e] + count)
-    __shared__ int wave_sum[C::NW];
+    // Before expert e: its rows, and the M tiles of three kinds ([n_experts] is the total): whole ones (BP rows),
+    // and last ones of more and of at most BP / 2 rows.
+    __shared__ int first_row[kMaxExperts + 1], first_whole[kMaxExperts + 1];
+    __shared__ uint16_t first_long[kMaxExperts + 1], first_short[kMaxExperts + 1];
+    __shared__ int wave_sum[2][C::NW];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int E = g.n_experts;
 
-    // the tile table: EPT consecutive experts per thread, a scan over the block
+    // the tile table: EPT consecutive experts per thread, a scan of the counts over the block (the two kinds of last
+    // tiles in the halves of one word)
     {
         constexpr int EPT = kMaxExperts / C::THREADS;
-        int n[EPT], sum = 0;
+        int whole[EPT], last[EPT], sum_w = 0, sum_l = 0;
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
-            n[i] = 0;
+            whole[i] = last[i] = 0;
             if (e < E) {
                 const int lo = min(max(g.offsets[e], 0), g.m_rows), hi = min(max(g.offsets[e + 1], lo), g.m_rows);
+                const int rest = (hi - lo) % C::BP;
                 first_row[e] = lo;
                 if (e == E - 1) first_row[E] = hi;
-                n[i] = (hi - lo + C::BP - 1) / C::BP;
+                whole[i] = (hi - lo) / C::BP;
+                last[i] = rest > C::BP / 2 ? 1 : rest > 0 ? 1 << 16 : 0;
             }
-            sum += n[i];
+            sum_w += whole[i];
+            sum_l += last[i];
         }
-        int x = sum;
+        int w = sum_w, l = sum_l;
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
-            const int y = __shfl_up(x, d, kWave);
-            if (lane >= d) x += y;
+            const int yw = __shfl_up(w, d, kWave), yl = __shfl_up(l, d, kWave);
+            if (lane >= d) {
+                w += yw;
+                l += yl;
+            }
         }
-        if (lane == kWave - 1) wave_sum[wave] = x;
+        if (lane == kWave - 1) {
+            wave_sum[0][wave] = w;
+            wave_sum[1][wave] = l;
+        }
         __syncthreads();
-        int before = x - sum;
-        for (int w = 0; w < wave; w++) before += wave_sum[w];
+        w -= sum_w;
+        l -= sum_l;
+        for (int i = 0; i < wave; i++) {
+            w += wave_sum[0][i];
+            l += wave_sum[1][i];
+        }
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
-            if (e < E) first_tile[e] = before;
-            before += n[i];
-            if (e == E - 1) first_tile[E] = before;
+            if (e < E) {
+                first_whole[e] = w;
+                first_long[e] = (uint16_t)l;
+                first_short[e] = (uint16_t)(l >> 16);
+            }
+            w += whole[i];
+            l += last[i];
+            if (e == E - 1) {
+                first_whole[E] = w;
+                first_long[E] = (uint16_t)l;
+                first_short[E] = (uint16_t)(l >> 16);
+            }
         }
         __syncthreads();
     }
-    const int m_tiles = __builtin_amdgcn_readfirstlane(first_tile[E]);
+    const int whole_tiles = __builtin_amdgcn_readfirstlane(first_whole[E]);
+    const int long_tiles = __builtin_amdgcn_readfirstlane(first_long[E]);
+    const int m_tiles = whole_tiles + long_tiles + __builtin_amdgcn_readfirstlane(first_short[E]);
     const int tiles = m_tiles * g.n_tiles;
     const int G = gridDim.x;
     const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
+
+    // Tile of this workgroup in round s.  The tiles that do not fill a last round go to the workgroups from the other
+    // end: whole tiles come first, so those had the shorter tiles of the round before.
+    auto tile_at = [&](int s) { return s * G + ((s + 1) * G > tiles ? G - 1 - start : start); };
 
     struct Tile {
         int expert, row0, rows, n0;
@@ -104,17 +135,23 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
         const int panel = t / per, r = t - panel * per;
         const int height = min(kPanel, m_tiles - panel * kPanel);
         const int nt = r / height, mt = panel * kPanel + r - nt * height;
-        int lo = 0, hi = E - 1;                        // last expert whose first tile is <= mt
+        // the last expert whose first tile of the kind is <= its number: the tile's expert
+        const bool whole = mt < whole_tiles, is_long = mt < whole_tiles + long_tiles;
+        const int k = whole ? mt : mt - whole_tiles - (is_long ? 0 : long_tiles);
+        auto first = [&](int e) {
+            return __builtin_amdgcn_readfirstlane(whole ? first_whole[e] : is_long ? (int)first_long[e] : (int)first_short[e]);
+        };
+        int lo = 0, hi = E - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (__builtin_amdgcn_readfirstlane(first_tile[mid]) <= mt) lo = mid;
+            if (first(mid) <= k) lo = mid;
             else hi = mid - 1;
         }
         Tile ti;
         ti.expert = lo;
-        const int skip = (mt - __builtin_amdgcn_readfirstlane(first_tile[lo])) * C::BP;
-        ti.row0 = __builtin_amdgcn_readfirstlane(first_row[lo]) + skip;
-        ti.rows = __builtin_amdgcn_readfirstlane(first_row[lo + 1]) - ti.row0;
+        const int from = __builtin_amdgcn_readfirstlane(first_row[lo]), end = __builtin_amdgcn_readfirstlane(first_row[lo + 1]);
+        ti.row0 = whole ? from + (k - first(lo)) * C::BP : end - (end - from) % C::BP;
+        ti.rows = whole ? C::BP : end - ti.row0;
         ti.n0 = nt * C::BQ;
         return ti;
     };
@@ -126,7 +163,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     // (prod_k = 0) into stages that nobody reads, so the loads in flight can be counted the same way to the end.
     P p;
     Q q;
-    int prod_t = start, prod_left = 0, prod_kt = 0, prod_stage = 0;   // steps left of the tile, and the next one's k
+    int prod_t = tile_at(0), prod_round = 0, prod_left = 0, prod_kt = 0, prod_stage = 0;   // steps left of the tile, and the next one's k
     int64_t prod_k = 0;
     auto aim = [&]() {
         prod_k = prod_t < tiles ? g.K : 0;
@@ -149,7 +186,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
             prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
             prod_kt = prod_kt + 1 == steps ? 0 : prod_kt + 1;
             if (--prod_left <= 0) {
-                prod_t += G;
+                prod_t = tile_at(++prod_round);
                 aim();
             }
         }
@@ -158,7 +195,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
 #pragma unroll
         for (int j = 0; j < LPS; j++) part(j);
     };
-    if (start >= tiles) return;
+    if (tile_at(0) >= tiles) return;
     aim();
     constexpr bool PIPED = C::MP >= 4;                 // a wave's MFMAs are worth the software pipeline
 #pragma unroll 1
@@ -171,27 +208,47 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     fq.set(wq * C::MQ, lane);
 
     int stage = 0;
-    Frags<C::MP, C::MQ> f;
+    Frags<C::MQ> f;
     if constexpr (PIPED) {
         arrive<S, LPS>();
         f.first(fp, fq, lds, lds + P::BYTES);
 #pragma unroll
-        for (int j = 0; j < parts_after_meet<C::MP, LPS>(); j++) part(j);
+        for (int j = 0; j < parts_per_group<C::MP, LPS>; j++) part(j);
     }
 #pragma unroll 1
-    for (int t = start; t < tiles; t += G) {
+    for (int round = 0, t; (t = tile_at(round)) < tiles; round++) {
+        const Tile ti = locate(t);
+        const int rows = min(ti.rows, C::BP) - wp * C::MP * 16;       // of this wave
+        const int subs = (rows + 15) / 16;
         v4f acc[C::MP][C::MQ];
 #pragma unroll
         for (int m = 0; m < C::MP; m++)
 #pragma unroll
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (PIPED) {
-#pragma unroll 1
-            for (int kt = 0; kt < steps; kt++) {
-                const uint32_t at = lds + stage * STAGE;
+            // A wave with at most half its rows in use leaves the other half's MFMAs out (a tile's two wave rows share
+            // their SIMDs, so a last tile of few rows takes about half the time).  Two loops in a row, of which one
+            // runs: as branches of one loop they would keep two sets of accumulators.
+            const bool half = C::MP == 8 && subs <= 4;
+            uint32_t at = lds + stage * STAGE;
+            auto next_stage = [&]() {
                 stage = stage + 1 == S ? 0 : stage + 1;
-                const uint32_t next = lds + stage * STAGE;
-                step_pipelined<C::MP, C::MQ, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
+                return lds + stage * STAGE;
+            };
+#pragma unroll 1
+            for (int kt = half ? steps : 0; kt < steps; kt++) {
+                const uint32_t next = next_stage();
+                step_pipelined<C::MP, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
+                at = next;
+            }
+            if constexpr (C::MP == 8) {
+                static_assert(parts_per_group<C::MP, LPS> == parts_per_group<4, LPS>, "one phase of the parts");
+#pragma unroll 1
+                for (int kt = half ? 0 : steps; kt < steps; kt++) {
+                    const uint32_t next = next_stage();
+                    step_pipelined<4, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
+                    at = next;
+                }
             }
         } else {
 #pragma unroll 1
@@ -203,8 +260,6 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
                 step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
             }
         }
-        const Tile ti = locate(t);
-        const int rows = min(ti.rows, C::BP) - wp * C::MP * 16;
         const int64_t c0 = ti.n0 + wq * C::MQ * 16;
         const int cols = (int)min(g.N - c0, (int64_t)(C::MQ * 16));
         if (rows > 0 && cols > 0)

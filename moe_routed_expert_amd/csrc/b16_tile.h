@@ -201,22 +201,6 @@ __device__ __forceinline__ void step_mfma(v4f (&acc)[MP][MQ], const FP& fp, cons
     }
 }
 
-// The same step as a software pipeline, for tiles whose MFMAs are the bound.  Its 2 MP groups of MQ MFMAs take
-// their P fragments from a ring that is read kAhead groups ahead.  When the last fragments of this stage are in
-// registers the workgroup meets (the next stage has landed for every wave, and this one is free), and the
-// groups that are left cover the first reads of the next stage, so no MFMA waits for LDS at a stage's start.  The
-// parts of the stage that is requested then (`part(j)`, one DMA each) are spread over the groups that
-// follow, into the next step: requested at once they fill the CU's address queue and the waves stall on it (dense
-// products ran 5 % slower).
-constexpr int kAhead = 3;
-
-// Parts of PARTS that a pipelined step of 2 MP groups requests after its meeting; the next step requests the rest.
-template <int MP, int PARTS>
-constexpr int parts_after_meet() {
-    const int n = kAhead * ((PARTS + 2 * MP - 1) / (2 * MP));
-    return n < PARTS ? n : PARTS;
-}
-
 // The wait and the barrier that make the next stage readable: all but the S - 2 stages after it (LPS loads each)
 // have to be in.  (Stores retire in the same order, so a tile's first wait covers its predecessor's stores as well.
 // Counting them out of it, with the stage's last parts requested before the stores, gained nothing once the stores
@@ -227,53 +211,56 @@ __device__ __forceinline__ void arrive() {
     block_barrier();
 }
 
-template <int MP, int MQ>
+// The same step as a software pipeline, for tiles whose MFMAs are the bound: 2 MP groups of MQ MFMAs, each group's P
+// fragment read while the group before it is multiplied (three groups ahead measured the same).  Before its last
+// group the last fragments of this stage are in registers and the workgroup meets: the next stage has landed for
+// every wave, and this one is free.  That group then covers the first reads of the next stage, so no MFMA waits for
+// LDS at a stage's start, and the PARTS loads of the stage that takes this one's place (`part(j)`) are spread over
+// it and the groups of the next step: requested at once they fill the CU's address queue and the waves stall on it
+// (dense products ran 5 % slower).  ROWS >= MP: the sub-tile rows of acc; a step may take the first MP only.
+template <int MQ>
 struct Frags {
-    v8s p[kAhead + 1];
+    v8s p[2];
     v8s q[2][MQ];
     template <class FP, class FQ>
     __device__ __forceinline__ void first(const FP& fp, const FQ& fq, uint32_t p_stage, uint32_t q_stage) {
 #pragma unroll
         for (int n = 0; n < MQ; n++) q[0][n] = fq.read(q_stage, n, 0);
-#pragma unroll
-        for (int i = 0; i < kAhead; i++) p[i] = fp.read(p_stage, i % MP, i / MP);
+        p[0] = fp.read(p_stage, 0, 0);
     }
 };
 
-template <int MP, int MQ, bool F16, int S, int PARTS, class FP, class FQ, class Part>
-__device__ __forceinline__ void step_pipelined(v4f (&acc)[MP][MQ], Frags<MP, MQ>& f, const FP& fp, const FQ& fq,
+// Parts a group, and so the parts that the group after the meeting requests.
+template <int MP, int PARTS>
+constexpr int parts_per_group = (PARTS + 2 * MP - 1) / (2 * MP);
+
+template <int MP, bool F16, int S, int PARTS, int ROWS, int MQ, class FP, class FQ, class Part>
+__device__ __forceinline__ void step_pipelined(v4f (&acc)[ROWS][MQ], Frags<MQ>& f, const FP& fp, const FQ& fq,
                                                uint32_t p_stage, uint32_t q_stage, uint32_t p_next, uint32_t q_next,
                                                const Part& part) {
-    constexpr int G = 2 * MP, MEET = G - kAhead;
-    static_assert(MP >= 4 && G % (kAhead + 1) == 0, "the ring's phase is the same in every step");
-    constexpr int PER = (PARTS + G - 1) / G;              // parts a group
+    constexpr int G = 2 * MP, PER = parts_per_group<MP, PARTS>;
+    constexpr int Q1 = MP > MQ ? MP - 1 - MQ : 0;         // from this group on, one fragment of Q's second half each
+    static_assert(MP >= 4 && MP >= MQ, "Q's second half is read before its first group");
 #pragma unroll
     for (int i = 0; i < G; i++) {
-        if (i == MEET) {
+        if (i == G - 1) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             arrive<S, PARTS>();
         }
-        // the part whose turn it is, counted in groups since the meeting
 #pragma unroll
         for (int u = 0; u < PER; u++) {
-            const int j = ((i - MEET + G) % G) * PER + u;
+            const int j = ((i + 1) % G) * PER + u;
             if (j < PARTS) part(j);
         }
-        // this stage's fragments kAhead groups ahead, the second half's Q in time for group MP
-        const int r = i + kAhead;
-        if (i < MEET) {
-            const int n = i - (MP - 1 - MQ > 0 ? MP - 1 - MQ : 0);
-            if (n >= 0 && n < MQ) f.q[1][n] = fq.read(q_stage, n, 1);
-            f.p[r % (kAhead + 1)] = fp.read(p_stage, r % MP, r / MP);
-        } else {                                          // the next stage's first
-#pragma unroll
-            for (int n = (i - MEET) * 2; n < MQ && n < (i - MEET) * 2 + 2; n++) f.q[0][n] = fq.read(q_next, n, 0);
-            f.p[r % (kAhead + 1)] = fp.read(p_next, r - G, 0);
+        if (i < G - 1) {
+            if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(q_stage, i - Q1, 1);
+            f.p[(i + 1) % 2] = fp.read(p_stage, (i + 1) % MP, (i + 1) / MP);
+        } else {
+            f.first(fp, fq, p_next, q_next);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = 0; n < MQ; n++)
-            acc[i % MP][n] = mfma16x16x32<F16>(f.q[i / MP][n], f.p[i % (kAhead + 1)], acc[i % MP][n]);
+        for (int n = 0; n < MQ; n++) acc[i % MP][n] = mfma16x16x32<F16>(f.q[i / MP][n], f.p[i % 2], acc[i % MP][n]);
         __builtin_amdgcn_sched_barrier(0);
     }
 }

@@ -200,12 +200,12 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     fq.set(wq * C::MQ, lane);
 
     int stage = 0;
-    Frags<C::MP, C::MQ> f;
+    Frags<C::MQ> f;
     if constexpr (PIPED) {
         arrive<S, LPS>();
         f.first(fp, fq, lds, lds + P::BYTES);
 #pragma unroll
-        for (int j = 0; j < parts_after_meet<C::MP, LPS>(); j++) part(j);
+        for (int j = 0; j < parts_per_group<C::MP, LPS>; j++) part(j);
     }
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
                 const uint32_t at = lds + stage * STAGE;
                 stage = stage + 1 == S ? 0 : stage + 1;
                 const uint32_t next = lds + stage * STAGE;
-                step_pipelined<C::MP, C::MQ, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
+                step_pipelined<C::MP, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
             }
         } else {
 #pragma unroll 1
