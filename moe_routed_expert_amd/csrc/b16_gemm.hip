@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
 #pragma unroll 1
             for (int kt = half ? steps : 0; kt < steps; kt++) {
                 const uint32_t next = next_stage();
-                step_pipelined<C::MP, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
+                step_pipelined<C::MP, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part, [](int) {});
                 at = next;
             }
             if constexpr (C::MP == 8) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
 #pragma unroll 1
                 for (int kt = half ? 0 : steps; kt < steps; kt++) {
                     const uint32_t next = next_stage();
-                    step_pipelined<4, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
+                    step_pipelined<4, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part, [](int) {});
                     at = next;
                 }
             }

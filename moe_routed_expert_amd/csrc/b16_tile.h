@@ -234,10 +234,11 @@ struct Frags {
 template <int MP, int PARTS>
 constexpr int parts_per_group = (PARTS + 2 * MP - 1) / (2 * MP);
 
-template <int MP, bool F16, int S, int PARTS, int ROWS, int MQ, class FP, class FQ, class Part>
+// `late(i)` runs in the groups before the meeting (group i): what has to be in the next stage by then.
+template <int MP, bool F16, int S, int PARTS, int ROWS, int MQ, class FP, class FQ, class Part, class Late>
 __device__ __forceinline__ void step_pipelined(v4f (&acc)[ROWS][MQ], Frags<MQ>& f, const FP& fp, const FQ& fq,
                                                uint32_t p_stage, uint32_t q_stage, uint32_t p_next, uint32_t q_next,
-                                               const Part& part) {
+                                               const Part& part, const Late& late) {
     constexpr int G = 2 * MP, PER = parts_per_group<MP, PARTS>;
     constexpr int Q1 = MP > MQ ? MP - 1 - MQ : 0;         // from this group on, one fragment of Q's second half each
     static_assert(MP >= 4 && MP >= MQ, "Q's second half is read before its first group");
@@ -252,6 +253,7 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[ROWS][MQ], Frags<MQ>& 
             const int j = ((i + 1) % G) * PER + u;
             if (j < PARTS) part(j);
         }
+        late(i);
         if (i < G - 1) {
             if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(q_stage, i - Q1, 1);
             f.p[(i + 1) % 2] = fp.read(p_stage, (i + 1) % MP, (i + 1) / MP);

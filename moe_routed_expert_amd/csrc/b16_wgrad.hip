@@ -78,23 +78,21 @@ struct TSaved {
             scale[j] = *(in ? ss : (const float*)&kZeroPiece);
         }
     }
-    __device__ __forceinline__ void commit(uint32_t dst, int tid) const {
+    // Piece j into the stage at dst.
+    __device__ __forceinline__ void commit(int j, uint32_t dst, int tid) const {
+        const int k = row(j, tid), c = (j * 64 * NW + tid) % PIECES;
+        const uint32_t at = dst + k * (T * 2) + ((c ^ TMajor<T, NW>::swizzle(k)) << 5);
+        const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+        uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < PER; j++) {
-            const int k = row(j, tid), c = (j * 64 * NW + tid) % PIECES;
-            const uint32_t at = dst + k * (T * 2) + ((c ^ TMajor<T, NW>::swizzle(k)) << 5);
-            const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
-                const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-                o[2 * i] = pk16<F16 ? kF16 : kBF16>(lo[0] * scale[j], lo[1] * scale[j]);
-                o[2 * i + 1] = pk16<F16 ? kF16 : kBF16>(hi[0] * scale[j], hi[1] * scale[j]);
-            }
-            *(MOE_LDS v4i*)(uintptr_t)at = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
-            *(MOE_LDS v4i*)(uintptr_t)(at + 16) = v4i{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
+        for (int i = 0; i < 4; i++) {
+            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+            o[2 * i] = pk16<F16 ? kF16 : kBF16>(lo[0] * scale[j], lo[1] * scale[j]);
+            o[2 * i + 1] = pk16<F16 ? kF16 : kBF16>(hi[0] * scale[j], hi[1] * scale[j]);
         }
+        *(MOE_LDS v4i*)(uintptr_t)at = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+        *(MOE_LDS v4i*)(uintptr_t)(at + 16) = v4i{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
     }
 };
 
@@ -165,13 +163,15 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     };
     auto part = [&](int j) {
         const uint32_t dst = lds + prod_stage * STAGE;
-        if (j < P::LOADS) p.issue(j, dst, prod_kt, prod_rows, wave, lane);
-        else if constexpr (!SAVED) q.issue(j - P::LOADS, dst + P::BYTES, prod_kt, prod_rows, wave, lane);
-        if (j == LPS - 1) {
-            if constexpr (SAVED) {
+        if constexpr (SAVED) {
+            if (j == 0) {
                 q.load(prod_kt, prod_rows, tid);
                 saved_dst = dst + P::BYTES;
             }
+        }
+        if (j < P::LOADS) p.issue(j, dst, prod_kt, prod_rows, wave, lane);
+        else if constexpr (!SAVED) q.issue(j - P::LOADS, dst + P::BYTES, prod_kt, prod_rows, wave, lane);
+        if (j == LPS - 1) {
             prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
             if (++prod_kt == prod_steps) {
                 prod_kt = 0;
@@ -180,17 +180,25 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
             }
         }
     };
+    // SAVED: the pieces that part 0 asked for go to LDS shortly before the stage is published
+    auto late = [&](int i) {
+        if constexpr (SAVED) {
+#pragma unroll
+            for (int j = 0; j < Q::PER; j++)
+                if (i == 2 * C::MP - 2 - 2 * (Q::PER - 1 - j)) q.commit(j, saved_dst, tid);
+        }
+    };
     auto produce = [&]() {
 #pragma unroll
         for (int j = 0; j < LPS; j++) part(j);
     };
     if (start >= tiles) return;
     aim();
-    constexpr bool PIPED = C::MP >= 4 && !SAVED;
 #pragma unroll 1
     for (int i = 0; i < S - 1; i++) {
         produce();
-        if constexpr (SAVED) q.commit(saved_dst, tid);
+        if constexpr (SAVED)
+            for (int j = 0; j < Q::PER; j++) q.commit(j, saved_dst, tid);
     }
 
     typename P::Frag fp;
@@ -201,12 +209,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
 
     int stage = 0;
     Frags<C::MQ> f;
-    if constexpr (PIPED) {
-        arrive<S, LPS>();
-        f.first(fp, fq, lds, lds + P::BYTES);
+    arrive<S, LPS>();
+    f.first(fp, fq, lds, lds + P::BYTES);
 #pragma unroll
-        for (int j = 0; j < parts_per_group<C::MP, LPS>; j++) part(j);
-    }
+    for (int j = 0; j < parts_per_group<C::MP, LPS>; j++) part(j);
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
         const Tile ti = locate(t);
@@ -216,24 +222,12 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
         for (int m = 0; m < C::MP; m++)
 #pragma unroll
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (PIPED) {
 #pragma unroll 1
-            for (int kt = 0; kt < steps; kt++) {
-                const uint32_t at = lds + stage * STAGE;
-                stage = stage + 1 == S ? 0 : stage + 1;
-                const uint32_t next = lds + stage * STAGE;
-                step_pipelined<C::MP, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part);
-            }
-        } else {
-#pragma unroll 1
-            for (int kt = 0; kt < steps; kt++) {
-                const uint32_t at = lds + stage * STAGE;
-                stage = stage + 1 == S ? 0 : stage + 1;
-                arrive<S, LPS>();
-                produce();                             // into the stage that the step before this one read
-                step_mfma<C::MP, C::MQ, F16>(acc, fp, fq, at, at + P::BYTES);
-                if constexpr (SAVED) q.commit(saved_dst, tid);
-            }
+        for (int kt = 0; kt < steps; kt++) {
+            const uint32_t at = lds + stage * STAGE;
+            stage = stage + 1 == S ? 0 : stage + 1;
+            const uint32_t next = lds + stage * STAGE;
+            step_pipelined<C::MP, F16, S, LPS>(acc, f, fp, fq, at, at + P::BYTES, next, next + P::BYTES, part, late);
         }
         const int rows = (int)min(g.N - ti.n0, (int64_t)C::BP) - wp * C::MP * 16;
         const int64_t c0 = ti.k0 + wq * C::MQ * 16;
