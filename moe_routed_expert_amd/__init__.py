@@ -329,20 +329,24 @@ def route_prep(logits, topk, stream=None):
 # ---------------------------------------------------------------------------
 # 16-bit experts and the backward pass
 
+_entry = {}          # C functions by name
+
+
 def _call(fn, tensors, args, stream):
     """Calls C entry point fn(*args, stream) for tensors of one GPU, with that GPU current; stream None is its
     current stream."""
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
+    assert dev >= 0, "tensors on a GPU expected"
     for t in tensors:
-        if t is not None:
-            assert t.device == dev and t.is_cuda, "tensors of one GPU expected"
-    if dev.index != torch.cuda.current_device():
+        assert t is None or t.get_device() == dev, "tensors of one GPU expected"
+    f = _entry.get(fn) or _entry.setdefault(fn, getattr(lib(), fn))
+    if dev == torch._C._cuda_getDevice():
+        st = f(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    else:
         with torch.cuda.device(dev):
-            s = stream if stream is not None else torch.cuda.current_stream(dev)
-            _check(fn, getattr(lib(), fn)(*args, s.cuda_stream))
-        return
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    _check(fn, getattr(lib(), fn)(*args, s.cuda_stream))
+            st = f(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    if st != MOE_OK:
+        raise MoeError(fn, st)
 
 
 def _addr(t):
