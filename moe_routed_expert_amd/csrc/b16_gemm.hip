@@ -78,26 +78,8 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
             sum_w += whole[i];
             sum_l += last[i];
         }
-        int w = sum_w, l = sum_l;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int yw = __shfl_up(w, d, kWave), yl = __shfl_up(l, d, kWave);
-            if (lane >= d) {
-                w += yw;
-                l += yl;
-            }
-        }
-        if (lane == kWave - 1) {
-            wave_sum[0][wave] = w;
-            wave_sum[1][wave] = l;
-        }
-        __syncthreads();
-        w -= sum_w;
-        l -= sum_l;
-        for (int i = 0; i < wave; i++) {
-            w += wave_sum[0][i];
-            l += wave_sum[1][i];
-        }
+        int w = block_exclusive_scan<C::NW>(sum_w, wave_sum[0], lane, wave);
+        int l = block_exclusive_scan<C::NW>(sum_l, wave_sum[1], lane, wave);
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;

@@ -87,6 +87,22 @@ __device__ __forceinline__ v4f mfma16x16x32(v8s a, v8s b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
+// Exclusive scan of one int per thread over a block of NW waves (sums: NW ints of LDS).
+template <int NW>
+__device__ __forceinline__ int block_exclusive_scan(int v, int* sums, int lane, int wave) {
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int y = __shfl_up(x, d, kWave);
+        if (lane >= d) x += y;
+    }
+    if (lane == kWave - 1) sums[wave] = x;
+    __syncthreads();
+    x -= v;
+    for (int w = 0; w < wave; w++) x += sums[w];
+    return x;
+}
+
 // T rows of an operand whose k is contiguous, staged by NW waves.  Row r's 16-byte piece c sits at slot
 // c ^ ((r >> 1) & 7): 16 consecutive rows of one piece cover 256 bytes, all 64 banks.
 template <int T, int NW>

@@ -7,8 +7,9 @@
 //
 // Persistent workgroups walk the tiles of every expert, expert by expert, so experts of unequal length are
 // shared by all of them; an expert without rows gets zeros.  Where the gradient has few tiles and many rows
-// (small matrices, long sequences), an expert's rows are cut into `splits` ranges whose fp32 partial
-// gradients go to a workspace and are summed in range order: no atomics, so results do not depend on timing.
+// (small matrices, long sequences), the experts' rows are cut into chunks of one length, so long experts count as
+// several: their fp32 partial gradients go to a workspace and are summed in order, without atomics, so results do
+// not depend on timing.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -18,7 +19,6 @@
 namespace moe {
 namespace b16 {
 
-constexpr int kMaxSplits = 16;
 
 struct WgradArgs {
     const char* dy;
@@ -31,8 +31,9 @@ struct WgradArgs {
     int m_rows;
     int n_experts;
     int64_t N, K;
-    int n_tiles, k_tiles, splits;
-    char* out;                        // dW, or the fp32 partials when splits > 1
+    int n_tiles, k_tiles;
+    int chunk_rows, max_chunks;       // rows of a chunk (0: an expert's rows are one), and chunks that the workspace holds
+    char* out;                        // dW, or the fp32 partials [chunk][N][K]
     int out_dt;
     int64_t stride_e, stride_n;       // elements
     int accumulate;
@@ -103,42 +104,70 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     using Q = std::conditional_t<SAVED, TSaved<C::BQ, C::NW, F16>, QD>;
     constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
-    __shared__ int first_row[kMaxExperts + 1];         // device offsets, clamped to [0, m_rows]
+    __shared__ int first_row[kMaxExperts + 1], first_chunk[kMaxExperts + 1];   // offsets, clamped to [0, m_rows]
+    __shared__ int wave_sum[C::NW];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int per = g.n_tiles * g.k_tiles, per_expert = per * g.splits;
-    const int tiles = per_expert * g.n_experts;
+    const int per = g.n_tiles * g.k_tiles;
+    for (int e = tid; e <= g.n_experts; e += C::THREADS) first_row[e] = min(max(g.offsets[e], 0), g.m_rows);
+    __syncthreads();
+    int chunks = g.n_experts;
+    if (g.chunk_rows > 0) {
+        constexpr int EPT = kMaxExperts / C::THREADS;
+        int n[EPT], sum = 0;
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            n[i] = e < g.n_experts ? (max(first_row[e + 1] - first_row[e], 0) + g.chunk_rows - 1) / g.chunk_rows : 0;
+            sum += n[i];
+        }
+        int before = block_exclusive_scan<C::NW>(sum, wave_sum, lane, wave);
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            if (e < g.n_experts) first_chunk[e] = before;
+            before += n[i];
+            if (e == g.n_experts - 1) first_chunk[e + 1] = before;
+        }
+        __syncthreads();
+        chunks = min(__builtin_amdgcn_readfirstlane(first_chunk[g.n_experts]), g.max_chunks);
+    }
+    const int tiles = per * chunks;
     const int G = gridDim.x;
     const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
 
-    for (int e = tid; e <= g.n_experts; e += C::THREADS) first_row[e] = min(max(g.offsets[e], 0), g.m_rows);
-    __syncthreads();
-
     struct Tile {
-        int expert, split, row0, rows, n0, k0;
+        int chunk, row0, rows, n0, k0;
     };
     auto locate = [&](int t) {
         Tile ti;
-        ti.expert = t / per_expert;
-        t -= ti.expert * per_expert;
-        ti.split = t / per;
-        t -= ti.split * per;
+        ti.chunk = t / per;
+        t -= ti.chunk * per;
         const int panel = t / (kPanel * g.k_tiles);
         t -= panel * kPanel * g.k_tiles;
         const int height = min(kPanel, g.n_tiles - panel * kPanel);
         const int kt = t / height;
         ti.k0 = kt * C::BQ;
         ti.n0 = (panel * kPanel + t - kt * height) * C::BP;
-        const int lo = __builtin_amdgcn_readfirstlane(first_row[ti.expert]);
-        const int hi = max(__builtin_amdgcn_readfirstlane(first_row[ti.expert + 1]), lo);
-        const int len = ((hi - lo + kStep - 1) / kStep + g.splits - 1) / g.splits * kStep;   // rows of a split
-        const int64_t from = lo + (int64_t)ti.split * len;
-        ti.row0 = (int)(from < hi ? from : hi);
-        ti.rows = (int)(from + len < hi ? from + len : hi) - ti.row0;
+        int expert = ti.chunk, from = 0;
+        if (g.chunk_rows > 0) {                        // the last expert whose first chunk is <= this one
+            int lo = 0, hi = g.n_experts - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (__builtin_amdgcn_readfirstlane(first_chunk[mid]) <= ti.chunk) lo = mid;
+                else hi = mid - 1;
+            }
+            expert = lo;
+            from = (ti.chunk - __builtin_amdgcn_readfirstlane(first_chunk[lo])) * g.chunk_rows;
+        }
+        const int lo = __builtin_amdgcn_readfirstlane(first_row[expert]) + from;
+        ti.row0 = lo;
+        ti.rows = max(__builtin_amdgcn_readfirstlane(first_row[expert + 1]) - lo, 0);
+        if (g.chunk_rows > 0) ti.rows = min(ti.rows, g.chunk_rows);
         return ti;
     };
-    // a range without rows still takes one step, of zeros, so that every tile is stored
+    // an expert without rows still takes one step, of zeros, so that its tiles are stored
     auto steps_of = [&](const Tile& ti) { return max(1, (ti.rows + kStep - 1) / kStep); };
 
     // Producer, as in b16_gemm_kernel: past the last tile it goes on with zeros (prod_rows = 0).
@@ -233,27 +262,40 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
         const int64_t c0 = ti.k0 + wq * C::MQ * 16;
         const int cols = (int)min(g.K - c0, (int64_t)(C::MQ * 16));
         if (rows > 0 && cols > 0) {
-            const int64_t o = ((int64_t)ti.split * g.n_experts + ti.expert) * g.stride_e + (int64_t)(ti.n0 + wp * C::MP * 16) * g.stride_n + c0;
+            const int64_t o = ti.chunk * g.stride_e + (int64_t)(ti.n0 + wp * C::MP * 16) * g.stride_n + c0;
             store_wave_dt(g.out, g.out_dt, g.accumulate != 0, o, g.stride_n, rows, cols, acc, fresh(lane));
         }
     }
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
-// The partial gradients of `splits` row ranges, [split][e][n][k] in fp32, summed in range order (onto what is
-// there, when accumulating) and rounded once.  Four consecutive k a thread.
+// The chunks' partial gradients, [chunk][n][k] in fp32, summed in chunk order for each expert (onto what is there,
+// when accumulating) and rounded once.  Four consecutive k a thread, an expert per blockIdx.y; its chunks are
+// counted again from the offsets.
 template <int DT>
 __global__ void __launch_bounds__(256)
-wgrad_join_kernel(const float* __restrict__ part, int splits, int64_t E, int64_t N, int64_t K, void* __restrict__ out,
-                  int64_t stride_e, int64_t stride_n, int accumulate) {
-    const int64_t total = E * N * K / 4;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= total) return;
-    const int64_t k4 = K / 4, row = i / k4;
-    const int64_t k = (i - row * k4) * 4, e = row / N, n = row - e * N;
-    v4f sum = *reinterpret_cast<const v4f*>(part + i * 4);
-    for (int s = 1; s < splits; s++) sum += *reinterpret_cast<const v4f*>(part + s * E * N * K + i * 4);
-    const int64_t o = e * stride_e + n * stride_n + k;
+wgrad_join_kernel(const float* __restrict__ part, const int32_t* __restrict__ offsets, int m_rows, int chunk_rows,
+                  int max_chunks, int64_t N, int64_t K, void* __restrict__ out, int64_t stride_e, int64_t stride_n,
+                  int accumulate) {
+    __shared__ int wave_sum[4];
+    const int e = blockIdx.y, tid = threadIdx.x;
+    auto chunks_of = [&](int x) {
+        const int lo = min(max(offsets[x], 0), m_rows), hi = min(max(offsets[x + 1], 0), m_rows);
+        return (max(hi - lo, 0) + chunk_rows - 1) / chunk_rows;
+    };
+    int before = 0;
+    for (int x = tid; x < e; x += 256) before += chunks_of(x);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d, kWave);
+    if (tid % kWave == 0) wave_sum[tid / kWave] = before;
+    __syncthreads();
+    const int first = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+    const int last = min(first + chunks_of(e), max_chunks);
+    const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 4;
+    if (i >= N * K) return;
+    const int64_t n = i / K, k = i - n * K, o = e * stride_e + n * stride_n + k;
+    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = first; c < last; c++) sum += *reinterpret_cast<const v4f*>(part + c * (N * K) + i);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         float v = sum[j];
@@ -282,7 +324,7 @@ int wgrad_resident() {
 template <class C, bool SAVED, bool F16>
 int wgrad_launch_cfg(hipStream_t st, WgradArgs g) {
     const int64_t nt = ceil_div(g.N, C::BP), kt = ceil_div(g.K, C::BQ);
-    const int64_t tiles = nt * kt * g.n_experts * g.splits;
+    const int64_t tiles = nt * kt * (g.chunk_rows > 0 ? g.max_chunks : g.n_experts);
     if (nt * kt > 0x7FFFFFFF / 64 || tiles > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
     g.n_tiles = (int)nt;
     g.k_tiles = (int)kt;
@@ -310,13 +352,17 @@ bool wgrad_shape_ok(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
 // The large tile needs enough tiles for the device's 256 CUs.
 bool wgrad_large(int64_t E, int64_t N, int64_t K) { return ceil_div(N, 256) * ceil_div(K, 256) * E >= 512; }
 
-// Row ranges per expert: enough for two workgroups a CU, none shorter than 256 rows on average.
-int wgrad_splits(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
-    if (wgrad_large(E, N, K)) return 1;
-    const int64_t tiles = ceil_div(N, 128) * ceil_div(K, 128) * E;
-    const int64_t want = std::min<int64_t>({512 / tiles, m_rows / E / 256, kMaxSplits});
-    return want < 2 ? 1 : (int)want;
+// Rows of a chunk, or 0 where the experts' rows stay whole: enough chunks for two workgroups of the 128 x 128 form on
+// each of the device's 256 CUs, none shorter than 256 rows, and only where that cuts an average expert.
+int wgrad_chunk_rows(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
+    if (wgrad_large(E, N, K)) return 0;
+    const int64_t want = 512 / (ceil_div(N, 128) * ceil_div(K, 128));
+    if (want <= E) return 0;
+    const int64_t rows = std::max<int64_t>(256, ceil_div(ceil_div(m_rows, want - E), kStep) * kStep);
+    return rows * E <= m_rows ? (int)rows : 0;
 }
+
+int64_t wgrad_max_chunks(int64_t m_rows, int64_t E, int64_t chunk_rows) { return m_rows / chunk_rows + E; }
 
 }  // namespace b16
 }  // namespace moe
@@ -325,8 +371,8 @@ using namespace moe;
 
 extern "C" size_t moe_b16_grouped_wgrad_workspace_size(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     if (!b16::wgrad_shape_ok(m_rows, n_experts, N, K)) return 0;
-    const int s = b16::wgrad_splits(m_rows, n_experts, N, K);
-    return s > 1 ? (size_t)s * n_experts * N * K * 4 : 0;
+    const int rows = b16::wgrad_chunk_rows(m_rows, n_experts, N, K);
+    return rows > 0 ? (size_t)b16::wgrad_max_chunks(m_rows, n_experts, rows) * N * K * 4 : 0;
 }
 
 extern "C" int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void* a, int64_t a_stride,
@@ -352,26 +398,30 @@ extern "C" int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, 
     g.a = (const char*)a; g.a_stride = saved ? a_stride : a_stride * 2;
     g.a_s = a_s; g.a_s_stride = a_s_stride;
     g.offsets = expert_offsets; g.m_rows = (int)m_rows; g.n_experts = (int)n_experts; g.N = N; g.K = K;
-    g.splits = b16::wgrad_splits(m_rows, n_experts, N, K);
+    g.chunk_rows = b16::wgrad_chunk_rows(m_rows, n_experts, N, K);
     g.out = (char*)dw; g.out_dt = dw_dt; g.stride_e = dw_stride_e; g.stride_n = dw_stride_n;
     g.accumulate = accumulate;
     auto st = as_stream(stream);
-    if (g.splits > 1) {
+    if (g.chunk_rows > 0) {
+        g.max_chunks = (int)b16::wgrad_max_chunks(m_rows, n_experts, g.chunk_rows);
         if (!workspace) return MOE_ERR_NULL;
-        if (ws_bytes < (size_t)g.splits * n_experts * N * K * 4) return MOE_ERR_WORKSPACE;
+        if (ws_bytes < (size_t)g.max_chunks * N * K * 4) return MOE_ERR_WORKSPACE;
         if (!aligned16(workspace)) return MOE_ERR_ALIGN;
         g.out = (char*)workspace; g.out_dt = MOE_F32; g.stride_e = N * K; g.stride_n = K; g.accumulate = 0;
     }
     const int rc = b16::wgrad_large(n_experts, N, K) ? b16::wgrad_launch<b16::Tile256>(st, saved, dt == MOE_F16, g)
                                                      : b16::wgrad_launch<b16::Tile128>(st, saved, dt == MOE_F16, g);
-    if (rc != MOE_OK || g.splits == 1) return rc;
-    const dim3 grid((unsigned)ceil_div(n_experts * N * K / 4, 256)), block(256);
+    if (rc != MOE_OK || g.chunk_rows == 0) return rc;
+    const dim3 grid((unsigned)ceil_div(N * K / 4, 256), (unsigned)n_experts), block(256);
     const float* part = (const float*)workspace;
     if (dw_dt == MOE_F32)
-        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF32>), grid, block, 0, st, part, g.splits, n_experts, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF32>), grid, block, 0, st, part, expert_offsets, g.m_rows, g.chunk_rows,
+                           g.max_chunks, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
     else if (dw_dt == MOE_BF16)
-        hipLaunchKernelGGL((b16::wgrad_join_kernel<kBF16>), grid, block, 0, st, part, g.splits, n_experts, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+        hipLaunchKernelGGL((b16::wgrad_join_kernel<kBF16>), grid, block, 0, st, part, expert_offsets, g.m_rows, g.chunk_rows,
+                           g.max_chunks, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
     else
-        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF16>), grid, block, 0, st, part, g.splits, n_experts, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF16>), grid, block, 0, st, part, expert_offsets, g.m_rows, g.chunk_rows,
+                           g.max_chunks, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
     return launch_status();
 }
