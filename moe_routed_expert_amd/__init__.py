@@ -33,7 +33,7 @@ EXPORTS = (
     "moe_fused_decode_workspace_layout", "moe_fused_decode_workspace_init", "moe_fused_decode",
     "moe_route_prep_workspace_size", "moe_route_prep", "moe_bf8_grouped_gemm_act_quant",
     "moe_mxfp4_grouped_gemm", "moe_mxfp4_grouped_gemm_act_quant", "moe_fused_decode_noalloc", "moe_pack_weights",
-    "moe_grouped_block_m", "moe_b16_grouped_gemm", "moe_b16_grouped_wgrad", "moe_b16_grouped_wgrad_workspace_size",
+    "moe_grouped_block_m", "moe_b16_grouped_gemm", "moe_b16_grouped_tile", "moe_b16_grouped_wgrad", "moe_b16_grouped_wgrad_workspace_size",
     "moe_act_checkpoint", "moe_gated_act_backward", "moe_topk_reduce_backward", "moe_route_prep_backward",
 )
 
@@ -86,6 +86,7 @@ def lib():
             "moe_pack_weights": ([P, I64, I64, I64, I64, I64, I64, P, I64, P], I32),
             "moe_b16_grouped_gemm": ([P, I64, P, I64, I64, I64, I64, I64, I32, I32, I32, P, P, I64, I64, P, I32, I64,
                                       P], I32),
+            "moe_b16_grouped_tile": ([I64, I64, I64, I64, P], I32),
             "moe_b16_grouped_wgrad_workspace_size": ([I64, I64, I64, I64], SZ),
             "moe_b16_grouped_wgrad": ([P, I64, I32, P, I64, I32, P, I64, P, I64, I64, I64, I64, P, I32, I64, I64, I32,
                                        P, SZ, P], I32),
@@ -375,6 +376,13 @@ def b16_grouped_gemm(a, w, out, *, mode, expert_offsets=None, slot_ids=None, m_r
     _call("moe_b16_grouped_gemm", (a, w, out, expert_offsets, slot_ids), (
         a.data_ptr(), _rowstride(a), w.data_ptr(), w.stride(0), w.stride(1), E, N, K, _dt(a), int(w_trans), mode,
         _addr(expert_offsets), _addr(slot_ids), rows, a_row_div, out.data_ptr(), _dt(out), _rowstride(out)), stream)
+
+
+def b16_grouped_tile(m_rows, n_experts, N, K):
+    """(rows, columns) of the output tile that b16_grouped_gemm's grouped mode takes."""
+    t = (ctypes.c_int32 * 2)()
+    _check("moe_b16_grouped_tile", lib().moe_b16_grouped_tile(m_rows, n_experts, N, K, t))
+    return t[0], t[1]
 
 
 def b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K) -> int:

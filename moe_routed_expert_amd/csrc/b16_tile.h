@@ -151,19 +151,22 @@ struct KMajor {
 
 // 64 k rows of T elements of an operand whose own index is contiguous.  Row k's 32-byte column pair c sits at
 // c ^ g(k), g(k) = (k & 3) | ((k >> 3) & 1) << 2: the eight rows that two groups of 16 lanes read for one
-// sub-tile (8q .. 8q+3 and 8(q+1) .. 8(q+1)+3) fall into the eight 32-byte parts of 256 bytes.
+// sub-tile (8q .. 8q+3 and 8(q+1) .. 8(q+1)+3) fall into the eight 32-byte parts of 256 bytes.  (T = 64: a row is
+// 128 bytes, so k's lowest bit chooses the half already and g(k) = ((k >> 1) & 1) | ((k >> 3) & 1) << 1.)
 template <int T, int NW>
 struct TMajor {
     static constexpr int BYTES = T * kStep * 2;
     static constexpr int PIECES = T / 8;                                    // 16-byte pieces of a row
     static constexpr int ROWS = 64 / PIECES;                                // rows of one DMA
     static constexpr int LOADS = kStep / (ROWS * NW);
-    static_assert(T % 128 == 0 && LOADS * ROWS * NW == kStep, "whole swizzle groups");
+    static_assert((T % 128 == 0 || T == 64) && LOADS * ROWS * NW == kStep, "whole swizzle groups");
     const char* p[LOADS];
     int64_t stride;
 
     __device__ __forceinline__ static int row(int j, int wave, int lane) { return (j * NW + wave) * ROWS + lane / PIECES; }
-    __device__ __forceinline__ static int swizzle(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+    __device__ __forceinline__ static int swizzle(int k) {
+        return T == 64 ? ((k >> 1) & 1) | (((k >> 3) & 1) << 1) : (k & 3) | (((k >> 3) & 1) << 2);
+    }
 
     // k rows base + k * stride (bytes); column pieces from `valid` elements on repeat the last one.
     __device__ __forceinline__ void set(const void* base, int64_t stride_bytes, int valid, int wave, int lane) {
@@ -186,8 +189,7 @@ struct TMajor {
         uint32_t a;
         __device__ __forceinline__ void set(int sub0, int lane) {
             const int q = lane >> 4, r = (lane >> 2) & 3;
-            const int g = r | ((q & 1) << 2);
-            a = (uint32_t)((8 * q + r) * (T * 2) + (sub0 >> 3) * 256 + (((sub0 & 7) ^ g) << 5) + (lane & 3) * 8);
+            a = (uint32_t)((8 * q + r) * (T * 2) + (sub0 >> 3) * 256 + (((sub0 & 7) ^ swizzle(8 * q + r)) << 5) + (lane & 3) * 8);
         }
         __device__ __forceinline__ v8s read(uint32_t stage, int m, int ks) const {
             const uint32_t at = stage + (a ^ ((m & 7) << 5)) + (m >> 3) * 256 + ks * (32 * T * 2);

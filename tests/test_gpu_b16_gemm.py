@@ -31,7 +31,7 @@ def grouped(counts, N, K, dt, odt, trans, seed, extra=0, w=None, a=None):
     return out
 
 
-# counts reach every tile: up to 16, 64, 256 and more rows an expert, tiles that end inside an expert, empty experts
+# up to 16, 64, 256 and more rows an expert, tiles that end inside an expert, empty experts
 COUNTS = {"one": [1], "few": [3, 0, 16, 1, 0, 17], "mid": [0, 33, 64, 65], "many": [130, 0, 255, 129, 1],
           "large": [300, 513], "last_empty": [5, 9, 0, 0]}
 
@@ -56,6 +56,73 @@ def test_widths(counts, N, K, trans):
 def test_output_types(counts, dt, odt):
     grouped(COUNTS[counts], 136, 328, dt, odt, False, seed=7)
     grouped(COUNTS[counts], 136, 328, dt, odt, True, seed=8)
+
+
+# problems of each output tile: ragged rows, empty experts, last tiles of few and of many rows, whole tiles only, N and
+# K that end inside a tile and a step
+TILES = [((32, 64), [0, 33, 5, 64, 1], 264, 200), ((64, 64), [21, 0, 33, 18, 64, 40, 1, 23, 8, 15, 30, 20, 17, 29, 12, 2], 1000, 520),
+         ((64, 256), [63, 64, 65, 0] * 8 + [50] * 8, 2056, 72), ((64, 256), [130, 7, 64, 0, 100, 128, 1] * 2, 2056, 136),
+         ((128, 256), [129, 0, 127, 128, 1, 300] * 4, 1032, 136), ((128, 256), [2001, 1999], 1000, 72),
+         ((256, 256), [2660, 3300, 1029, 2011], 1032, 72), ((256, 256), [2660, 3300, 0, 3040], 1032, 328),
+         ((256, 256), [4096, 4096], 1032, 200), ((256, 256), [0, 0, 8000, 200, 1, 255, 257, 100], 1288, 136)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt,odt", [(BF, F32), (FP, FP), (BF, BF)])
+@pytest.mark.parametrize("tile,counts,N,K", TILES)
+def test_every_tile(tile, counts, N, K, dt, odt, trans):
+    assert m.b16_grouped_tile(int(sum(counts)), len(counts), N, K) == tile
+    grouped(counts, N, K, dt, odt, trans, seed=N + K + len(counts), extra=2)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("tile,counts,N,K", [TILES[i] for i in (0, 1, 3, 4, 7)])
+def test_every_tile_keeps_non_finite_values_apart(tile, counts, N, K, trans):
+    c, R, E = counts, int(sum(counts)), len(counts)
+    a, w = randn((R, K), BF, 1), randn((E, K, N) if trans else (E, N, K), BF, 2)
+    offs = offsets_of(c)
+    busy = [e for e in range(E) if c[e] > 0]
+    r, e = int(offs[busy[-1]]), busy[0]
+    a[r, K - 1] = float("nan")
+    if trans:
+        w[e, 3, N - 1] = float("inf")
+    else:
+        w[e, N - 1, 3] = float("inf")
+    out = torch.empty((R, N), dtype=F32, device=dev())
+    m.b16_grouped_gemm(a.to(dev()), w.to(dev()), out, mode=m.MOE_MODE_GROUPED, expert_offsets=to_dev(offs), w_trans=trans)
+    torch.cuda.synchronize()
+    want = np.zeros((R, N), bool)
+    want[r] = True
+    want[offs[e]:offs[e + 1], N - 1] = True
+    assert np.array_equal(~torch.isfinite(out).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("odt,pad", [(BF, 1), (F32, 1), (FP, 4), (F32, 2)])
+def test_every_tile_with_unaligned_output(odt, pad):
+    for tile, c, N, K in TILES[::2]:
+        R = int(sum(c))
+        a, w = randn((R, K), BF, 1), randn((len(c), N, K), BF, 2)
+        out = Guarded((R, N), odt, pad=pad)
+        m.b16_grouped_gemm(a.to(dev()), w.to(dev()), out.view, mode=m.MOE_MODE_GROUPED, expert_offsets=to_dev(offsets_of(c)))
+        torch.cuda.synchronize()
+        assert out.intact()
+        ref, mag = tr.grouped_gemm(f64(a), f64(w), offsets_of(c))
+        check(out.view, ref, sum_bound(K, mag, odt)(ref), "unaligned output")
+
+
+def test_large_tiles_replayed():
+    """The 256 x 256 and 128 x 256 tiles in a graph whose offsets change, some experts empty, then all rows in one."""
+    for (R, E, N, K), cuts in (((9000, 4, 1032, 200), [(0, 9000, 9000), (2000, 2100, 6000), (9000, 9000, 9000)]),
+                               ((4000, 4, 1000, 72), [(0, 0, 0), (1000, 1001, 3500), (128, 256, 384)])):
+        a, w = randn((R, K), BF, 1).to(dev()), randn((E, K, N), BF, 2).to(dev())
+        offs, out = to_dev(offsets_of([R, 0, 0, 0])), torch.empty((R, N), dtype=BF, device=dev())
+        call = lambda: m.b16_grouped_gemm(a, w, out, mode=m.MOE_MODE_GROUPED, expert_offsets=offs, w_trans=True)
+
+        def fresh(i):
+            offs.copy_(torch.tensor([0, *cuts[i], R], dtype=torch.int32))
+
+        for got, want in replayed(call, None, [out], fresh):
+            assert torch.equal(got[0], want[0])
 
 
 def test_rows_behind_the_last_are_left():

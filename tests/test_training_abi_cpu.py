@@ -39,6 +39,23 @@ def test_gemm_refusals(kw, want):
     assert gemm(**kw) == want
 
 
+def test_grouped_tile():
+    tiles = {(32, 64), (64, 64), (64, 256), (128, 256), (256, 256)}
+    seen = set()
+    for R in (1, 8, 100, 1000, 4000, 20000):
+        for E in (1, 8, 64, 256):
+            for N in (8, 264, 1000, 2048, 8192):
+                t = m.b16_grouped_tile(R, E, N, 1024)
+                assert t in tiles and t == m.b16_grouped_tile(R, E, N, 1024)
+                seen.add(t)
+    assert seen == tiles
+    out = (ctypes.c_int32 * 2)()
+    f = m.lib().moe_b16_grouped_tile
+    assert f(8, 4, 64, 64, None) == m.MOE_ERR_NULL
+    for bad in ((0, 4, 64, 64), (8, 0, 64, 64), (8, 1025, 64, 64), (8, 4, 60, 64), (8, 4, 64, 0), (2 ** 31, 4, 64, 64)):
+        assert f(*bad, out) == m.MOE_ERR_SHAPE
+
+
 def wgrad(**kw):
     a = dict(dy=FAKE, dy_stride=1024, dt=0, a=FAKE, a_stride=1024, a_dt=0, a_s=FAKE, a_s_stride=8, offsets=FAKE,
              n_experts=8, N=1024, K=1024, m_rows=8, dw=FAKE, dw_dt=1, dw_stride_e=1024 * 1024, dw_stride_n=1024,
