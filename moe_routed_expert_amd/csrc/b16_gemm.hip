@@ -341,9 +341,11 @@ int grouped_launch(hipStream_t st, bool trans, bool f16, const GemmArgs& g) {
 }
 
 // ------------------------------------------------------------------ slot mode
-// One wave holds kSlotCols columns of one row: its lanes take 8 consecutive k each (512 a pass), products and
-// sums in fp32, and the lanes' sums meet in six shuffles.  Bound by streaming the row's expert.
-constexpr int kSlotCols = 4;
+// One wave holds COLS columns of one row: its lanes take 8 consecutive k each (512 a chunk), products and sums in fp32,
+// and the lanes' sums meet in six shuffles.  Bound by streaming the row's expert, so a wave asks for UNROLL chunks of
+// all its columns (8 KB of weights) at once before it multiplies: 8 routes of 1536 x 2048 take 9.3 us (4.8 TB/s), 64
+// of them 67 us (5.9 TB/s), one row of 8192 x 8192 26 us.  Four columns a wave and a loop over single chunks took
+// 11.2, 77 and 48 us.
 constexpr int kSlotWaves = 4;
 
 template <bool F16>
@@ -357,41 +359,55 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
     }
 }
 
-template <bool F16>
+template <bool F16, int COLS, int UNROLL>
 __global__ void __launch_bounds__(64 * kSlotWaves)
 b16_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_row_div, int col_groups) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t r = blockIdx.x / (unsigned)col_groups;
-    const int64_t n0 = ((int64_t)(blockIdx.x % (unsigned)col_groups) * kSlotWaves + wave) * kSlotCols;
-    if (n0 >= g.N) return;
+    const int64_t n0 = ((int64_t)(blockIdx.x % (unsigned)col_groups) * kSlotWaves + wave) * COLS;
+    if (n0 >= g.N) return;                             // N is a multiple of COLS
     const int slot = slots[r];
-    float sum[kSlotCols];
-#pragma unroll
-    for (int c = 0; c < kSlotCols; c++) sum[c] = 0.0f;
+    float sum[COLS] = {};
     if (slot >= 0 && slot < g.n_experts) {
         const char* x = g.a + (r / a_row_div) * g.a_stride;
         const char* w = g.w + slot * g.w_stride_e + n0 * g.w_stride_r;
-#pragma unroll 4
-        for (int64_t k = lane * 8; k < g.K; k += kWave * 8) {
-            float xv[8];
-            unpack8<F16>(*reinterpret_cast<const uint4*>(x + k * 2), xv);
+        // UNROLL chunks from k0; in the last ones lanes past K read the last piece and count it as zero on both sides
+        auto chunks = [&](int64_t k0, auto tail) {
+            uint4 xv[UNROLL], wv[COLS][UNROLL];
 #pragma unroll
-            for (int c = 0; c < kSlotCols; c++) {
-                float wv[8];
-                unpack8<F16>(*reinterpret_cast<const uint4*>(w + c * g.w_stride_r + k * 2), wv);
+            for (int u = 0; u < UNROLL; u++) {
+                int64_t k = k0 + u * (kWave * 8) + lane * 8;
+                if (tail) k = k < g.K ? k : g.K - 8;
+                xv[u] = *reinterpret_cast<const uint4*>(x + k * 2);
 #pragma unroll
-                for (int i = 0; i < 8; i++) sum[c] = __builtin_fmaf(wv[i], xv[i], sum[c]);
+                for (int c = 0; c < COLS; c++) wv[c][u] = *reinterpret_cast<const uint4*>(w + c * g.w_stride_r + k * 2);
             }
-        }
 #pragma unroll
-        for (int c = 0; c < kSlotCols; c++)
+            for (int u = 0; u < UNROLL; u++) {
+                const bool in = !tail || k0 + u * (kWave * 8) + lane * 8 < g.K;
+                float xf[8];
+                unpack8<F16>(in ? xv[u] : make_uint4(0u, 0u, 0u, 0u), xf);
+#pragma unroll
+                for (int c = 0; c < COLS; c++) {
+                    float wf[8];
+                    unpack8<F16>(in ? wv[c][u] : make_uint4(0u, 0u, 0u, 0u), wf);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) sum[c] = __builtin_fmaf(wf[i], xf[i], sum[c]);
+                }
+            }
+        };
+        int64_t k0 = 0;
+        for (; k0 + UNROLL * kWave * 8 <= g.K; k0 += UNROLL * kWave * 8) chunks(k0, std::false_type{});
+        if (k0 < g.K) chunks(k0, std::true_type{});
+#pragma unroll
+        for (int c = 0; c < COLS; c++)
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) sum[c] += __shfl_xor(sum[c], d, kWave);
     }
-    if (lane < kSlotCols) {
+    if (lane < COLS) {
         float v = sum[0];
 #pragma unroll
-        for (int c = 1; c < kSlotCols; c++) v = lane == c ? sum[c] : v;
+        for (int c = 1; c < COLS; c++) v = lane == c ? sum[c] : v;
         const int64_t o = r * g.out_stride + n0 + lane;
         if (g.out_dt == MOE_F32) store_from_f32<kF32>(g.out, o, v);
         else if (g.out_dt == MOE_BF16) store_from_f32<kBF16>(g.out, o, v);
@@ -399,13 +415,20 @@ b16_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
     }
 }
 
-int slot_launch(hipStream_t st, bool f16, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
-    const int64_t groups = ceil_div(g.N, kSlotCols * kSlotWaves);
+template <bool F16, int COLS, int UNROLL>
+int slot_launch_cols(hipStream_t st, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
+    const int64_t groups = ceil_div(g.N, COLS * kSlotWaves);
     if (groups * g.m_rows > 0x7FFFFFFF) return MOE_ERR_SHAPE;
-    const dim3 grid((unsigned)(groups * g.m_rows)), block(64 * kSlotWaves);
-    if (f16) hipLaunchKernelGGL((b16_slot_kernel<true>), grid, block, 0, st, g, slots, a_row_div, (int)groups);
-    else hipLaunchKernelGGL((b16_slot_kernel<false>), grid, block, 0, st, g, slots, a_row_div, (int)groups);
+    hipLaunchKernelGGL((b16_slot_kernel<F16, COLS, UNROLL>), dim3((unsigned)(groups * g.m_rows)), dim3(64 * kSlotWaves), 0, st, g,
+                       slots, a_row_div, (int)groups);
     return launch_status();
+}
+
+// Up to 1024 k a row is two chunks, so a wave takes four columns of them; beyond, two columns of four chunks.
+int slot_launch(hipStream_t st, bool f16, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
+    if (g.K <= 1024)
+        return f16 ? slot_launch_cols<true, 4, 2>(st, g, slots, a_row_div) : slot_launch_cols<false, 4, 2>(st, g, slots, a_row_div);
+    return f16 ? slot_launch_cols<true, 2, 4>(st, g, slots, a_row_div) : slot_launch_cols<false, 2, 4>(st, g, slots, a_row_div);
 }
 
 }  // namespace b16
