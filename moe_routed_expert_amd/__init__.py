@@ -120,8 +120,11 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.float16: MOE_F16}
+
+
 def _dt(t: torch.Tensor) -> int:
-    return {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.float16: MOE_F16}[t.dtype]
+    return _DT[t.dtype]
 
 
 def _rowstride(t: torch.Tensor) -> int:
@@ -354,8 +357,15 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _rows(t):
+    """Row stride of a 2-D tensor with unit column stride."""
+    r, c = t.stride()
+    assert c == 1, "unit column stride expected"
+    return r
+
+
 def _i32(t, n, what):
-    assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n, "%s: %d contiguous int32 expected" % (what, n)
+    assert t.dtype is torch.int32 and t.numel() == n and t.is_contiguous(), "%s: %d contiguous int32 expected" % (what, n)
 
 
 def b16_grouped_gemm(a, w, out, *, mode, expert_offsets=None, slot_ids=None, m_rows=None, a_row_div=1,
@@ -363,19 +373,24 @@ def b16_grouped_gemm(a, w, out, *, mode, expert_offsets=None, slot_ids=None, m_r
     """16-bit grouped GEMM: out[r] = a[r] @ w[e].T with w [E, N, K], or a[r] @ w[e] with w [E, K, N] when w_trans
     (the data gradient of a layer whose forward used the same bank).  a [rows, K] and w bf16 or fp16, out
     [rows, N] bf16, fp16 or fp32; rows by expert_offsets [E+1] (grouped) or slot_ids [m_rows] (slot mode)."""
-    E, K, N = w.shape if w_trans else (w.shape[0], w.shape[2], w.shape[1])
-    rows = out.shape[0] if m_rows is None else m_rows
-    assert a.dtype == w.dtype and a.shape[1] == K and out.shape[1] == N and w.stride(2) == 1, "operands do not match"
-    assert 0 <= rows <= out.shape[0], "m_rows exceeds out"
+    E, N, K = w.shape
+    if w_trans:
+        N, K = K, N
+    se, sr, sc = w.stride()
+    a_rows, a_cols = a.shape
+    o_rows, o_cols = out.shape
+    rows = o_rows if m_rows is None else m_rows
+    assert a.dtype is w.dtype and a_cols == K and o_cols == N and sc == 1, "operands do not match"
+    assert 0 <= rows <= o_rows, "m_rows exceeds out"
     if mode == MOE_MODE_SLOT:
         _i32(slot_ids, rows, "slot_ids")
-        assert a.shape[0] * a_row_div >= rows, "a has too few rows"
+        assert a_rows * a_row_div >= rows, "a has too few rows"
     else:
         _i32(expert_offsets, E + 1, "expert_offsets")
-        assert a.shape[0] >= rows, "a has too few rows"
+        assert a_rows >= rows, "a has too few rows"
     _call("moe_b16_grouped_gemm", (a, w, out, expert_offsets, slot_ids), (
-        a.data_ptr(), _rowstride(a), w.data_ptr(), w.stride(0), w.stride(1), E, N, K, _dt(a), int(w_trans), mode,
-        _addr(expert_offsets), _addr(slot_ids), rows, a_row_div, out.data_ptr(), _dt(out), _rowstride(out)), stream)
+        a.data_ptr(), _rows(a), w.data_ptr(), se, sr, E, N, K, _dt(a), int(w_trans), mode,
+        _addr(expert_offsets), _addr(slot_ids), rows, a_row_div, out.data_ptr(), _dt(out), _rows(out)), stream)
 
 
 def b16_grouped_tile(m_rows, n_experts, N, K):
@@ -411,8 +426,8 @@ def b16_grouped_wgrad(dy, a, expert_offsets, dw, *, a_s=None, m_rows=None, accum
     if workspace is not None:
         assert workspace.is_contiguous() and workspace.element_size() == 1, "workspace: contiguous bytes"
     _call("moe_b16_grouped_wgrad", (dy, a, a_s, expert_offsets, dw, workspace), (
-        dy.data_ptr(), _rowstride(dy), _dt(dy), a.data_ptr(), _rowstride(a), MOE_E4M3 if saved else _dt(a), _addr(a_s),
-        _rowstride(a_s) if saved else 0, expert_offsets.data_ptr(), E, N, K, rows, dw.data_ptr(), _dt(dw), dw.stride(0),
+        dy.data_ptr(), _rows(dy), _dt(dy), a.data_ptr(), _rows(a), MOE_E4M3 if saved else _dt(a), _addr(a_s),
+        _rows(a_s) if saved else 0, expert_offsets.data_ptr(), E, N, K, rows, dw.data_ptr(), _dt(dw), dw.stride(0),
         dw.stride(1), int(accumulate), _addr(workspace), workspace.numel() if workspace is not None else 0), stream)
 
 
@@ -424,11 +439,11 @@ def act_checkpoint(x, out_q, out_s, act=MOE_ACT_IDENTITY, h=None, stream=None):
     both = 1 if act == MOE_ACT_IDENTITY else 2
     assert width == both * n, "gate and up of one width expected"
     assert out_q.dtype == torch.uint8 and out_s.dtype == torch.float32, "codes are uint8, scales float32"
-    assert tuple(out_q.shape) == (rows, width) and tuple(out_s.shape) == (rows, both * ((n + 127) // 128)), "outputs do not match"
-    assert h is None or (h.dtype == x.dtype and tuple(h.shape) == (rows, n)), "h does not match"
+    assert out_q.shape == (rows, width) and out_s.shape == (rows, both * ((n + 127) // 128)), "outputs do not match"
+    assert h is None or (h.dtype == x.dtype and h.shape == (rows, n)), "h does not match"
     _call("moe_act_checkpoint", (x, out_q, out_s, h), (
-        x.data_ptr(), _dt(x), _rowstride(x), rows, n, act, out_q.data_ptr(), _rowstride(out_q), out_s.data_ptr(),
-        _rowstride(out_s), _addr(h), _rowstride(h) if h is not None else 0), stream)
+        x.data_ptr(), _dt(x), _rows(x), rows, n, act, out_q.data_ptr(), _rows(out_q), out_s.data_ptr(),
+        _rows(out_s), _addr(h), _rows(h) if h is not None else 0), stream)
 
 
 def gated_act_backward(dh, q, s, dx, act=MOE_ACT_SILU_MUL, h=None, stream=None):
@@ -436,12 +451,12 @@ def gated_act_backward(dh, q, s, dx, act=MOE_ACT_SILU_MUL, h=None, stream=None):
     and h [rows, n] again when given.  dh, dx, h of one type."""
     rows, n = dh.shape
     assert q.dtype == torch.uint8 and s.dtype == torch.float32, "codes are uint8, scales float32"
-    assert tuple(q.shape) == (rows, 2 * n) and tuple(s.shape) == (rows, 2 * ((n + 127) // 128)), "saved rows do not match"
-    assert dx.dtype == dh.dtype and tuple(dx.shape) == (rows, 2 * n), "dx does not match"
-    assert h is None or (h.dtype == dh.dtype and tuple(h.shape) == (rows, n)), "h does not match"
+    assert q.shape == (rows, 2 * n) and s.shape == (rows, 2 * ((n + 127) // 128)), "saved rows do not match"
+    assert dx.dtype == dh.dtype and dx.shape == (rows, 2 * n), "dx does not match"
+    assert h is None or (h.dtype == dh.dtype and h.shape == (rows, n)), "h does not match"
     _call("moe_gated_act_backward", (dh, q, s, dx, h), (
-        dh.data_ptr(), _dt(dh), _rowstride(dh), q.data_ptr(), _rowstride(q), s.data_ptr(), _rowstride(s), rows, n, act,
-        dx.data_ptr(), _rowstride(dx), _addr(h), _rowstride(h) if h is not None else 0), stream)
+        dh.data_ptr(), _dt(dh), _rows(dh), q.data_ptr(), _rows(q), s.data_ptr(), _rows(s), rows, n, act,
+        dx.data_ptr(), _rows(dx), _addr(h), _rows(h) if h is not None else 0), stream)
 
 
 def topk_reduce_backward(dout, y, slot_ids, weights, dy, dweights=None, route_rows=None, stream=None):
@@ -450,7 +465,7 @@ def topk_reduce_backward(dout, y, slot_ids, weights, dy, dweights=None, route_ro
     T, topk = slot_ids.shape
     rows, H = dy.shape
     _i32(slot_ids, T * topk, "slot_ids")
-    assert dout.dtype == torch.bfloat16 and tuple(dout.shape) == (T, H), "dout: [T, H] bfloat16"
+    assert dout.dtype == torch.bfloat16 and dout.shape == (T, H), "dout: [T, H] bfloat16"
     assert weights.dtype == torch.float32 and weights.is_contiguous() and weights.shape == slot_ids.shape, "weights do not match"
     assert dweights is None or (dweights.dtype == torch.float32 and dweights.is_contiguous() and
                                 dweights.shape == slot_ids.shape), "dweights do not match"
@@ -460,8 +475,8 @@ def topk_reduce_backward(dout, y, slot_ids, weights, dy, dweights=None, route_ro
     else:
         assert rows >= T * topk, "a row for every route expected"
     _call("moe_topk_reduce_backward", (dout, y if y is not None else dout, slot_ids, route_rows, weights, dy, dweights), (
-        dout.data_ptr(), _rowstride(dout), _addr(y), _dt(dy), _rowstride(y) if y is not None else 0, rows,
-        slot_ids.data_ptr(), _addr(route_rows), weights.data_ptr(), T, topk, H, dy.data_ptr(), _rowstride(dy),
+        dout.data_ptr(), _rows(dout), _addr(y), _dt(dy), _rows(y) if y is not None else 0, rows,
+        slot_ids.data_ptr(), _addr(route_rows), weights.data_ptr(), T, topk, H, dy.data_ptr(), _rows(dy),
         _addr(dweights)), stream)
 
 
@@ -474,4 +489,4 @@ def route_prep_backward(expert_ids, weights, dweights, dlogits, stream=None):
     assert dlogits.dtype == torch.float32 and dlogits.shape[0] == T, "dlogits: [T, E] float32"
     _call("moe_route_prep_backward", (expert_ids, weights, dweights, dlogits), (
         expert_ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), T, dlogits.shape[1], topk, dlogits.data_ptr(),
-        _rowstride(dlogits)), stream)
+        _rows(dlogits)), stream)
