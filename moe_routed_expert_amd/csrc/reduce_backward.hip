@@ -8,6 +8,8 @@
 // dout is read once per P routes and y and dy once.  P is 8, or 1 for few tokens, where a workgroup per route
 // fills more of the chip.  The dot products are summed in fp32: 8 columns at a time per thread, then lanes by
 // shuffles, then waves through LDS, always in the same order.
+#include <algorithm>
+
 #include "cols8.h"
 #include "host.h"
 
@@ -15,6 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMaxBlocks = 1 << 23;           // a grid's threads fit 32 bits; workgroups take more items in turn
 
 struct BackArgs {
     const uint16_t* dout;
@@ -35,66 +38,70 @@ __global__ void __launch_bounds__(kThreads) topk_reduce_backward_kernel(const Ba
     __shared__ float part[kThreads / kWave][P];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int64_t passes = ceil_div(a.topk, P);
-    const int64_t t = blockIdx.x / (unsigned)passes, j0 = (blockIdx.x % (unsigned)passes) * P;
-    // per route: its row (-1: none to write), and its weight; an inactive route's weight and y are not read
-    int64_t row[P];
-    bool on[P];
-    float w[P], dot[P];
-#pragma unroll
-    for (int u = 0; u < P; u++) {
-        const int64_t rt = t * a.topk + j0 + u;
-        const bool in = j0 + u < a.topk;
-        on[u] = in && a.slots[in ? rt : 0] >= 0;
-        row[u] = -1;
-        if (a.route_rows) {
-            if (on[u]) row[u] = a.route_rows[rt];
-        } else if (in) {
-            row[u] = rt;
-        }
-        if (row[u] >= a.y_rows) row[u] = -1;
-        on[u] = on[u] && row[u] >= 0;
-        w[u] = on[u] ? a.weights[rt] : 0.0f;
-        dot[u] = 0.0f;
-    }
-    for (int64_t c = (int64_t)tid * kCols; c < a.H; c += kThreads * kCols) {
-        const int valid = (int)(a.H - c < kCols ? a.H - c : kCols);
-        float d[kCols];
-        load_cols<kBF16, VEC>(a.dout, t * a.dout_stride + c, valid, d);
+    for (int64_t item = blockIdx.x; item < a.T * passes; item += gridDim.x) {
+        const int64_t t = item / passes, j0 = item % passes * P;
+        // per route: its row (-1: none to write), and its weight; an inactive route's weight and y are not read
+        int64_t row[P];
+        bool on[P];
+        float w[P], dot[P];
 #pragma unroll
         for (int u = 0; u < P; u++) {
-            if (on[u] && a.dweights) {
-                float y[kCols];
-                load_cols<DT, VEC>(a.y, row[u] * a.y_stride + c, valid, y);
-#pragma unroll
-                for (int i = 0; i < kCols; i++) dot[u] = __builtin_fmaf(d[i], y[i], dot[u]);
+            const int64_t rt = t * a.topk + j0 + u;
+            const bool in = j0 + u < a.topk;
+            on[u] = in && a.slots[in ? rt : 0] >= 0;
+            row[u] = -1;
+            if (a.route_rows) {
+                if (on[u]) row[u] = a.route_rows[rt];
+            } else if (in) {
+                row[u] = rt;
             }
-            if (row[u] >= 0) {
-                float o[kCols];
+            if (row[u] >= a.y_rows) row[u] = -1;
+            on[u] = on[u] && row[u] >= 0;
+            w[u] = on[u] ? a.weights[rt] : 0.0f;
+            dot[u] = 0.0f;
+        }
+        for (int64_t c = (int64_t)tid * kCols; c < a.H; c += kThreads * kCols) {
+            const int valid = (int)(a.H - c < kCols ? a.H - c : kCols);
+            float d[kCols];
+            load_cols<kBF16, VEC>(a.dout, t * a.dout_stride + c, valid, d);
 #pragma unroll
-                for (int i = 0; i < kCols; i++) o[i] = on[u] ? w[u] * d[i] : 0.0f;
-                store_cols<DT, VEC>(a.dy, row[u] * a.dy_stride + c, valid, o);
+            for (int u = 0; u < P; u++) {
+                if (on[u] && a.dweights) {
+                    float y[kCols];
+                    load_cols<DT, VEC>(a.y, row[u] * a.y_stride + c, valid, y);
+#pragma unroll
+                    for (int i = 0; i < kCols; i++) dot[u] = __builtin_fmaf(d[i], y[i], dot[u]);
+                }
+                if (row[u] >= 0) {
+                    float o[kCols];
+#pragma unroll
+                    for (int i = 0; i < kCols; i++) o[i] = on[u] ? w[u] * d[i] : 0.0f;
+                    store_cols<DT, VEC>(a.dy, row[u] * a.dy_stride + c, valid, o);
+                }
             }
         }
-    }
-    if (!a.dweights) return;
+        if (!a.dweights) continue;
 #pragma unroll
-    for (int u = 0; u < P; u++) {
+        for (int u = 0; u < P; u++) {
 #pragma unroll
-        for (int m = 32; m > 0; m >>= 1) dot[u] += __shfl_xor(dot[u], m, kWave);
-        if (lane == 0) part[wave][u] = dot[u];
-    }
-    __syncthreads();
-    if (tid < P && j0 + tid < a.topk) {
-        float sum = part[0][tid];
+            for (int m = 32; m > 0; m >>= 1) dot[u] += __shfl_xor(dot[u], m, kWave);
+            if (lane == 0) part[wave][u] = dot[u];
+        }
+        __syncthreads();
+        if (tid < P && j0 + tid < a.topk) {
+            float sum = part[0][tid];
 #pragma unroll
-        for (int i = 1; i < kThreads / kWave; i++) sum += part[i][tid];
-        a.dweights[t * a.topk + j0 + tid] = sum;
+            for (int i = 1; i < kThreads / kWave; i++) sum += part[i][tid];
+            a.dweights[t * a.topk + j0 + tid] = sum;
+        }
+        __syncthreads();                                   // part is read before the next item writes it
     }
 }
 
 template <int DT, int P>
 void launch_back(hipStream_t st, bool vec, const BackArgs& a) {
-    const dim3 grid((unsigned)(a.T * ceil_div(a.topk, P))), block(kThreads);
+    const int64_t items = a.T * ceil_div(a.topk, P);
+    const dim3 grid((unsigned)(items < kMaxBlocks ? items : kMaxBlocks)), block(kThreads);
     if (vec) hipLaunchKernelGGL((topk_reduce_backward_kernel<DT, P, true>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((topk_reduce_backward_kernel<DT, P, false>), grid, block, 0, st, a);
 }
@@ -112,23 +119,23 @@ route_prep_backward_kernel(const int32_t* __restrict__ ids, const float* __restr
                            const float* __restrict__ dweights, int64_t T, int E, int topk, float* __restrict__ dlogits,
                            int64_t stride) {
     const int lane = threadIdx.x & (kWave - 1);
-    const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-    if (t >= T) return;
-    const bool in = lane < topk;
-    const float w = in ? weights[t * topk + lane] : 0.0f, dw = in ? dweights[t * topk + lane] : 0.0f;
-    const int id = in ? ids[t * topk + lane] : -1;
-    float mean = in ? w * dw : 0.0f;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; t < T; t += (int64_t)gridDim.x * 4) {
+        const bool in = lane < topk;
+        const float w = in ? weights[t * topk + lane] : 0.0f, dw = in ? dweights[t * topk + lane] : 0.0f;
+        const int id = in ? ids[t * topk + lane] : -1;
+        float mean = in ? w * dw : 0.0f;
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) mean += __shfl_xor(mean, m, kWave);
-    const float g = w * (dw - mean);
-    for (int e = lane; e < E + kWave - 1 - (E + kWave - 1) % kWave; e += kWave) {
-        float v = 0.0f;
-        for (int j = 0; j < topk; j++) {
-            const int idj = __builtin_amdgcn_readlane(id, j);
-            const float gj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g), j));
-            if (idj == e) v += gj;
+        for (int m = 32; m > 0; m >>= 1) mean += __shfl_xor(mean, m, kWave);
+        const float g = w * (dw - mean);
+        for (int e = lane; e < E + kWave - 1 - (E + kWave - 1) % kWave; e += kWave) {
+            float v = 0.0f;
+            for (int j = 0; j < topk; j++) {
+                const int idj = __builtin_amdgcn_readlane(id, j);
+                const float gj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g), j));
+                if (idj == e) v += gj;
+            }
+            if (e < E) dlogits[t * stride + e] = v;
         }
-        if (e < E) dlogits[t * stride + e] = v;
     }
 }
 
@@ -167,7 +174,7 @@ extern "C" int moe_route_prep_backward(const int32_t* expert_ids, const float* w
     if (T == 0) return MOE_OK;
     if (!expert_ids || !weights || !dweights || !dlogits) return MOE_ERR_NULL;
     if (dlogits_stride < E) return MOE_ERR_SHAPE;
-    hipLaunchKernelGGL(route_prep_backward_kernel, dim3((unsigned)ceil_div(T, 4)), dim3(256), 0, as_stream(stream),
+    hipLaunchKernelGGL(route_prep_backward_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(T, 4), kMaxBlocks)), dim3(256), 0, as_stream(stream),
                        expert_ids, weights, dweights, T, (int)E, (int)topk, dlogits, dlogits_stride);
     return launch_status();
 }

@@ -289,6 +289,26 @@ def test_offsets_beyond_m_rows_are_clamped():
     assert bool((out[25:] == 9).all())
 
 
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("mode", ["forward", "trans", "slot"])
+def test_subnormal_operands_count(dt, mode):
+    """Values below a type's normal range (common among fp16 gradients) are not flushed."""
+    tiny = {FP: 2.0 ** -20, BF: 2.0 ** -130}[dt]
+    K, N = 200, 72
+    a = torch.full((40, K), tiny, dtype=dt)
+    w = randn((2, K, N) if mode == "trans" else (2, N, K), dt, 1).sign() * {FP: 1.0, BF: 2.0 ** 20}[dt]
+    out = torch.empty((40, N), dtype=F32, device=dev())
+    if mode == "slot":
+        slots = np.arange(40, dtype=np.int32) % 2
+        m.b16_grouped_gemm(a.to(dev()), w.to(dt).to(dev()), out, mode=m.MOE_MODE_SLOT, slot_ids=to_dev(slots))
+        ref, _ = tr.slot_gemm(f64(a), f64(w), slots, 1)
+    else:
+        m.b16_grouped_gemm(a.to(dev()), w.to(dt).to(dev()), out, mode=m.MOE_MODE_GROUPED, expert_offsets=to_dev(offsets_of([25, 15])),
+                           w_trans=mode == "trans")
+        ref, _ = tr.grouped_gemm(f64(a), f64(w), [0, 25, 40], mode == "trans")
+    assert np.array_equal(f64(out), ref)                   # sums of a few equal powers of two: exact
+
+
 def test_binding_checks():
     a, w = torch.zeros((4, 64), dtype=BF, device=dev()), torch.zeros((2, 32, 64), dtype=BF, device=dev())
     out, offs = torch.zeros((4, 32), dtype=BF, device=dev()), torch.zeros(3, dtype=torch.int32, device=dev())

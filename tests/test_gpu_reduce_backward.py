@@ -127,6 +127,25 @@ def test_route_backward_odd_ids():
     assert np.array_equal(f64(out), ref)                   # sums of powers of two: exact
 
 
+def test_more_items_than_a_grid_holds():
+    """More tokens than workgroups of one launch: they are taken in turn."""
+    T, H = (1 << 23) + 5, 8
+    dout = torch.ones((T, H), dtype=BF, device=dev())
+    y = torch.full((T, H), 0.5, dtype=BF, device=dev())
+    slots = torch.zeros((T, 1), dtype=torch.int32, device=dev())
+    w = (torch.arange(T, device=dev()) % 7).float()[:, None].contiguous()
+    dy, dw = torch.empty_like(y), torch.empty_like(w)
+    m.topk_reduce_backward(dout, y, slots, w, dy, dw)
+    assert bool((dw == 4).all()) and bool((dy.float() == w).all())
+    del dout, y, dy
+    T = (1 << 25) + 3
+    ids = torch.zeros((T, 1), dtype=torch.int32, device=dev())
+    w, dw = torch.full((T, 1), 0.5, device=dev()), (torch.arange(T, device=dev()) % 9).float()[:, None].contiguous()
+    out = torch.full((T, 1), float("nan"), device=dev())
+    m.route_prep_backward(ids, w, dw, out)
+    assert bool((out == 0.25 * dw).all())
+
+
 def test_graph_replay():
     T, k, H, E = 12, 4, 264, 16
     dout, y, slots, w, rows = reduce_case(T, k, H, BF, 3, mapped=True)

@@ -27,7 +27,7 @@ def gemm(**kw):
     (dict(m_rows=2 ** 31), m.MOE_ERR_SHAPE), (dict(n_experts=0), m.MOE_ERR_SHAPE), (dict(n_experts=1025), m.MOE_ERR_SHAPE),
     (dict(n_experts=-1), m.MOE_ERR_SHAPE), (dict(out=None), m.MOE_ERR_NULL), (dict(a=None), m.MOE_ERR_NULL),
     (dict(w=None), m.MOE_ERR_NULL), (dict(expert_offsets=None), m.MOE_ERR_NULL),
-    (dict(mode=1, slot_ids=None), m.MOE_ERR_NULL), (dict(mode=1, a_row_div=0), m.MOE_ERR_SHAPE),
+    (dict(mode=1, m_rows=2 ** 24), m.MOE_ERR_SHAPE), (dict(mode=1, slot_ids=None), m.MOE_ERR_NULL), (dict(mode=1, a_row_div=0), m.MOE_ERR_SHAPE),
     (dict(a_stride=248), m.MOE_ERR_SHAPE), (dict(w_stride_r=248), m.MOE_ERR_SHAPE),
     (dict(w_stride_e=128 * 256 - 8), m.MOE_ERR_SHAPE), (dict(out_stride=120), m.MOE_ERR_SHAPE),
     (dict(w_trans=1, w_stride_r=120), m.MOE_ERR_SHAPE), (dict(w_trans=1, w_stride_r=128, w_stride_e=255 * 128), m.MOE_ERR_SHAPE),
