@@ -10,22 +10,41 @@ namespace moe {
 
 constexpr int kCols = 8;
 
+// The eight columns as loaded, so that several rows can be asked for before the first is used.
+template <int DT>
+struct RawCols8 {
+    uint4 w[DT == kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* __restrict__ base, int64_t off) {
+        const uint4* p = reinterpret_cast<const uint4*>((const char*)base + off * (DT == kF32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < (DT == kF32 ? 2 : 1); i++) w[i] = p[i];
+    }
+    __device__ __forceinline__ void get(float (&v)[kCols]) const {
+        const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+        if constexpr (DT == kF32) {
+            const uint32_t b[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[i] = __uint_as_float(a[i]);
+                v[4 + i] = __uint_as_float(b[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint16_t lo = (uint16_t)(a[i] & 0xFFFFu), hi = (uint16_t)(a[i] >> 16);
+                v[2 * i] = DT == kBF16 ? bf16_to_f32(lo) : f16_to_f32(lo);
+                v[2 * i + 1] = DT == kBF16 ? bf16_to_f32(hi) : f16_to_f32(hi);
+            }
+        }
+    }
+};
+
 template <int DT, bool VEC>
 __device__ __forceinline__ void load_cols(const void* __restrict__ base, int64_t off, int valid, float (&v)[kCols]) {
-    if constexpr (VEC && DT == kF32) {
-        const v4f a = *reinterpret_cast<const v4f*>((const float*)base + off);
-        const v4f b = *reinterpret_cast<const v4f*>((const float*)base + off + 4);
-#pragma unroll
-        for (int i = 0; i < 4; i++) { v[i] = a[i]; v[4 + i] = b[i]; }
-    } else if constexpr (VEC) {
-        const uint4 r = *reinterpret_cast<const uint4*>((const uint16_t*)base + off);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint16_t lo = (uint16_t)(w[i] & 0xFFFFu), hi = (uint16_t)(w[i] >> 16);
-            v[2 * i] = DT == kBF16 ? bf16_to_f32(lo) : f16_to_f32(lo);
-            v[2 * i + 1] = DT == kBF16 ? bf16_to_f32(hi) : f16_to_f32(hi);
-        }
+    if constexpr (VEC) {
+        RawCols8<DT> r;
+        r.load(base, off);
+        r.get(v);
     } else {
 #pragma unroll
         for (int i = 0; i < kCols; i++) v[i] = i < valid ? load_as_f32<DT>(base, off + i) : 0.0f;

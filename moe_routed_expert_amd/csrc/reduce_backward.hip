@@ -4,9 +4,11 @@
 // w_j = softmax over the top-k logits gives dlogits[id_j] = w_j (dw_j - sum_i w_i dw_i), zero elsewhere.
 //
 // MI355X design: HBM-bound.  A workgroup takes one token and up to P of its routes: each thread holds 8
-// columns of dout in registers and, route by route, reads y, adds to that route's dot product and writes dy, so
-// dout is read once per P routes and y and dy once.  P is 8, or 1 for few tokens, where a workgroup per route
-// fills more of the chip.  The dot products are summed in fp32: 8 columns at a time per thread, then lanes by
+// columns of dout in registers, asks for the routes' y and then, route by route, adds to that route's dot product
+// and writes dy, so y and dy move once and dout once per P routes (from L2 after the first).  P is 2: at 4096
+// tokens, six routes and 4096 bf16 columns 2 took 91 us (4.8 TB/s, of a copy's 4.9), 1 94 us and 8, with a quarter
+// of the workgroups, 98 us.  Below 1024 tokens P is 1, a workgroup per route, which fills more of the chip.  The dot
+// products are summed in fp32: 8 columns at a time per thread, then lanes by
 // shuffles, then waves through LDS, always in the same order.
 #include <algorithm>
 
@@ -63,12 +65,19 @@ __global__ void __launch_bounds__(kThreads) topk_reduce_backward_kernel(const Ba
         for (int64_t c = (int64_t)tid * kCols; c < a.H; c += kThreads * kCols) {
             const int valid = (int)(a.H - c < kCols ? a.H - c : kCols);
             float d[kCols];
+            RawCols8<DT> raw[P];
+            if constexpr (VEC) {                           // every route's y is on its way before the first is used
+#pragma unroll
+                for (int u = 0; u < P; u++)
+                    if (on[u] && a.dweights) raw[u].load(a.y, row[u] * a.y_stride + c);
+            }
             load_cols<kBF16, VEC>(a.dout, t * a.dout_stride + c, valid, d);
 #pragma unroll
             for (int u = 0; u < P; u++) {
                 if (on[u] && a.dweights) {
                     float y[kCols];
-                    load_cols<DT, VEC>(a.y, row[u] * a.y_stride + c, valid, y);
+                    if constexpr (VEC) raw[u].get(y);
+                    else load_cols<DT, false>(a.y, row[u] * a.y_stride + c, valid, y);
 #pragma unroll
                     for (int i = 0; i < kCols; i++) dot[u] = __builtin_fmaf(d[i], y[i], dot[u]);
                 }
@@ -109,7 +118,7 @@ void launch_back(hipStream_t st, bool vec, const BackArgs& a) {
 template <int DT>
 void launch_back_p(hipStream_t st, bool few, bool vec, const BackArgs& a) {
     if (few) launch_back<DT, 1>(st, vec, a);
-    else launch_back<DT, 8>(st, vec, a);
+    else launch_back<DT, 2>(st, vec, a);
 }
 
 // One wave per token: lane j holds route j's id and g_j = w_j (dw_j - sum_i w_i dw_i); every lane then writes
