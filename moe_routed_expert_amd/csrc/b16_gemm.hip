@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     // and last ones of more and of at most BP / 2 rows.  (Not by_size: all of them are of the first kind.)
     __shared__ int first_row[kMaxExperts + 1], first_whole[kMaxExperts + 1];
     __shared__ uint16_t first_long[kMaxExperts + 1], first_short[kMaxExperts + 1];
-    __shared__ int wave_sum[2][C::NW];
+    __shared__ int wave_sum[2 * C::NW];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
             sum_w += whole[i];
             sum_l += last[i];
         }
-        int w = block_exclusive_scan<C::NW>(sum_w, wave_sum[0], lane, wave);
-        int l = block_exclusive_scan<C::NW>(sum_l, wave_sum[1], lane, wave);
+        int w = sum_w, l = sum_l;
+        block_exclusive_scan2<C::NW>(w, l, wave_sum, lane, wave);
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
@@ -122,19 +122,12 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
         // the last expert whose first tile of the kind is <= its number: the tile's expert
         const bool whole = mt < whole_tiles, is_long = mt < whole_tiles + long_tiles;
         const int k = whole ? mt : mt - whole_tiles - (is_long ? 0 : long_tiles);
-        auto first = [&](int e) {
-            return __builtin_amdgcn_readfirstlane(whole ? first_whole[e] : is_long ? (int)first_long[e] : (int)first_short[e]);
-        };
-        int lo = 0, hi = E - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (first(mid) <= k) lo = mid;
-            else hi = mid - 1;
-        }
+        auto first = [&](int e) { return whole ? first_whole[e] : is_long ? (int)first_long[e] : (int)first_short[e]; };
+        const int lo = last_at_most(first, E, k, lane);
         Tile ti;
         ti.expert = lo;
         const int from = __builtin_amdgcn_readfirstlane(first_row[lo]), end = __builtin_amdgcn_readfirstlane(first_row[lo + 1]);
-        ti.row0 = whole ? from + (k - first(lo)) * C::BP : end - (end - from) % C::BP;
+        ti.row0 = whole ? from + (k - __builtin_amdgcn_readfirstlane(first(lo))) * C::BP : end - (end - from) % C::BP;
         ti.rows = min(end - ti.row0, C::BP);
         ti.n0 = nt * C::BQ;
         return ti;

@@ -87,20 +87,42 @@ __device__ __forceinline__ v4f mfma16x16x32(v8s a, v8s b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Exclusive scan of one int per thread over a block of NW waves (sums: NW ints of LDS).
+// Exclusive scans of a and b (one int of each per thread) over a block of NW waves; sums: 2 NW ints of LDS.
 template <int NW>
-__device__ __forceinline__ int block_exclusive_scan(int v, int* sums, int lane, int wave) {
-    int x = v;
+__device__ __forceinline__ void block_exclusive_scan2(int& a, int& b, int* sums, int lane, int wave) {
+    int x = a, y = b;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
-        const int y = __shfl_up(x, d, kWave);
-        if (lane >= d) x += y;
+        const int u = __shfl_up(x, d, kWave), v = __shfl_up(y, d, kWave);
+        if (lane >= d) {
+            x += u;
+            y += v;
+        }
     }
-    if (lane == kWave - 1) sums[wave] = x;
+    if (lane == kWave - 1) {
+        sums[wave] = x;
+        sums[NW + wave] = y;
+    }
     __syncthreads();
-    x -= v;
-    for (int w = 0; w < wave; w++) x += sums[w];
-    return x;
+    a = x - a;
+    b = y - b;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+        a += w < wave ? sums[w] : 0;
+        b += w < wave ? sums[NW + w] : 0;
+    }
+}
+
+// The largest i < n with value(i) <= k, for a non-decreasing table of at most 1024 entries with value(0) <= k: two
+// reads of the table by the whole wave, where a binary search would take ten in a row.
+template <class F>
+__device__ __forceinline__ int last_at_most(const F& value, int n, int k, int lane) {
+    const int i = lane * 16;
+    const uint64_t blocks = __ballot(i < n && value(i < n ? i : 0) <= k);
+    const int b = __popcll(blocks) - 1;
+    const int j = b * 16 + (lane & 15);
+    const uint64_t in = __ballot(j < n && value(j < n ? j : 0) <= k) & 0xFFFFu;
+    return __builtin_amdgcn_readfirstlane(b * 16 + __popcll(in) - 1);
 }
 
 // T rows of an operand whose k is contiguous, staged by NW waves.  Row r's 16-byte piece c sits at slot

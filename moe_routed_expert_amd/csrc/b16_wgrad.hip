@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
     __shared__ int first_row[kMaxExperts + 1], first_chunk[kMaxExperts + 1];   // offsets, clamped to [0, m_rows]
-    __shared__ int wave_sum[C::NW];
+    __shared__ int wave_sum[2 * C::NW];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
             n[i] = e < g.n_experts ? (max(first_row[e + 1] - first_row[e], 0) + g.chunk_rows - 1) / g.chunk_rows : 0;
             sum += n[i];
         }
-        int before = block_exclusive_scan<C::NW>(sum, wave_sum, lane, wave);
+        int before = sum, none = 0;
+        block_exclusive_scan2<C::NW>(before, none, wave_sum, lane, wave);
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
@@ -152,12 +153,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
         ti.n0 = (panel * kPanel + t - kt * height) * C::BP;
         int expert = ti.chunk, from = 0;
         if (g.chunk_rows > 0) {                        // the last expert whose first chunk is <= this one
-            int lo = 0, hi = g.n_experts - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (__builtin_amdgcn_readfirstlane(first_chunk[mid]) <= ti.chunk) lo = mid;
-                else hi = mid - 1;
-            }
+            const int lo = last_at_most([&](int e) { return first_chunk[e]; }, g.n_experts, ti.chunk, lane);
             expert = lo;
             from = (ti.chunk - __builtin_amdgcn_readfirstlane(first_chunk[lo])) * g.chunk_rows;
         }
