@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
                 const int rest = g.by_size ? (hi - lo) % C::BP : 0;
                 first_row[e] = lo;
                 if (e == E - 1) first_row[E] = hi;
-                whole[i] = (hi - lo - rest + C::BP - 1) / C::BP;
+                whole[i] = pieces(hi - lo - rest, C::BP);
                 last[i] = rest > C::BP / 2 ? 1 : rest > 0 ? 1 << 16 : 0;
             }
             sum_w += whole[i];

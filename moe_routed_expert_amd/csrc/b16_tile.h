@@ -45,6 +45,9 @@ struct Cfg {
     static constexpr int WAVES_PER_EU = NW * WGS_ / 4;
 };
 
+// ceil(rows / size): up to 2^31 - 1 rows, whose rounded-up sum passes an int.
+__host__ __device__ __forceinline__ int pieces(int rows, int size) { return (int)(((unsigned)rows + (unsigned)size - 1) / (unsigned)size); }
+
 static __device__ const uint4 kZeroPiece = {0u, 0u, 0u, 0u};
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {

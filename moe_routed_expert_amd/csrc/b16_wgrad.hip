@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
-            n[i] = e < g.n_experts ? (max(first_row[e + 1] - first_row[e], 0) + g.chunk_rows - 1) / g.chunk_rows : 0;
+            n[i] = e < g.n_experts ? pieces(max(first_row[e + 1] - first_row[e], 0), g.chunk_rows) : 0;
             sum += n[i];
         }
         int before = sum, none = 0;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
         return ti;
     };
     // an expert without rows still takes one step, of zeros, so that its tiles are stored
-    auto steps_of = [&](const Tile& ti) { return max(1, (ti.rows + kStep - 1) / kStep); };
+    auto steps_of = [&](const Tile& ti) { return max(1, pieces(ti.rows, kStep)); };
 
     // Producer, as in b16_gemm_kernel: past the last tile it goes on with zeros (prod_rows = 0).
     const uint32_t lds = lds_offset(ring);
@@ -277,7 +277,7 @@ wgrad_join_kernel(const float* __restrict__ part, const int32_t* __restrict__ of
     const int e = blockIdx.y, tid = threadIdx.x;
     auto chunks_of = [&](int x) {
         const int lo = min(max(offsets[x], 0), m_rows), hi = min(max(offsets[x + 1], 0), m_rows);
-        return (max(hi - lo, 0) + chunk_rows - 1) / chunk_rows;
+        return pieces(max(hi - lo, 0), chunk_rows);
     };
     int before = 0;
     for (int x = tid; x < e; x += 256) before += chunks_of(x);

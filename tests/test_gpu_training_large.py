@@ -61,6 +61,37 @@ def test_bank_and_gradient():
     assert bool((dw[38] == 0).all()) and bool((dw[1:37:9] == 0).all())
 
 
+def test_most_rows():
+    """2^31 - 1 rows, the most there are, nearly all of one expert: counts rounded up to tiles and chunks pass an int."""
+    R, W = 2 ** 31 - 1, 8
+    at = [0, 3, 4, 5, 2 ** 30, R - 2, R - 1]
+    a = torch.zeros((R, W), dtype=BF, device=dev())
+    some = randn((len(at), W), BF, 1)
+    for i, r in enumerate(at):
+        a[r] = some[i].to(dev())
+    w, offs = randn((2, W, W), BF, 2), to_dev(np.array([0, 4, R], np.int32))
+    out = torch.full((R, W), 3.0, dtype=BF, device=dev())
+    m.b16_grouped_gemm(a, w.to(dev()), out, mode=m.MOE_MODE_GROUPED, expert_offsets=offs)
+    torch.cuda.synchronize()
+    print("product of %d rows done" % R, flush=True)
+    ref, mag = tr.grouped_gemm(f64(some), f64(w), [0, 2, len(at)])
+    check(torch.stack([out[r] for r in at]), ref, sum_bound(W, mag, BF)(ref), "rows")
+    for r in at:
+        out[r] = 0
+    for lo in range(0, R, 2 ** 28):
+        assert bool((out[lo:lo + 2 ** 28] == 0).all()), "rows from %d" % lo
+    dy = out
+    other = randn((len(at), W), BF, 3)
+    for i, r in enumerate(at):
+        dy[r] = other[i].to(dev())
+    dw = torch.empty((2, W, W), dtype=F32, device=dev())
+    assert m.b16_grouped_wgrad_workspace_size(R, 2, W, W) > 0
+    m.b16_grouped_wgrad(dy, a, offs, dw)
+    torch.cuda.synchronize()
+    ref, mag = tr.grouped_wgrad(f64(other), f64(some), [0, 2, len(at)])
+    check(dw, ref, sum_bound(len(at) + 600, mag, F32)(ref), "gradient")     # zeros add without an error
+
+
 def test_elementwise_rows():
     R, n = 1100000, 1024
     x = torch.zeros((R, 2 * n), dtype=BF, device=dev())
