@@ -466,7 +466,8 @@ int moe_fused_decode_noalloc(const uint16_t* x_bf16, int64_t T, int64_t H, int64
  *   out  [m_rows][out_stride] of out_dt (MOE_BF16, MOE_F16 or MOE_F32)
  *   mode, expert_offsets, slot_ids, m_rows, a_row_div: as moe_bf8_grouped_gemm.  Grouped: rows
  *        [expert_offsets[e], expert_offsets[e+1]) use expert e and A row r, offsets are clamped to [0, m_rows],
- *        rows beyond the last are left untouched, any number of rows per expert (none included).  Slot:
+ *        rows beyond the last are left untouched, any number of rows per expert (none included); offsets that
+ *        decrease somewhere leave all of out untouched.  Slot:
  *        w_trans = 0 only; a slot outside [0, n_experts) writes a +0 row and reads nothing of that row.
  *   An infinity or NaN in a row of A or W reaches exactly the outputs whose sums hold it.
  *   Requirements: N % 8 == 0, K % 8 == 0, 8 <= N, K <= 2^20, m_rows <= 2^31 - 1, 1 <= n_experts <= 1024 in
@@ -496,7 +497,8 @@ int moe_b16_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K
  *        with moe_act_checkpoint's power-of-two scales that product is exact in bf16 (and in fp16 within its
  *        range), with moe_act_quant's it is rounded once to dt.  a_s is ignored otherwise.
  *   dw   element (e, n, k) at e*dw_stride_e + n*dw_stride_n + k, of dw_dt (MOE_BF16, MOE_F16 or MOE_F32)
- *   expert_offsets as moe_b16_grouped_gemm; rows beyond the last are not read.
+ *   expert_offsets as moe_b16_grouped_gemm; rows beyond the last are not read.  Offsets that decrease
+ *   are read within bounds, but give gradients that may lack rows.
  *   workspace: moe_b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K) bytes, 16-byte aligned, no
  *   initialization; 0 bytes (NULL allowed) unless the gradient has few tiles and long row ranges, which are
  *   then cut and their fp32 parts summed in order.  Scratch within one call: overlapping calls need their own.
@@ -521,6 +523,7 @@ int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void*
  *   written unless h is NULL.
  *   in    [rows][in_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32);  h [rows][h_stride] of dt
  *   out_q [rows][q_stride] bytes, out_s [rows][s_stride] fp32
+ *   A value v above 1.9375 * 2^127 rounds to 2^128, so code * s of it is an infinity.
  *   Pointers aligned to their types; 16-byte aligned rows with n % 8 == 0 take the vector path.
  */
 int moe_act_checkpoint(const void* in, int dt, int64_t in_stride, int64_t rows, int64_t n, int act, uint8_t* out_q,

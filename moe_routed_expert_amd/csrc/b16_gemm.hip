@@ -54,52 +54,59 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     // and last ones of more and of at most BP / 2 rows.  (Not by_size: all of them are of the first kind.)
     __shared__ int first_row[kMaxExperts + 1], first_whole[kMaxExperts + 1];
     __shared__ uint16_t first_long[kMaxExperts + 1], first_short[kMaxExperts + 1];
-    __shared__ int wave_sum[2 * C::NW];
+    __shared__ int decreases;                          // offsets that are below the one before
+    __shared__ uint32_t wave_sum[2 * C::NW];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int E = g.n_experts;
 
     // the tile table: EPT consecutive experts per thread, a scan of the counts over the block (the two kinds of last
-    // tiles in the halves of one word)
+    // tiles and the decreases in one word, 11, 11 and 10 bits: an expert adds to one of them, so only 1024 decreases
+    // could pass theirs, and then no expert has rows)
     {
         constexpr int EPT = kMaxExperts / C::THREADS;
-        int whole[EPT], last[EPT], sum_w = 0, sum_l = 0;
+        int whole[EPT];
+        uint32_t last[EPT], sum_w = 0, sum_l = 0;
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
-            whole[i] = last[i] = 0;
+            whole[i] = 0;
+            last[i] = 0;
             if (e < E) {
-                const int lo = min(max(g.offsets[e], 0), g.m_rows), hi = min(max(g.offsets[e + 1], lo), g.m_rows);
+                const int lo = min(max(g.offsets[e], 0), g.m_rows), to = min(max(g.offsets[e + 1], 0), g.m_rows), hi = max(to, lo);
                 const int rest = g.by_size ? (hi - lo) % C::BP : 0;
                 first_row[e] = lo;
                 if (e == E - 1) first_row[E] = hi;
                 whole[i] = pieces(hi - lo - rest, C::BP);
-                last[i] = rest > C::BP / 2 ? 1 : rest > 0 ? 1 << 16 : 0;
+                last[i] = to < lo ? 1u << 22 : rest > C::BP / 2 ? 1u : rest > 0 ? 1u << 11 : 0u;
             }
             sum_w += whole[i];
             sum_l += last[i];
         }
-        int w = sum_w, l = sum_l;
+        uint32_t w = sum_w, l = sum_l;
         block_exclusive_scan2<C::NW>(w, l, wave_sum, lane, wave);
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
             if (e < E) {
-                first_whole[e] = w;
-                first_long[e] = (uint16_t)l;
-                first_short[e] = (uint16_t)(l >> 16);
+                first_whole[e] = (int)w;
+                first_long[e] = (uint16_t)(l & 0x7FFu);
+                first_short[e] = (uint16_t)(l >> 11 & 0x7FFu);
             }
             w += whole[i];
             l += last[i];
             if (e == E - 1) {
-                first_whole[E] = w;
-                first_long[E] = (uint16_t)l;
-                first_short[E] = (uint16_t)(l >> 16);
+                first_whole[E] = (int)w;
+                first_long[E] = (uint16_t)(l & 0x7FFu);
+                first_short[E] = (uint16_t)(l >> 11 & 0x7FFu);
+                decreases = (int)(l >> 22);
             }
         }
         __syncthreads();
     }
+    // Experts that overlap may have more tiles than the host counted on, and share rows: nothing is computed.
+    if (__builtin_amdgcn_readfirstlane(decreases) != 0) return;
     const int whole_tiles = __builtin_amdgcn_readfirstlane(first_whole[E]);
     const int long_tiles = __builtin_amdgcn_readfirstlane(first_long[E]);
     const int m_tiles = whole_tiles + long_tiles + __builtin_amdgcn_readfirstlane(first_short[E]);

@@ -90,13 +90,13 @@ __device__ __forceinline__ v4f mfma16x16x32(v8s a, v8s b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Exclusive scans of a and b (one int of each per thread) over a block of NW waves; sums: 2 NW ints of LDS.
+// Exclusive scans of a and b (one word of each per thread) over a block of NW waves; sums: 2 NW words of LDS.
 template <int NW>
-__device__ __forceinline__ void block_exclusive_scan2(int& a, int& b, int* sums, int lane, int wave) {
-    int x = a, y = b;
+__device__ __forceinline__ void block_exclusive_scan2(uint32_t& a, uint32_t& b, uint32_t* sums, int lane, int wave) {
+    uint32_t x = a, y = b;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
-        const int u = __shfl_up(x, d, kWave), v = __shfl_up(y, d, kWave);
+        const uint32_t u = __shfl_up(x, d, kWave), v = __shfl_up(y, d, kWave);
         if (lane >= d) {
             x += u;
             y += v;

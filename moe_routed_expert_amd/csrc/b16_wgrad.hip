@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
     __shared__ int first_row[kMaxExperts + 1], first_chunk[kMaxExperts + 1];   // offsets, clamped to [0, m_rows]
-    __shared__ int wave_sum[2 * C::NW];
+    __shared__ uint32_t wave_sum[2 * C::NW];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -115,21 +115,22 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     int chunks = g.n_experts;
     if (g.chunk_rows > 0) {
         constexpr int EPT = kMaxExperts / C::THREADS;
-        int n[EPT], sum = 0;
+        int n[EPT];
+        uint32_t sum = 0;
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
             n[i] = e < g.n_experts ? pieces(max(first_row[e + 1] - first_row[e], 0), g.chunk_rows) : 0;
             sum += n[i];
         }
-        int before = sum, none = 0;
+        uint32_t before = sum, none = 0;
         block_exclusive_scan2<C::NW>(before, none, wave_sum, lane, wave);
 #pragma unroll
         for (int i = 0; i < EPT; i++) {
             const int e = tid * EPT + i;
-            if (e < g.n_experts) first_chunk[e] = before;
+            if (e < g.n_experts) first_chunk[e] = (int)before;
             before += n[i];
-            if (e == g.n_experts - 1) first_chunk[e + 1] = before;
+            if (e == g.n_experts - 1) first_chunk[e + 1] = (int)before;
         }
         __syncthreads();
         chunks = min(__builtin_amdgcn_readfirstlane(first_chunk[g.n_experts]), g.max_chunks);

@@ -289,6 +289,25 @@ def test_offsets_beyond_m_rows_are_clamped():
     assert bool((out[25:] == 9).all())
 
 
+@pytest.mark.parametrize("offs", [[0, 30, 10, 40], [40, 0, 40, 40], [5, 5, 5, 4], [0, 40, -3, 40]])
+@pytest.mark.parametrize("N,K", [(32, 64), (4096, 2048)])
+def test_decreasing_offsets_leave_the_output(offs, N, K):
+    a, w = randn((40, K), BF, 1).to(dev()), randn((3, N, K), BF, 2).to(dev())
+    out = torch.full((40, N), 9.0, dtype=F32, device=dev())
+    m.b16_grouped_gemm(a, w, out, mode=m.MOE_MODE_GROUPED, expert_offsets=to_dev(np.array(offs, np.int32)))
+    torch.cuda.synchronize()
+    assert bool((out == 9).all())
+
+
+def test_decreasing_offsets_of_every_expert():
+    E = 1024
+    a, w = randn((E, 8), BF, 1).to(dev()), randn((E, 8, 8), BF, 2).to(dev())
+    out = torch.full((E, 8), 9.0, dtype=F32, device=dev())
+    m.b16_grouped_gemm(a, w, out, mode=m.MOE_MODE_GROUPED, expert_offsets=to_dev(np.arange(E, -1, -1, dtype=np.int32)))
+    torch.cuda.synchronize()
+    assert bool((out == 9).all())
+
+
 @pytest.mark.parametrize("dt", [BF, FP])
 @pytest.mark.parametrize("mode", ["forward", "trans", "slot"])
 def test_subnormal_operands_count(dt, mode):
