@@ -8,10 +8,12 @@
 // Persistent workgroups walk the tiles of every expert, expert by expert, so experts of unequal length are
 // shared by all of them; an expert without rows gets zeros.  Where the gradient has few tiles and many rows
 // (small matrices, long sequences), the experts' rows are cut into chunks of one length, so long experts count as
-// several: their fp32 partial gradients go to a workspace and are summed in order, without atomics, so results do
-// not depend on timing.
+// several: their fp32 partial gradients go to a workspace and are summed in a fixed order, without atomics, so
+// results do not depend on timing.  Tile and cut are chosen by estimated time (wgrad_plan): the partials are written
+// and read once more, so a cut pays only where the device would be far from full.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "b16_tile.h"
@@ -266,39 +268,80 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
-// The chunks' partial gradients, [chunk][n][k] in fp32, summed in chunk order for each expert (onto what is there,
-// when accumulating) and rounded once.  Four consecutive k a thread, an expert per blockIdx.y; its chunks are
-// counted again from the offsets.
-template <int DT>
-__global__ void __launch_bounds__(256)
+// The chunks' partial gradients, [chunk][n][k] in fp32, summed for each expert (onto what is there, when accumulating)
+// and rounded once.  Four consecutive k a thread, an expert per blockIdx.y; its chunks are counted again from the
+// offsets.  Eight chunks are asked for at once: one by one each cost a trip to memory (a
+// gradient of 64 x 128 over 391 chunks took 179 us, and 24 now).  A gradient of few elements is shared further: its SPLIT waves take an equal run of chunks each, and wave 0
+// adds their sums in order.  The order depends on the counts alone.
+constexpr int kJoinSplit = 16;
+
+template <int DT, int SPLIT>
+__global__ void __launch_bounds__(SPLIT == 1 ? 256 : 64 * SPLIT)
 wgrad_join_kernel(const float* __restrict__ part, const int32_t* __restrict__ offsets, int m_rows, int chunk_rows,
                   int max_chunks, int64_t N, int64_t K, void* __restrict__ out, int64_t stride_e, int64_t stride_n,
                   int accumulate) {
-    __shared__ int wave_sum[4];
+    constexpr int THREADS = SPLIT == 1 ? 256 : 64 * SPLIT, OWN = THREADS / SPLIT;      // elements (of four) a workgroup
+    __shared__ int wave_sum[THREADS / kWave];
+    __shared__ v4f others[SPLIT == 1 ? 1 : SPLIT][SPLIT == 1 ? 1 : OWN];
     const int e = blockIdx.y, tid = threadIdx.x;
     auto chunks_of = [&](int x) {
         const int lo = min(max(offsets[x], 0), m_rows), hi = min(max(offsets[x + 1], 0), m_rows);
         return pieces(max(hi - lo, 0), chunk_rows);
     };
     int before = 0;
-    for (int x = tid; x < e; x += 256) before += chunks_of(x);
+    for (int x = tid; x < e; x += THREADS) before += chunks_of(x);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d, kWave);
     if (tid % kWave == 0) wave_sum[tid / kWave] = before;
     __syncthreads();
-    const int first = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
-    const int last = min(first + chunks_of(e), max_chunks);
-    const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 4;
-    if (i >= N * K) return;
-    const int64_t n = i / K, k = i - n * K, o = e * stride_e + n * stride_n + k;
+    int first = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / kWave; i++) first += wave_sum[i];
+    int last = min(first + chunks_of(e), max_chunks);
+    const int lane = tid % OWN, share = SPLIT == 1 ? 0 : tid / OWN;
+    if constexpr (SPLIT > 1) {
+        const int run = (max(last - first, 0) + SPLIT - 1) / SPLIT;
+        first += share * run;
+        last = min(last, first + run);
+    }
+    const int64_t i = ((int64_t)blockIdx.x * OWN + lane) * 4;
+    const bool in = i < N * K;
     v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = first; c < last; c++) sum += *reinterpret_cast<const v4f*>(part + c * (N * K) + i);
+    const float* p = part + (in ? i : 0);
+    for (int c = first; c < last; c += 8) {
+        v4f v[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) v[u] = *reinterpret_cast<const v4f*>(p + min(c + u, last - 1) * (N * K));
+#pragma unroll
+        for (int u = 0; u < 8; u++)
+            if (c + u < last) sum += v[u];
+    }
+    if constexpr (SPLIT > 1) {
+        others[share][lane] = sum;
+        __syncthreads();
+        if (share > 0) return;
+#pragma unroll
+        for (int s = 1; s < SPLIT; s++) sum += others[s][lane];
+    }
+    if (!in) return;
+    const int64_t n = i / K, k = i - n * K, o = e * stride_e + n * stride_n + k;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         float v = sum[j];
         if (accumulate) v += load_as_f32<DT>(out, o + j);
         store_from_f32<DT>(out, o + j, v);
     }
+}
+
+template <int DT>
+void launch_join(hipStream_t st, const float* part, const WgradArgs& g, void* dw, int64_t stride_e, int64_t stride_n, int accumulate) {
+    const int64_t quads = g.N * g.K / 4;
+    if (quads * g.n_experts >= 65536)                 // a workgroup of 256 for every CU
+        hipLaunchKernelGGL((wgrad_join_kernel<DT, 1>), dim3((unsigned)ceil_div(quads, 256), (unsigned)g.n_experts), dim3(256), 0, st, part,
+                           g.offsets, g.m_rows, g.chunk_rows, g.max_chunks, g.N, g.K, dw, stride_e, stride_n, accumulate);
+    else
+        hipLaunchKernelGGL((wgrad_join_kernel<DT, kJoinSplit>), dim3((unsigned)ceil_div(quads, 64), (unsigned)g.n_experts), dim3(64 * kJoinSplit), 0, st,
+                           part, g.offsets, g.m_rows, g.chunk_rows, g.max_chunks, g.N, g.K, dw, stride_e, stride_n, accumulate);
 }
 
 template <class C, bool SAVED, bool F16>
@@ -333,6 +376,7 @@ int wgrad_launch_cfg(hipStream_t st, WgradArgs g) {
 }
 
 using Tile256 = Cfg<256, 256, 2, 4, 2, 1>;
+using Tile256x128 = Cfg<256, 128, 4, 2, 3, 1>;
 using Tile128 = Cfg<128, 128, 2, 2, 2, 2>;
 
 template <class C>
@@ -346,17 +390,63 @@ bool wgrad_shape_ok(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
            K >= 8 && K <= kMaxWidth && K % 8 == 0;
 }
 
-// The large tile needs enough tiles for the device's 256 CUs.
-bool wgrad_large(int64_t E, int64_t N, int64_t K) { return ceil_div(N, 256) * ceil_div(K, 256) * E >= 512; }
+// The tile, and the rows of a chunk (0: the experts' rows stay whole).
+struct WgradPlan {
+    int tile, chunk_rows;
+};
 
-// Rows of a chunk, or 0 where the experts' rows stay whole: enough chunks for two workgroups of the 128 x 128 form on
-// each of the device's 256 CUs, none shorter than 256 rows, and only where that cuts an average expert.
-int wgrad_chunk_rows(int64_t m_rows, int64_t E, int64_t N, int64_t K) {
-    if (wgrad_large(E, N, K)) return 0;
-    const int64_t want = 512 / (ceil_div(N, 128) * ceil_div(K, 128));
-    if (want <= E) return 0;
-    const int64_t rows = std::max<int64_t>(256, ceil_div(ceil_div(m_rows, want - E), kStep) * kStep);
-    return rows * E <= m_rows ? (int)rows : 0;
+// Measured per tile: the workgroups that the device's 256 CUs hold, and the time of a step in us when they are few and
+// when they are all there.
+struct WgradCost {
+    int bp, bq, slots;
+    double alone, full;
+};
+constexpr WgradCost kWgradCosts[] = {{128, 128, 512, 0.80, 1.07}, {256, 128, 256, 0.83, 1.00}, {256, 256, 256, 1.33, 1.86}};
+
+// The plan of least estimated time, in us: rounds of workgroups times (a chunk's steps, and 4.3 for its start and
+// stores), or the bytes at 5 TB/s if that is more, and for cut rows the join: 6.8 and its bytes at 4.9 TB/s.  Whole
+// ranges are taken as 1.12 of the average expert's, 1.35 where one round has to wait for the longest (the counts are
+// on the device); a cut adds half a chunk an expert.  Chunks are tried that fill the device once or twice, and the
+// length at which steps and join would balance.  A tenth of the work is added so that tiles bound by the same bytes are
+// told apart.  Over 42 problems from 2 to 100000 rows and 1 to 224 experts the plan took 3 % more time than the best of
+// all tiles and chunk lengths in the mean and 17 % at most; cutting whenever the 128 x 128 tiles left the device
+// unfilled took 13 % more over 18 of them and 44 % at most (2 x 4096 rows of 2048 x 1024: 82 us against 59 whole).
+WgradPlan wgrad_plan(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
+    const double R = (double)m_rows, E = (double)n_experts, NK = (double)N * (double)K;
+    WgradPlan best{0, 0};
+    double least = 0.0;
+    for (int i = 0; i < 3; i++) {
+        const WgradCost& c = kWgradCosts[i];
+        const double nt = (double)(ceil_div(N, c.bp) * ceil_div(K, c.bq));
+        auto time = [&](double chunks, double rows, bool cut) {
+            const double tiles = chunks * nt, rounds = std::ceil(tiles / c.slots - 1e-9);
+            const double step = c.alone + (c.full - c.alone) * std::min(1.0, std::max(0.0, i == 0 ? tiles / 256.0 - 1.0 : tiles / 256.0));
+            const double uneven = cut || n_experts == 1 ? 1.0 : rounds > 1.0 ? 1.12 : 1.35;
+            const double steps = std::max(1.0, std::ceil(rows / kStep)) * uneven;
+            const double work = rounds * (steps * step + 4.3);
+            const double bytes = R * (double)(N + K) * 2.0 + chunks * NK * (cut ? 4.0 : 2.0);
+            return std::max(work, bytes / 5e6 + 3.0) + 0.1 * work + (cut ? 6.8 + (chunks + E) * 4.0 * NK / 4.9e6 : 0.0);
+        };
+        const double whole = time(E, R / E, false);
+        if (i == 0 || whole < least) {
+            least = whole;
+            best = {i, 0};
+        }
+        const double balance = std::sqrt(R * kStep / c.alone * 4.0 * NK / 4.9e6);
+        for (int j = 0; j < 3; j++) {
+            const double room = j * c.slots / nt - (n_experts == 1 ? 0.0 : E);      // chunks of j rounds
+            if (j > 0 && std::floor(room) < 1.0) continue;
+            const double want = j == 0 ? balance : R / std::floor(room);
+            const double rows = std::max(256.0, std::ceil(want / kStep) * kStep);
+            if (rows * E > R || rows >= R) continue;                                   // would not cut an average expert
+            const double t = time(n_experts == 1 ? std::ceil(R / rows) : R / rows + 0.5 * E, rows, true);
+            if (t < least) {
+                least = t;
+                best = {i, (int)rows};
+            }
+        }
+    }
+    return best;
 }
 
 int64_t wgrad_max_chunks(int64_t m_rows, int64_t E, int64_t chunk_rows) { return m_rows / chunk_rows + E; }
@@ -368,7 +458,7 @@ using namespace moe;
 
 extern "C" size_t moe_b16_grouped_wgrad_workspace_size(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     if (!b16::wgrad_shape_ok(m_rows, n_experts, N, K)) return 0;
-    const int rows = b16::wgrad_chunk_rows(m_rows, n_experts, N, K);
+    const int rows = b16::wgrad_plan(m_rows, n_experts, N, K).chunk_rows;
     return rows > 0 ? (size_t)b16::wgrad_max_chunks(m_rows, n_experts, rows) * N * K * 4 : 0;
 }
 
@@ -395,7 +485,8 @@ extern "C" int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, 
     g.a = (const char*)a; g.a_stride = saved ? a_stride : a_stride * 2;
     g.a_s = a_s; g.a_s_stride = a_s_stride;
     g.offsets = expert_offsets; g.m_rows = (int)m_rows; g.n_experts = (int)n_experts; g.N = N; g.K = K;
-    g.chunk_rows = b16::wgrad_chunk_rows(m_rows, n_experts, N, K);
+    const b16::WgradPlan plan = b16::wgrad_plan(m_rows, n_experts, N, K);
+    g.chunk_rows = plan.chunk_rows;
     g.out = (char*)dw; g.out_dt = dw_dt; g.stride_e = dw_stride_e; g.stride_n = dw_stride_n;
     g.accumulate = accumulate;
     auto st = as_stream(stream);
@@ -406,19 +497,14 @@ extern "C" int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, 
         if (!aligned16(workspace)) return MOE_ERR_ALIGN;
         g.out = (char*)workspace; g.out_dt = MOE_F32; g.stride_e = N * K; g.stride_n = K; g.accumulate = 0;
     }
-    const int rc = b16::wgrad_large(n_experts, N, K) ? b16::wgrad_launch<b16::Tile256>(st, saved, dt == MOE_F16, g)
-                                                     : b16::wgrad_launch<b16::Tile128>(st, saved, dt == MOE_F16, g);
+    const bool f16 = dt == MOE_F16;
+    const int rc = plan.tile == 0   ? b16::wgrad_launch<b16::Tile128>(st, saved, f16, g)
+                   : plan.tile == 1 ? b16::wgrad_launch<b16::Tile256x128>(st, saved, f16, g)
+                                    : b16::wgrad_launch<b16::Tile256>(st, saved, f16, g);
     if (rc != MOE_OK || g.chunk_rows == 0) return rc;
-    const dim3 grid((unsigned)ceil_div(N * K / 4, 256), (unsigned)n_experts), block(256);
     const float* part = (const float*)workspace;
-    if (dw_dt == MOE_F32)
-        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF32>), grid, block, 0, st, part, expert_offsets, g.m_rows, g.chunk_rows,
-                           g.max_chunks, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
-    else if (dw_dt == MOE_BF16)
-        hipLaunchKernelGGL((b16::wgrad_join_kernel<kBF16>), grid, block, 0, st, part, expert_offsets, g.m_rows, g.chunk_rows,
-                           g.max_chunks, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
-    else
-        hipLaunchKernelGGL((b16::wgrad_join_kernel<kF16>), grid, block, 0, st, part, expert_offsets, g.m_rows, g.chunk_rows,
-                           g.max_chunks, N, K, dw, dw_stride_e, dw_stride_n, accumulate);
+    if (dw_dt == MOE_F32) b16::launch_join<kF32>(st, part, g, dw, dw_stride_e, dw_stride_n, accumulate);
+    else if (dw_dt == MOE_BF16) b16::launch_join<kBF16>(st, part, g, dw, dw_stride_e, dw_stride_n, accumulate);
+    else b16::launch_join<kF16>(st, part, g, dw, dw_stride_e, dw_stride_n, accumulate);
     return launch_status();
 }

@@ -85,6 +85,28 @@ def test_large_tiles(counts, E, N, K, saved):
     wgrad(list(c), N, K, BF, F32, saved, seed=E)
 
 
+# rows an expert, matrix, and whether the rows are cut: each tile whole and cut, both forms of the join
+PLANS = [([6001], 136, 80, True), ([0, 9000, 5], 72, 80, True), ([12000, 7000, 0, 1001], 512, 768, True), ([20000], 520, 528, True),
+         ([65536], 1024, 1024, True), ([300], 2040, 4080, False), ([200, 0, 3, 64], 1032, 2064, False), ([1500, 1500], 1024, 512, None)]
+
+
+@pytest.mark.parametrize("saved", [False, True])
+@pytest.mark.parametrize("counts,N,K,cut", PLANS)
+def test_every_plan(counts, N, K, cut, saved):
+    if cut is not None:
+        assert (m.b16_grouped_wgrad_workspace_size(sum(counts), len(counts), N, K) > 0) == cut
+    wgrad(counts, N, K, BF, F32, saved, seed=N)
+
+
+@pytest.mark.parametrize("odt", [BF, FP, F32])
+@pytest.mark.parametrize("counts,N,K", [([3, 9000, 0], 72, 80), ([12000, 8001], 512, 768)])
+def test_cut_rows_added_on(counts, N, K, odt):
+    assert m.b16_grouped_wgrad_workspace_size(sum(counts), len(counts), N, K) > 0
+    one = wgrad(counts, N, K, FP, odt, False, seed=5, accumulate=True)
+    two = wgrad(counts, N, K, FP, odt, False, seed=5, accumulate=True)
+    assert torch.equal(one.view, two.view)
+
+
 @pytest.mark.parametrize("saved", [False, True])
 @pytest.mark.parametrize("odt", [BF, FP, F32])
 @pytest.mark.parametrize("accumulate", [False, True])
