@@ -333,7 +333,14 @@ def route_prep(logits, topk, stream=None):
 # ---------------------------------------------------------------------------
 # 16-bit experts and the backward pass
 
+# These wrappers are called once or more per layer, and a small operator's time is its call's: they read each tensor's
+# properties once, in place.
+
 _entry = {}          # C functions by name
+_U8, _I32T, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_UNIT = "unit column stride expected"
 
 
 def _call(fn, tensors, args, stream):
@@ -344,28 +351,17 @@ def _call(fn, tensors, args, stream):
     for t in tensors:
         assert t is None or t.get_device() == dev, "tensors of one GPU expected"
     f = _entry.get(fn) or _entry.setdefault(fn, getattr(lib(), fn))
-    if dev == torch._C._cuda_getDevice():
-        st = f(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        st = f(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev))
+            st = f(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
     if st != MOE_OK:
         raise MoeError(fn, st)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _rows(t):
-    """Row stride of a 2-D tensor with unit column stride."""
-    r, c = t.stride()
-    assert c == 1, "unit column stride expected"
-    return r
-
-
 def _i32(t, n, what):
-    assert t.dtype is torch.int32 and t.numel() == n and t.is_contiguous(), "%s: %d contiguous int32 expected" % (what, n)
+    assert t.dtype is _I32T and t.numel() == n and t.is_contiguous(), "%s: %d contiguous int32 expected" % (what, n)
 
 
 def b16_grouped_gemm(a, w, out, *, mode, expert_offsets=None, slot_ids=None, m_rows=None, a_row_div=1,
@@ -376,21 +372,27 @@ def b16_grouped_gemm(a, w, out, *, mode, expert_offsets=None, slot_ids=None, m_r
     E, N, K = w.shape
     if w_trans:
         N, K = K, N
-    se, sr, sc = w.stride()
+    w_e, w_r, w_1 = w.stride()
     a_rows, a_cols = a.shape
+    a_r, a_1 = a.stride()
     o_rows, o_cols = out.shape
+    o_r, o_1 = out.stride()
+    dt = a.dtype
     rows = o_rows if m_rows is None else m_rows
-    assert a.dtype is w.dtype and a_cols == K and o_cols == N and sc == 1, "operands do not match"
+    assert dt is w.dtype and a_cols == K and o_cols == N, "operands do not match"
+    assert w_1 == 1 and a_1 == 1 and o_1 == 1, _UNIT
     assert 0 <= rows <= o_rows, "m_rows exceeds out"
     if mode == MOE_MODE_SLOT:
         _i32(slot_ids, rows, "slot_ids")
         assert a_rows * a_row_div >= rows, "a has too few rows"
+        offs, slots = None if expert_offsets is None else expert_offsets.data_ptr(), slot_ids.data_ptr()
     else:
         _i32(expert_offsets, E + 1, "expert_offsets")
         assert a_rows >= rows, "a has too few rows"
+        offs, slots = expert_offsets.data_ptr(), None if slot_ids is None else slot_ids.data_ptr()
     _call("moe_b16_grouped_gemm", (a, w, out, expert_offsets, slot_ids), (
-        a.data_ptr(), _rows(a), w.data_ptr(), se, sr, E, N, K, _dt(a), int(w_trans), mode,
-        _addr(expert_offsets), _addr(slot_ids), rows, a_row_div, out.data_ptr(), _dt(out), _rows(out)), stream)
+        a.data_ptr(), a_r, w.data_ptr(), w_e, w_r, E, N, K, _DT[dt], 1 if w_trans else 0, mode, offs, slots, rows, a_row_div,
+        out.data_ptr(), _DT[out.dtype], o_r), stream)
 
 
 def b16_grouped_tile(m_rows, n_experts, N, K):
@@ -412,12 +414,21 @@ def b16_grouped_wgrad(dy, a, expert_offsets, dw, *, a_s=None, m_rows=None, accum
     fp16 or fp32.  workspace: uint8 tensor of b16_grouped_wgrad_workspace_size bytes, allocated here when None."""
     E, N, K = dw.shape
     rows = dy.shape[0] if m_rows is None else m_rows
-    saved = a.dtype == torch.uint8
+    saved = a.dtype is _U8
+    dy_rows, dy_cols = dy.shape
+    a_rows, a_cols = a.shape
+    dy_r, dy_1 = dy.stride()
+    a_r, a_1 = a.stride()
+    dw_e, dw_n, dw_1 = dw.stride()
     assert saved == (a_s is not None), "scales go with saved (uint8) rows"
-    assert dy.shape[1] == N and a.shape[1] == K and dw.stride(2) == 1, "operands do not match"
-    assert 0 <= rows <= min(dy.shape[0], a.shape[0]), "m_rows exceeds dy or a"
+    assert dy_cols == N and a_cols == K, "operands do not match"
+    assert dy_1 == 1 and a_1 == 1 and dw_1 == 1, _UNIT
+    assert 0 <= rows <= dy_rows and rows <= a_rows, "m_rows exceeds dy or a"
+    s_r = 0
     if saved:
-        assert a_s.dtype == torch.float32 and a_s.shape[0] >= rows and a_s.shape[1] >= (K + 127) // 128, "scales do not match"
+        assert a_s.dtype is _F32 and a_s.shape[0] >= rows and a_s.shape[1] >= (K + 127) // 128, "scales do not match"
+        s_r, s_1 = a_s.stride()
+        assert s_1 == 1, _UNIT
     _i32(expert_offsets, E + 1, "expert_offsets")
     size = b16_grouped_wgrad_workspace_size(rows, E, N, K)
     if size and workspace is None:
@@ -426,9 +437,10 @@ def b16_grouped_wgrad(dy, a, expert_offsets, dw, *, a_s=None, m_rows=None, accum
     if workspace is not None:
         assert workspace.is_contiguous() and workspace.element_size() == 1, "workspace: contiguous bytes"
     _call("moe_b16_grouped_wgrad", (dy, a, a_s, expert_offsets, dw, workspace), (
-        dy.data_ptr(), _rows(dy), _dt(dy), a.data_ptr(), _rows(a), MOE_E4M3 if saved else _dt(a), _addr(a_s),
-        _rows(a_s) if saved else 0, expert_offsets.data_ptr(), E, N, K, rows, dw.data_ptr(), _dt(dw), dw.stride(0),
-        dw.stride(1), int(accumulate), _addr(workspace), workspace.numel() if workspace is not None else 0), stream)
+        dy.data_ptr(), dy_r, _DT[dy.dtype], a.data_ptr(), a_r, MOE_E4M3 if saved else _DT[a.dtype],
+        a_s.data_ptr() if saved else None, s_r, expert_offsets.data_ptr(), E, N, K, rows, dw.data_ptr(), _DT[dw.dtype],
+        dw_e, dw_n, 1 if accumulate else 0, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel()), stream)
 
 
 def act_checkpoint(x, out_q, out_s, act=MOE_ACT_IDENTITY, h=None, stream=None):
@@ -437,56 +449,87 @@ def act_checkpoint(x, out_q, out_s, act=MOE_ACT_IDENTITY, h=None, stream=None):
     rows, width = x.shape
     n = width if act == MOE_ACT_IDENTITY else width // 2
     both = 1 if act == MOE_ACT_IDENTITY else 2
+    dt = x.dtype
+    x_r, x_1 = x.stride()
+    q_r, q_1 = out_q.stride()
+    s_r, s_1 = out_s.stride()
     assert width == both * n, "gate and up of one width expected"
-    assert out_q.dtype == torch.uint8 and out_s.dtype == torch.float32, "codes are uint8, scales float32"
+    assert out_q.dtype is _U8 and out_s.dtype is _F32, "codes are uint8, scales float32"
     assert out_q.shape == (rows, width) and out_s.shape == (rows, both * ((n + 127) // 128)), "outputs do not match"
-    assert h is None or (h.dtype == x.dtype and h.shape == (rows, n)), "h does not match"
+    assert x_1 == 1 and q_1 == 1 and s_1 == 1, _UNIT
+    h_r, h_p = 0, None
+    if h is not None:
+        h_r, h_1 = h.stride()
+        h_p = h.data_ptr()
+        assert h.dtype is dt and h.shape == (rows, n) and h_1 == 1, "h does not match"
     _call("moe_act_checkpoint", (x, out_q, out_s, h), (
-        x.data_ptr(), _dt(x), _rows(x), rows, n, act, out_q.data_ptr(), _rows(out_q), out_s.data_ptr(),
-        _rows(out_s), _addr(h), _rows(h) if h is not None else 0), stream)
+        x.data_ptr(), _DT[dt], x_r, rows, n, act, out_q.data_ptr(), q_r, out_s.data_ptr(), s_r, h_p, h_r), stream)
 
 
 def gated_act_backward(dh, q, s, dx, act=MOE_ACT_SILU_MUL, h=None, stream=None):
     """Backward of h = act(gate) * up from saved codes q [rows, 2n] and scales s: dx [rows, 2n] = [d gate | d up],
     and h [rows, n] again when given.  dh, dx, h of one type."""
     rows, n = dh.shape
-    assert q.dtype == torch.uint8 and s.dtype == torch.float32, "codes are uint8, scales float32"
-    assert q.shape == (rows, 2 * n) and s.shape == (rows, 2 * ((n + 127) // 128)), "saved rows do not match"
-    assert dx.dtype == dh.dtype and dx.shape == (rows, 2 * n), "dx does not match"
-    assert h is None or (h.dtype == dh.dtype and h.shape == (rows, n)), "h does not match"
+    dt = dh.dtype
+    d_r, d_1 = dh.stride()
+    q_r, q_1 = q.stride()
+    s_r, s_1 = s.stride()
+    x_r, x_1 = dx.stride()
+    wide = (rows, 2 * n)
+    assert q.dtype is _U8 and s.dtype is _F32, "codes are uint8, scales float32"
+    assert q.shape == wide and s.shape == (rows, 2 * ((n + 127) // 128)), "saved rows do not match"
+    assert dx.dtype is dt and dx.shape == wide, "dx does not match"
+    assert d_1 == 1 and q_1 == 1 and s_1 == 1 and x_1 == 1, _UNIT
+    h_r, h_p = 0, None
+    if h is not None:
+        h_r, h_1 = h.stride()
+        h_p = h.data_ptr()
+        assert h.dtype is dt and h.shape == (rows, n) and h_1 == 1, "h does not match"
     _call("moe_gated_act_backward", (dh, q, s, dx, h), (
-        dh.data_ptr(), _dt(dh), _rows(dh), q.data_ptr(), _rows(q), s.data_ptr(), _rows(s), rows, n, act,
-        dx.data_ptr(), _rows(dx), _addr(h), _rows(h) if h is not None else 0), stream)
+        dh.data_ptr(), _DT[dt], d_r, q.data_ptr(), q_r, s.data_ptr(), s_r, rows, n, act, dx.data_ptr(), x_r, h_p, h_r),
+        stream)
 
 
 def topk_reduce_backward(dout, y, slot_ids, weights, dy, dweights=None, route_rows=None, stream=None):
     """Backward of topk_reduce: dy[row(t,j)] = weights[t,j] * dout[t], dweights[t,j] = <dout[t], y[row(t,j)]>.
     dout [T, H] bf16; y (None when dweights is None) and dy [rows, H] of one type."""
-    T, topk = slot_ids.shape
+    routes = slot_ids.shape
+    T, topk = routes
     rows, H = dy.shape
+    dt = dy.dtype
+    d_r, d_1 = dout.stride()
+    o_r, o_1 = dy.stride()
     _i32(slot_ids, T * topk, "slot_ids")
-    assert dout.dtype == torch.bfloat16 and dout.shape == (T, H), "dout: [T, H] bfloat16"
-    assert weights.dtype == torch.float32 and weights.is_contiguous() and weights.shape == slot_ids.shape, "weights do not match"
-    assert dweights is None or (dweights.dtype == torch.float32 and dweights.is_contiguous() and
-                                dweights.shape == slot_ids.shape), "dweights do not match"
-    assert y is None or (y.dtype == dy.dtype and y.shape == dy.shape), "y does not match dy"
+    assert dout.dtype is _BF16 and dout.shape == (T, H), "dout: [T, H] bfloat16"
+    assert weights.dtype is _F32 and weights.is_contiguous() and weights.shape == routes, "weights do not match"
+    assert d_1 == 1 and o_1 == 1, _UNIT
+    y_r, y_p, dw_p, rr_p = 0, None, None, None
+    if dweights is not None:
+        assert dweights.dtype is _F32 and dweights.is_contiguous() and dweights.shape == routes, "dweights do not match"
+        dw_p = dweights.data_ptr()
+    if y is not None:
+        y_r, y_1 = y.stride()
+        y_p = y.data_ptr()
+        assert y.dtype is dt and y.shape == (rows, H) and y_1 == 1, "y does not match dy"
     if route_rows is not None:
         _i32(route_rows, T * topk, "route_rows")
+        rr_p = route_rows.data_ptr()
     else:
         assert rows >= T * topk, "a row for every route expected"
-    _call("moe_topk_reduce_backward", (dout, y if y is not None else dout, slot_ids, route_rows, weights, dy, dweights), (
-        dout.data_ptr(), _rows(dout), _addr(y), _dt(dy), _rows(y) if y is not None else 0, rows,
-        slot_ids.data_ptr(), _addr(route_rows), weights.data_ptr(), T, topk, H, dy.data_ptr(), _rows(dy),
-        _addr(dweights)), stream)
+    _call("moe_topk_reduce_backward", (dout, y, slot_ids, route_rows, weights, dy, dweights), (
+        dout.data_ptr(), d_r, y_p, _DT[dt], y_r, rows, slot_ids.data_ptr(), rr_p, weights.data_ptr(), T, topk, H,
+        dy.data_ptr(), o_r, dw_p), stream)
 
 
 def route_prep_backward(expert_ids, weights, dweights, dlogits, stream=None):
     """Router gradient: dlogits [T, E] from route_prep's expert_ids and weights and the weights' gradient."""
-    T, topk = expert_ids.shape
+    routes = expert_ids.shape
+    T, topk = routes
+    rows, E = dlogits.shape
+    l_r, l_1 = dlogits.stride()
     _i32(expert_ids, T * topk, "expert_ids")
-    for t in (weights, dweights):
-        assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == expert_ids.shape, "weights do not match"
-    assert dlogits.dtype == torch.float32 and dlogits.shape[0] == T, "dlogits: [T, E] float32"
+    assert weights.dtype is _F32 and weights.is_contiguous() and weights.shape == routes, "weights do not match"
+    assert dweights.dtype is _F32 and dweights.is_contiguous() and dweights.shape == routes, "dweights do not match"
+    assert dlogits.dtype is _F32 and rows == T and l_1 == 1, "dlogits: [T, E] float32"
     _call("moe_route_prep_backward", (expert_ids, weights, dweights, dlogits), (
-        expert_ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), T, dlogits.shape[1], topk, dlogits.data_ptr(),
-        _rows(dlogits)), stream)
+        expert_ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), T, E, topk, dlogits.data_ptr(), l_r), stream)
