@@ -5,12 +5,17 @@
 //
 // MI355X design of the grouped mode (the tile engine is b16_tile.h).
 //  * Tiles from 32 x 64 to 256 x 256, by estimated time (pick_tile).  Persistent workgroups, one per CU (two of the
-//    64 x 64 tile): a tile's LDS ring takes most of the CU's 160 KB.  Each reads the device offsets once into an LDS table of every expert's first M tile and walks its tiles; the
-//    load pipeline runs on across tiles, so a tile's first steps are in flight while the tile before it is
-//    multiplied and stored.
+//    64 x 64 tile): a tile's LDS ring takes most of the CU's 160 KB.  Each reads the device offsets once into an LDS
+//    table of every expert's first M tile and walks its tiles; the load pipeline runs on across tiles, so a tile's
+//    first steps are in flight while the tile before it is multiplied and stored.
 //  * Tiles are numbered in panels of kPanel M tiles, M fastest, and tile t of round s goes to workgroup t % G
 //    with the workgroups of one XCD next to each other: the tiles that an XCD works on at one time form a
 //    patch whose A rows and weight columns meet in its L2.
+//  * Bound by the bank's bytes where experts have few rows: 256 experts of 2048 x 4096 and 24576 rows take 742 us
+//    (6.2 TB/s over banks, rows and output).  Bound by the MFMAs' feed where they have many: 8 experts of 2048 rows,
+//    4096 x 8192 take 860 us (1.28 PFLOP/s; the matrix units are busy two thirds of the cycles, and zeros as data
+//    take 771 us).  Bound by latency where there is little: 333 rows over 16 experts, 1000 x 520 take 9.5 us, of which
+//    6.5 are there at K = 8 already.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -343,9 +348,9 @@ int grouped_launch(hipStream_t st, bool trans, bool f16, const GemmArgs& g) {
 // ------------------------------------------------------------------ slot mode
 // One wave holds COLS columns of one row: its lanes take 8 consecutive k each (512 a chunk), products and sums in fp32,
 // and the lanes' sums meet in six shuffles.  Bound by streaming the row's expert, so a wave asks for UNROLL chunks of
-// all its columns (8 KB of weights) at once before it multiplies: 8 routes of 1536 x 2048 take 9.3 us (4.8 TB/s), 64
-// of them 67 us (5.9 TB/s), one row of 8192 x 8192 26 us.  Four columns a wave and a loop over single chunks took
-// 11.2, 77 and 48 us.
+// all its columns (8 KB of weights) at once before it multiplies: 8 routes of 1536 x 2048, one of them inactive, take
+// 8.6 us a call (4.9 TB/s); 64 routes 67 us (5.9 TB/s), one row of 8192 x 8192 26 us.  Four columns a wave and a loop
+// over single chunks took 77 and 48 us for these two.
 constexpr int kSlotWaves = 4;
 
 template <bool F16>

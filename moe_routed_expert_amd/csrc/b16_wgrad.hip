@@ -11,6 +11,10 @@
 // several: their fp32 partial gradients go to a workspace and are summed in a fixed order, without atomics, so
 // results do not depend on timing.  Tile and cut are chosen by estimated time (wgrad_plan): the partials are written
 // and read once more, so a cut pays only where the device would be far from full.
+//
+// Two transposing reads a fragment and both operands' loads bound it where experts have many rows (8 experts, 16384
+// rows, 8192 x 4096 in fp32: 995 us, 1.10 PFLOP/s), the gradient's stores where they have few (256 experts, 24576 rows
+// from 8 bits, 2048 x 4096 in bf16: 1240 us for 4.3 GB, which a kernel of such stores alone writes in 772 us).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
