@@ -44,16 +44,25 @@ struct GemmArgs {
     int m_rows;
     int n_tiles;                      // N tiles
     int by_size;                      // whole tiles of all experts first, then the last ones by size
+    int main_wgs;                     // by_size: workgroups of the launch that a tail launch follows, or 0
+    int main_n_tiles;                 // and its N tiles
     void* out;
     int out_dt;
     int64_t out_stride;               // elements
 };
 
-template <class C, bool QT, bool F16>
+// TAIL: the launch behind a by_size one of tiles twice as high.  It takes the last tiles of at most C::BP rows where
+// they alone would cost the main launch one more round, and is empty otherwise; both find out from the offsets.  Few
+// of the 256 x 256 tiles are then left, with one step in flight each, so their round waits for memory; 128 x 128
+// tiles with three in flight share it among more workgroups: 8 experts of ragged rows, 16384 x 8192 to 4096 1026 -> 964
+// us, one of 4200 rows, 8192 x 8192 544 -> 462, 16 of 2048 rows, 2048 x 2048 250 -> 252.  (Tail tiles of 128 x 256:
+// 982 us, 481, 245.)  An empty tail costs about 1 % of 250 us.
+template <class C, bool QT, bool F16, bool TAIL>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(const GemmArgs g) {
     using P = KMajor<C::BP, C::NW>;
     using Q = std::conditional_t<QT, TMajor<C::BQ, C::NW>, KMajor<C::BQ, C::NW>>;
     constexpr int S = C::S, STAGE = P::BYTES + Q::BYTES, LPS = P::LOADS + Q::LOADS;
+    constexpr int TB = TAIL ? 2 * C::BP : C::BP;       // rows of the table's tiles
     __shared__ __attribute__((aligned(1024))) uint8_t ring[S * STAGE];
     // Before expert e: its rows, and the M tiles of three kinds ([n_experts] is the total): whole ones (BP rows),
     // and last ones of more and of at most BP / 2 rows.  (Not by_size: all of them are of the first kind.)
@@ -80,11 +89,11 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
             last[i] = 0;
             if (e < E) {
                 const int lo = min(max(g.offsets[e], 0), g.m_rows), to = min(max(g.offsets[e + 1], 0), g.m_rows), hi = max(to, lo);
-                const int rest = g.by_size ? (hi - lo) % C::BP : 0;
+                const int rest = g.by_size ? (hi - lo) % TB : 0;
                 first_row[e] = lo;
                 if (e == E - 1) first_row[E] = hi;
-                whole[i] = pieces(hi - lo - rest, C::BP);
-                last[i] = to < lo ? 1u << 22 : rest > C::BP / 2 ? 1u : rest > 0 ? 1u << 11 : 0u;
+                whole[i] = pieces(hi - lo - rest, TB);
+                last[i] = to < lo ? 1u << 22 : rest > TB / 2 ? 1u : rest > 0 ? 1u << 11 : 0u;
             }
             sum_w += whole[i];
             sum_l += last[i];
@@ -114,7 +123,11 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     if (__builtin_amdgcn_readfirstlane(decreases) != 0) return;
     const int whole_tiles = __builtin_amdgcn_readfirstlane(first_whole[E]);
     const int long_tiles = __builtin_amdgcn_readfirstlane(first_long[E]);
-    const int m_tiles = whole_tiles + long_tiles + __builtin_amdgcn_readfirstlane(first_short[E]);
+    const int short_tiles = __builtin_amdgcn_readfirstlane(first_short[E]);
+    const int main_tiles = (whole_tiles + long_tiles) * g.main_n_tiles;
+    const bool tail = g.main_wgs > 0 && ceil_div(main_tiles + short_tiles * g.main_n_tiles, g.main_wgs) > ceil_div(main_tiles, g.main_wgs);
+    const int m_first = TAIL ? whole_tiles + long_tiles : 0;
+    const int m_tiles = TAIL ? (tail ? short_tiles : 0) : whole_tiles + long_tiles + (tail ? 0 : short_tiles);
     const int tiles = m_tiles * g.n_tiles;
     const int G = gridDim.x;
     const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
@@ -130,7 +143,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
         const int per = kPanel * g.n_tiles;
         const int panel = t / per, r = t - panel * per;
         const int height = min(kPanel, m_tiles - panel * kPanel);
-        const int nt = r / height, mt = panel * kPanel + r - nt * height;
+        const int nt = r / height, mt = m_first + panel * kPanel + r - nt * height;
         // the last expert whose first tile of the kind is <= its number: the tile's expert
         const bool whole = mt < whole_tiles, is_long = mt < whole_tiles + long_tiles;
         const int k = whole ? mt : mt - whole_tiles - (is_long ? 0 : long_tiles);
@@ -139,7 +152,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
         Tile ti;
         ti.expert = lo;
         const int from = __builtin_amdgcn_readfirstlane(first_row[lo]), end = __builtin_amdgcn_readfirstlane(first_row[lo + 1]);
-        ti.row0 = whole ? from + (k - __builtin_amdgcn_readfirstlane(first(lo))) * C::BP : end - (end - from) % C::BP;
+        ti.row0 = whole ? from + (k - __builtin_amdgcn_readfirstlane(first(lo))) * TB : end - (end - from) % TB;
         ti.rows = min(end - ti.row0, C::BP);
         ti.n0 = nt * C::BQ;
         return ti;
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(c
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
-template <class C, bool QT, bool F16>
+template <class C, bool QT, bool F16, bool TAIL>
 int resident_blocks() {
     static std::atomic<int> cached[64];   // concurrent first calls may both fill it, with the same value
     int dev = 0;
@@ -265,7 +278,7 @@ int resident_blocks() {
     int c = cached[dev].load(std::memory_order_relaxed);
     if (c == 0) {
         int per_cu = 0, cus = 0;
-        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, b16_gemm_kernel<C, QT, F16>, C::THREADS, 0) != hipSuccess ||
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, b16_gemm_kernel<C, QT, F16, TAIL>, C::THREADS, 0) != hipSuccess ||
             hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
             return 0;
         c = per_cu * cus;
@@ -274,26 +287,41 @@ int resident_blocks() {
     return c;
 }
 
-template <class C, bool QT, bool F16>
-int launch_cfg(hipStream_t st, GemmArgs g) {
-    const int64_t n_tiles = ceil_div(g.N, C::BQ);
-    const int64_t most = (g.m_rows / C::BP + std::min<int64_t>(g.n_experts, g.m_rows)) * n_tiles;
-    if (most > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
-    int wgs = resident_blocks<C, QT, F16>() / kXcds * kXcds;
-    if (wgs < kXcds) return MOE_ERR_HIP;
-    wgs = (int)std::min<int64_t>(wgs, ceil_div(most, kXcds) * kXcds);
-    g.n_tiles = (int)n_tiles;
-    // only for experts of several whole tiles: an expert's last tile then reads its weights once more
-    g.by_size = g.m_rows / g.n_experts >= 4 * C::BP;
-    hipLaunchKernelGGL((b16_gemm_kernel<C, QT, F16>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
-    return launch_status();
-}
-
 using Tile256 = Cfg<256, 256, 2, 4, 2, 1>;
 using Tile128 = Cfg<128, 256, 2, 4, 3, 1>;
 using Tile64 = Cfg<64, 256, 2, 4, 3, 1>;
 using Tile64x64 = Cfg<64, 64, 2, 2, 4, 2>;
 using Tile32x64 = Cfg<32, 64, 1, 4, 8, 1>;
+using TileTail = Cfg<128, 128, 2, 4, 4, 1>;
+static_assert(2 * TileTail::BP == Tile256::BP, "the tail takes the last tiles of at most half the rows");
+
+template <class C, bool QT, bool F16>
+int launch_cfg(hipStream_t st, GemmArgs g) {
+    constexpr bool TAILED = std::is_same_v<C, Tile256>;
+    const int64_t n_tiles = ceil_div(g.N, C::BQ);
+    const int64_t most = (g.m_rows / C::BP + std::min<int64_t>(g.n_experts, g.m_rows)) * n_tiles;
+    if (most > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
+    int wgs = resident_blocks<C, QT, F16, false>() / kXcds * kXcds;
+    if (wgs < kXcds) return MOE_ERR_HIP;
+    wgs = (int)std::min<int64_t>(wgs, ceil_div(most, kXcds) * kXcds);
+    g.n_tiles = (int)n_tiles;
+    // only for experts of several whole tiles: an expert's last tile then reads its weights once more
+    g.by_size = g.m_rows / g.n_experts >= 4 * C::BP;
+    g.main_n_tiles = (int)n_tiles;
+    g.main_wgs = TAILED && g.by_size ? wgs : 0;
+    hipLaunchKernelGGL((b16_gemm_kernel<C, QT, F16, false>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
+    if constexpr (TAILED) {                            // E <= m_rows / 1024, so its tiles are at most half of `most`
+        if (g.main_wgs > 0) {
+            using T = TileTail;
+            g.n_tiles = (int)ceil_div(g.N, T::BQ);
+            int tail = resident_blocks<T, QT, F16, true>() / kXcds * kXcds;
+            if (tail < kXcds) return MOE_ERR_HIP;
+            tail = (int)std::min<int64_t>(tail, ceil_div((int64_t)g.n_experts * g.n_tiles, kXcds) * kXcds);
+            hipLaunchKernelGGL((b16_gemm_kernel<T, QT, F16, true>), dim3((unsigned)tail), dim3(T::THREADS), 0, st, g);
+        }
+    }
+    return launch_status();
+}
 
 template <class C>
 int launch_form(hipStream_t st, bool trans, bool f16, const GemmArgs& g) {

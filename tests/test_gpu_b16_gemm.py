@@ -110,6 +110,39 @@ def test_every_tile_with_unaligned_output(odt, pad):
         check(out.view, ref, sum_bound(K, mag, odt)(ref), "unaligned output")
 
 
+# large tiles whose last tiles of at most 128 rows would open one more round (they go to a launch of their own), rows and N
+# of experts; then the same where a longer last tile opens it anyway
+TAILS = [([2137, 2100, 2062, 1650], 4104), ([4200], 8192), ([0, 1920, 2048, 2100, 2049, 0, 1921, 1600], 4104),
+         ([2137, 2100, 2062, 1737], 4104)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt,odt", [(BF, BF), (FP, F32)])
+@pytest.mark.parametrize("counts,N", TAILS)
+def test_last_tiles_of_a_full_round(counts, N, dt, odt, trans):
+    K = 200
+    assert m.b16_grouped_tile(sum(counts), len(counts), N, K) == (256, 256)
+    grouped(counts, N, K, dt, odt, trans, seed=N, extra=5)
+
+
+def test_last_tiles_keep_non_finite_values_apart_and_replay():
+    counts, N, K = TAILS[0][0], TAILS[0][1], 72
+    R = sum(counts)
+    a, w = randn((R, K), BF, 1).to(dev()), randn((4, N, K), BF, 2, 0.05).to(dev())
+    offs, out = to_dev(offsets_of(counts)), torch.empty((R, N), dtype=BF, device=dev())
+    call = lambda: m.b16_grouped_gemm(a, w, out, mode=m.MOE_MODE_GROUPED, expert_offsets=offs)  # noqa: E731
+
+    def fresh(i):
+        a.copy_(randn((R, K), BF, 10 + i))
+        offs.copy_(to_dev(offsets_of([counts, [R - 6000, 3000, 2900, 100], counts[::-1]][i])))
+        a[R - 1 - i, 3] = float("inf")
+        a[2136 - i, 71] = float("nan")
+
+    for got, eager in replayed(call, None, [out], fresh):
+        assert torch.equal(got[0].nan_to_num(nan=7e4), eager[0].nan_to_num(nan=7e4))
+        assert int((~torch.isfinite(got[0])).any(dim=1).sum()) == 2
+
+
 def test_large_tiles_replayed():
     """The 256 x 256 and 128 x 256 tiles in a graph whose offsets change, some experts empty, then all rows in one."""
     for (R, E, N, K), cuts in (((9000, 4, 1032, 200), [(0, 9000, 9000), (2000, 2100, 6000), (9000, 9000, 9000)]),
