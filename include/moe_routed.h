@@ -524,7 +524,8 @@ int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void*
  *   written unless h is NULL.
  *   in    [rows][in_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32);  h [rows][h_stride] of dt
  *   out_q [rows][q_stride] bytes, out_s [rows][s_stride] fp32
- *   A value v above 1.9375 * 2^127 rounds to 2^128, so code * s of it is an infinity.
+ *   A value v above 1.9375 * 2^127 rounds to 2^128, so code * s of it is an infinity.  A NaN gate gives a NaN in h,
+ *   RELU's as well, and an infinity or NaN leaves its group a scale that may round the others to 0.
  *   Pointers aligned to their types; 16-byte aligned rows with n % 8 == 0 take the vector path.
  */
 int moe_act_checkpoint(const void* in, int dt, int64_t in_stride, int64_t rows, int64_t n, int act, uint8_t* out_q,
@@ -534,7 +535,7 @@ int moe_act_checkpoint(const void* in, int dt, int64_t in_stride, int64_t rows, 
  * moe_gated_act_backward  -- backward of h = act(gate) * up from the saved gate and up
  *   With g, u = code * scale of the two halves (moe_act_checkpoint's layout, any finite scales):
  *     dx[r, c] = dh * u * act'(g),  dx[r, n + c] = dh * act(g),  h[r, c] = act(g) * u (unless h is NULL)
- *   in fp32, rounded to dt.  ReLU's slope at 0 is 0.
+ *   in fp32, rounded to dt.  ReLU's slope at 0 is 0; a NaN gate gives NaN in h, d up and (but for MUL's) d gate.
  *   dh [rows][dh_stride], dx [rows][dx_stride] (2n used), h [rows][h_stride], all of dt (MOE_BF16, MOE_F16 or
  *   MOE_F32); act: moe_act 1..5.  Alignment as moe_act_checkpoint.  An infinity or NaN in dh stays in its dx.
  */

@@ -108,8 +108,8 @@ __device__ __forceinline__ void sigmoid_and_slope(float g, float& f, float& d) {
 // 6 on), so the lower tail is formed as itself.  fp32: erfcf.  16 bits: Phi(-z) = e^(-z^2/2) R(z) with the density's
 // exponential; R falls smoothly from 1/2 like 1/z and is t P(t), t = 1 / (1 + 0.345 z), with P of degree 8 fitted for the
 // least relative error over 0 <= z <= 14.5, where the exponential passes 2^-126 (2.4e-8 in exact arithmetic, 3.5e-7 in
-// fp32).  The backward of 24576 x 1024 fp16
-// rows takes 42.5 us a call so, 55 with erfcf and expf, 46 to 49 with erff and expf.
+// fp32).  The backward of 24576 x 1024 fp16 rows takes 42.5 us a call so, 55 with erfcf and expf, 46 to 49 with erff and
+// expf.
 template <bool EXACT>
 __device__ __forceinline__ void normal_and_density(float g, float& p, float& density) {
     constexpr float kRootHalf = 0.70710678118654752f, kDensity0 = 0.39894228040143268f;
@@ -148,8 +148,8 @@ __device__ __forceinline__ void gate_and_slope(float g, float& f, float& d) {
         f = g * p;
         d = p + g * density;
     } else if constexpr (ACT == 3) {
-        f = g > 0.0f ? g : 0.0f;
-        d = g > 0.0f ? 1.0f : 0.0f;
+        f = g <= 0.0f ? 0.0f : g;                // a NaN stays one, in the slope too
+        d = g > 0.0f ? 1.0f : f;
     } else if constexpr (ACT == 4) {
         sigmoid_and_slope<EXACT>(g, f, d);
     } else {

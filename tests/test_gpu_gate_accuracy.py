@@ -74,3 +74,22 @@ def test_gates_far_from_zero(dt, act):
         check(got, f * u, bound(f * u, ef * u), "h")
     check(dx, np.concatenate([dh * u * d, dh * f], 1),
           np.concatenate([bound(dh * u * d, ed * dh * u), bound(dh * f, ef * dh)], 1), "dx")
+
+
+@pytest.mark.parametrize("act", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("dt", [BF, FP, F32])
+@pytest.mark.parametrize("n", [8, 5])
+def test_a_nan_gate_is_not_lost(n, dt, act):
+    """An overflow upstream has to stay visible behind every activation, in the forward pass and in the gradients."""
+    x = torch.full((3, 2 * n), 2.0, dtype=dt)
+    x[1, 3], x[2, :n] = float("nan"), -1.0
+    q, s = torch.empty((3, 2 * n), dtype=torch.uint8, device=dev()), torch.empty((3, 2), device=dev())
+    h, h2, dx = (torch.empty((3, w), dtype=dt, device=dev()) for w in (n, n, 2 * n))
+    m.act_checkpoint(x.to(dev()), q, s, act=act, h=h)
+    m.gated_act_backward(torch.ones((3, n), dtype=dt, device=dev()), q, s, dx, act=act, h=h2)
+    torch.cuda.synchronize()
+    want = np.zeros((3, n), bool)
+    want[1, 3] = True
+    for got in (h, h2, dx[:, n:]):
+        assert np.array_equal(~np.isfinite(f64(got)), want)
+    assert np.array_equal(~np.isfinite(f64(dx[:, :n])), want & (act != 5))
