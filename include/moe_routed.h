@@ -496,7 +496,8 @@ int moe_b16_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K
  *   a    [m_rows][a_stride] of a_dt: dt, or MOE_E4M3 for rows saved in 8 bits: codes, and a_s
  *        [m_rows][a_s_stride] fp32 scales (ceil(K/128) used).  A saved operand is round_dt(code * scale);
  *        with moe_act_checkpoint's power-of-two scales that product is exact in bf16 (and in fp16 within its
- *        range), with moe_act_quant's it is rounded once to dt.  a_s is ignored otherwise.
+ *        range), with moe_act_quant's it is rounded once to dt.  In fp16 a product past its range is held at 65504,
+ *        so finite rows saved by moe_act_checkpoint stay finite; a NaN code stays a NaN.  a_s is ignored otherwise.
  *   dw   element (e, n, k) at e*dw_stride_e + n*dw_stride_n + k, of dw_dt (MOE_BF16, MOE_F16 or MOE_F32)
  *   expert_offsets as moe_b16_grouped_gemm; rows beyond the last are not read.  Offsets that decrease
  *   are read within bounds, but give gradients that may lack rows.
@@ -524,7 +525,8 @@ int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void*
  *   written unless h is NULL.
  *   in    [rows][in_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32);  h [rows][h_stride] of dt
  *   out_q [rows][q_stride] bytes, out_s [rows][s_stride] fp32
- *   A value v above 1.9375 * 2^127 rounds to 2^128, so code * s of it is an infinity.  A NaN gate gives a NaN in h,
+ *   A value v above 1.9375 * 2^127 rounds to 2^128, so code * s of it is an infinity; fp16's values from 63488 on
+ *   round to 65536, which moe_b16_grouped_wgrad reads as 65504 in fp16.  A NaN gate gives a NaN in h,
  *   RELU's as well, and an infinity or NaN leaves its group a scale that may round the others to 0.
  *   Pointers aligned to their types; 16-byte aligned rows with n % 8 == 0 take the vector path.
  */

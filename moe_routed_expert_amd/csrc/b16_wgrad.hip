@@ -3,7 +3,7 @@
 // loads of b16_tile.h and nothing is transposed in memory.  A may be the 8-bit checkpoint of a forward pass:
 // its e4m3 codes and 1 x 128 scales are read (half the bytes), and each 16-bit operand value
 // round(code * scale) is formed once per workgroup on its way into LDS.  With power-of-two scales
-// (moe_act_checkpoint) that product is exact in bf16 and no rounding is added.
+// (moe_act_checkpoint) that product is exact in bf16 and no rounding is added.  (In fp16 its top value is held in range.)
 //
 // Persistent workgroups walk the tiles of every expert, expert by expert, so experts of unequal length are
 // shared by all of them; an expert without rows gets zeros.  Where the gradient has few tiles and many rows
@@ -85,6 +85,17 @@ struct TSaved {
             scale[j] = *(in ? ss : (const float*)&kZeroPiece);
         }
     }
+    // fp16's values from 63488 on are saved as 65536, which fp16 does not hold: a product past its range is held at 65504,
+    // so that finite rows stay finite.  minimum and maximum keep a NaN.  (As a branch on the few scales that reach there it
+    // broke up the step's schedule: 8 experts, 16384 rows, 8192 x 4096 took 1322 us, with these two instructions a pair
+    // 1162, without them 1172.)
+    __device__ __forceinline__ static uint32_t in_range(uint32_t pair) {
+        if constexpr (!F16) return pair;
+        typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+        const v2h top = {(_Float16)65504.0f, (_Float16)65504.0f};
+        const v2h h = __builtin_elementwise_minimum(__builtin_bit_cast(v2h, pair), top);
+        return __builtin_bit_cast(uint32_t, (v2h)__builtin_elementwise_maximum(h, -top));
+    }
     // Piece j into the stage at dst.
     __device__ __forceinline__ void commit(int j, uint32_t dst, int tid) const {
         const int k = row(j, tid), c = (j * 64 * NW + tid) % PIECES;
@@ -95,8 +106,8 @@ struct TSaved {
         for (int i = 0; i < 4; i++) {
             const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
             const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-            o[2 * i] = pk16<F16 ? kF16 : kBF16>(lo[0] * scale[j], lo[1] * scale[j]);
-            o[2 * i + 1] = pk16<F16 ? kF16 : kBF16>(hi[0] * scale[j], hi[1] * scale[j]);
+            o[2 * i] = in_range(pk16<F16 ? kF16 : kBF16>(lo[0] * scale[j], lo[1] * scale[j]));
+            o[2 * i + 1] = in_range(pk16<F16 ? kF16 : kBF16>(hi[0] * scale[j], hi[1] * scale[j]));
         }
         *(MOE_LDS v4i*)(uintptr_t)at = v4i{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
         *(MOE_LDS v4i*)(uintptr_t)(at + 16) = v4i{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
