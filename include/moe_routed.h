@@ -39,7 +39,8 @@
  *   - Sizes and strides are in ELEMENTS of the buffer they describe (bytes for
  *     fp8 buffers, floats for scale buffers), 64-bit.
  *   - Every output element named in a call is overwritten; outputs never need
- *     to be cleared by the caller.
+ *     to be cleared by the caller (moe_topk_reduce_backward's dy may: rows of
+ *     dropped routes are not named by its call).
  *   - Argument checks are host-side and look at scalars and pointers only.
  *     Device contents are not validated: a slot id >= the number of slots or
  *     offsets that disagree with m_rows are undefined behaviour (the gather's
@@ -453,6 +454,9 @@ int moe_fused_decode_noalloc(const uint16_t* x_bf16, int64_t T, int64_t H, int64
  *               dW2 = moe_b16_grouped_wgrad(dy, h);  dW13 = moe_b16_grouped_wgrad(dc1, x rows, 16 bits or
  *               saved in 8);  dx rows = moe_b16_grouped_gemm(dc1, W13, w_trans), then moe_topk_reduce with
  *               unit weights sums each token's rows.
+ *   Routes that are dropped after moe_route_prep (slots set negative) keep their rows in expert_offsets, and
+ *   moe_topk_reduce_backward with route_rows does not write them: such a step clears dy before that call, in
+ *   every step, or the gradients take up what the rows held before.
  */
 
 /*
@@ -551,8 +555,9 @@ int moe_gated_act_backward(const void* dh, int dt, int64_t dh_stride, const uint
  *     dy[row, 0:H] = weights[t, j] * dout[t, 0:H] (fp32, rounded to y_dt)
  *     dweights[t, j] = sum_h dout[t, h] * y[row, h] (fp32, in a fixed order)
  *   Any other route gets dweights = +0 and reads neither its weight nor y; its dy row is +0 when route_rows is
- *   NULL (the row t*topk + j exists), and with route_rows it has no row.  Rows that no route names are left as
- *   they were; active routes name distinct rows.
+ *   NULL (the row t*topk + j exists), and with route_rows it has no row (its entry is not read).  Rows that no
+ *   active route names are then left as they were: clear dy first if a later product counts them.  Active routes
+ *   name distinct rows.
  *   dout [T][dout_stride] bf16;  y [y_rows][y_stride] and dy [y_rows][dy_stride] of y_dt;  slot_ids, weights,
  *   dweights [T][topk];  route_rows as moe_topk_reduce (DEVICE int32 [T*topk] or NULL).
  *   dweights may be NULL (a router that is not trained); y is then not read and may be NULL.

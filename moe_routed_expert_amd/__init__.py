@@ -492,7 +492,8 @@ def gated_act_backward(dh, q, s, dx, act=MOE_ACT_SILU_MUL, h=None, stream=None):
 
 def topk_reduce_backward(dout, y, slot_ids, weights, dy, dweights=None, route_rows=None, stream=None):
     """Backward of topk_reduce: dy[row(t,j)] = weights[t,j] * dout[t], dweights[t,j] = <dout[t], y[row(t,j)]>.
-    dout [T, H] bf16; y (None when dweights is None) and dy [rows, H] of one type."""
+    dout [T, H] bf16; y (None when dweights is None) and dy [rows, H] of one type.  With route_rows the rows of dropped
+    routes (negative slots) are left as they were: call dy.zero_() first if expert offsets count them."""
     routes = slot_ids.shape
     T, topk = routes
     rows, H = dy.shape
