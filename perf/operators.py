@@ -365,6 +365,8 @@ def _own(s, c):
             return dict(codes=s["q"].view(torch.float8_e4m3fn), scales=s["s"])
         m.act_checkpoint(s["x"], s["q"], s["s"], act=ACTS[c["act"]], h=s["h"])
         return dict(h=s["h"], codes=s["q"].view(torch.float8_e4m3fn), scales=s["s"])
+    if c["mapped"] and c["off"]:
+        s["dy"].zero_()                                   # a step that drops routes clears their rows every time
     m.topk_reduce_backward(s["dout"], s["y"], s["slots"], s["weights"], s["dy"], s["dweights"],
                            route_rows=s["route_rows"])
     m.route_prep_backward(s["ids"], s["weights"], s["dweights"], s["dlogits"])
