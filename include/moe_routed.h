@@ -487,8 +487,8 @@ int moe_b16_grouped_gemm(const void* a, int64_t a_stride, const void* w, int64_t
  * moe_b16_grouped_tile
  *   The output tile (rows, columns) that moe_b16_grouped_gemm's grouped mode takes for m_rows rows over n_experts
  *   experts: the one of 32 x 64, 64 x 64, 64 x 256, 128 x 256 and 256 x 256 with the least estimated time.  (The
- *   largest leaves its experts' short last tiles to a second launch where they alone would cost a round more.)  Pure
- *   function of its arguments; MOE_ERR_SHAPE for those the product rejects or has no work for.
+ *   largest leaves its experts' short last tiles to a second launch where with them it would take more rounds.)
+ *   Pure function of its arguments; MOE_ERR_SHAPE for those the product rejects or has no work for.
  */
 int moe_b16_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K, int32_t tile[2]);
 

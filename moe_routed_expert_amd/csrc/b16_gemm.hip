@@ -51,12 +51,15 @@ struct GemmArgs {
     int64_t out_stride;               // elements
 };
 
-// TAIL: the launch behind a by_size one of tiles twice as high.  It takes the last tiles of at most C::BP rows where
-// they alone would cost the main launch one more round, and is empty otherwise; both find out from the offsets.  Few
-// of the 256 x 256 tiles are then left, with one step in flight each, so their round waits for memory; 128 x 128
+// TAIL: the launch behind a by_size one of tiles twice as high.  It takes all last tiles of at most C::BP rows where with
+// them the main launch would need more rounds than without, one or several, and is empty otherwise; both find out from
+// the offsets.  A last round of few 256 x 256 tiles, with one step in flight each, waits for memory; 128 x 128
 // tiles with three in flight share it among more workgroups: 8 experts of ragged rows, 16384 x 8192 to 4096 1026 -> 964
 // us, one of 4200 rows, 8192 x 8192 544 -> 462, 16 of 2048 rows, 2048 x 2048 250 -> 252.  (Tail tiles of 128 x 256:
-// 982 us, 481, 245.)  An empty tail costs about 1 % of 250 us.
+// 982 us, 481, 245.)  An empty tail costs about 1 % of 250 us.  Whole rounds of short tiles gain a little too: experts of
+// 1100 rows, NT, in the tail and (where that holds no more than one round) in the main launch, 16 of 4096 x 4096 557 and
+// 575 us, 32 of 2048 x 4096 565 and 585, 64 of them 1119 - 1199 and 1171 - 1177, 256 of 4096 x 2048 4718 and 4852; least
+// where most of them would have fitted a round that is there already: 64 ragged experts (8.5 rounds and 1.1) 1179 and 1161.
 template <class C, bool QT, bool F16, bool TAIL>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_gemm_kernel(const GemmArgs g) {
     using P = KMajor<C::BP, C::NW>;
