@@ -472,7 +472,9 @@ int moe_fused_decode_noalloc(const uint16_t* x_bf16, int64_t T, int64_t H, int64
  *        [expert_offsets[e], expert_offsets[e+1]) use expert e and A row r, offsets are clamped to [0, m_rows],
  *        rows beyond the last are left untouched, any number of rows per expert (none included); offsets that
  *        decrease somewhere leave all of out untouched.  Slot:
- *        w_trans = 0 only; a slot outside [0, n_experts) writes a +0 row and reads nothing of that row.
+ *        w_trans = 0 only; a slot outside [0, n_experts) writes a +0 row and reads nothing of that row; and
+ *        m_rows * ceil(N / 16) < 2^24 up to K = 1024, m_rows * ceil(N / 8) < 2^24 beyond (the workgroups of one
+ *        launch; MOE_ERR_SHAPE).
  *   An infinity or NaN in a row of A or W reaches exactly the outputs whose sums hold it.
  *   Requirements: N % 8 == 0, K % 8 == 0, 8 <= N, K <= 2^20, m_rows <= 2^31 - 1, 1 <= n_experts <= 1024 in
  *   grouped mode (0 allowed in slot mode, with NULL a and w); a, w and their strides 16-byte aligned; out
