@@ -505,8 +505,8 @@ int moe_b16_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K
  *        range), with moe_act_quant's it is rounded once to dt.  In fp16 a product past its range is held at 65504,
  *        so finite rows saved by moe_act_checkpoint stay finite; a NaN code stays a NaN.  a_s is ignored otherwise.
  *   dw   element (e, n, k) at e*dw_stride_e + n*dw_stride_n + k, of dw_dt (MOE_BF16, MOE_F16 or MOE_F32)
- *   expert_offsets as moe_b16_grouped_gemm; rows beyond the last are not read.  Offsets that decrease
- *   are read within bounds, but give gradients that may lack rows.
+ *   expert_offsets as moe_b16_grouped_gemm: rows beyond the last are not read, and offsets that decrease
+ *   somewhere leave all of dw untouched.
  *   workspace: moe_b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K) bytes, 16-byte aligned, no
  *   initialization; 0 bytes (NULL allowed) unless the gradient has few tiles and long row ranges, which are
  *   then cut and their fp32 parts summed in order.  Scratch within one call: overlapping calls need their own.

@@ -129,6 +129,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) b16_wgrad_kernel(
     const int per = g.n_tiles * g.k_tiles;
     for (int e = tid; e <= g.n_experts; e += C::THREADS) first_row[e] = min(max(g.offsets[e], 0), g.m_rows);
     __syncthreads();
+    // Offsets that decrease name rows twice: nothing is written, as in the products.  (Every wave looks at all of them.)
+    bool decreases = false;
+    for (int e = lane; e < g.n_experts; e += kWave) decreases |= first_row[e + 1] < first_row[e];
+    if (__any(decreases)) return;
     int chunks = g.n_experts;
     if (g.chunk_rows > 0) {
         constexpr int EPT = kMaxExperts / C::THREADS;
@@ -296,23 +300,35 @@ wgrad_join_kernel(const float* __restrict__ part, const int32_t* __restrict__ of
                   int max_chunks, int64_t N, int64_t K, void* __restrict__ out, int64_t stride_e, int64_t stride_n,
                   int accumulate) {
     constexpr int THREADS = SPLIT == 1 ? 256 : 64 * SPLIT, OWN = THREADS / SPLIT;      // elements (of four) a workgroup
-    __shared__ int wave_sum[THREADS / kWave];
+    __shared__ int wave_sum[THREADS / kWave], wave_decreases[THREADS / kWave];
     __shared__ v4f others[SPLIT == 1 ? 1 : SPLIT][SPLIT == 1 ? 1 : OWN];
     const int e = blockIdx.y, tid = threadIdx.x;
-    auto chunks_of = [&](int x) {
+    auto chunks_of = [&](int x, bool& decreases) {
         const int lo = min(max(offsets[x], 0), m_rows), hi = min(max(offsets[x + 1], 0), m_rows);
+        decreases |= hi < lo;
         return pieces(max(hi - lo, 0), chunk_rows);
     };
     int before = 0;
-    for (int x = tid; x < e; x += THREADS) before += chunks_of(x);
+    bool decreases = false;                            // then there are no parts, and nothing is written
+    for (int x = tid; x < (int)gridDim.y; x += THREADS) {
+        const int n = chunks_of(x, decreases);
+        before += x < e ? n : 0;
+    }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d, kWave);
-    if (tid % kWave == 0) wave_sum[tid / kWave] = before;
+    const bool any = __any(decreases);
+    if (tid % kWave == 0) {
+        wave_sum[tid / kWave] = before;
+        wave_decreases[tid / kWave] = any;
+    }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / kWave; i++)
+        if (wave_decreases[i]) return;
     int first = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / kWave; i++) first += wave_sum[i];
-    int last = min(first + chunks_of(e), max_chunks);
+    int last = min(first + chunks_of(e, decreases), max_chunks);
     const int lane = tid % OWN, share = SPLIT == 1 ? 0 : tid / OWN;
     if constexpr (SPLIT > 1) {
         const int run = (max(last - first, 0) + SPLIT - 1) / SPLIT;
