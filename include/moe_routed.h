@@ -515,6 +515,9 @@ int moe_b16_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K
  *   m_rows == 0 still writes the zeros (dy and a may be NULL).
  */
 size_t moe_b16_grouped_wgrad_workspace_size(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K);
+/* How moe_b16_grouped_wgrad takes such a problem: plan = {tile rows (N), tile columns (K), rows of a chunk or 0 where
+ * the experts' rows stay whole}; tiles are 128 x 128, 256 x 128 and 256 x 256.  Pure function of its arguments. */
+int moe_b16_grouped_wgrad_plan(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K, int32_t plan[3]);
 int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void* a, int64_t a_stride, int a_dt,
                           const float* a_s, int64_t a_s_stride, const int32_t* expert_offsets, int64_t n_experts,
                           int64_t N, int64_t K, int64_t m_rows, void* dw, int dw_dt, int64_t dw_stride_e,

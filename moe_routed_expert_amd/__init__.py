@@ -34,6 +34,7 @@ EXPORTS = (
     "moe_route_prep_workspace_size", "moe_route_prep", "moe_bf8_grouped_gemm_act_quant",
     "moe_mxfp4_grouped_gemm", "moe_mxfp4_grouped_gemm_act_quant", "moe_fused_decode_noalloc", "moe_pack_weights",
     "moe_grouped_block_m", "moe_b16_grouped_gemm", "moe_b16_grouped_tile", "moe_b16_grouped_wgrad", "moe_b16_grouped_wgrad_workspace_size",
+    "moe_b16_grouped_wgrad_plan",
     "moe_act_checkpoint", "moe_gated_act_backward", "moe_topk_reduce_backward", "moe_route_prep_backward",
 )
 
@@ -88,6 +89,7 @@ def lib():
                                       P], I32),
             "moe_b16_grouped_tile": ([I64, I64, I64, I64, P], I32),
             "moe_b16_grouped_wgrad_workspace_size": ([I64, I64, I64, I64], SZ),
+            "moe_b16_grouped_wgrad_plan": ([I64, I64, I64, I64, P], I32),
             "moe_b16_grouped_wgrad": ([P, I64, I32, P, I64, I32, P, I64, P, I64, I64, I64, I64, P, I32, I64, I64, I32,
                                        P, SZ, P], I32),
             "moe_act_checkpoint": ([P, I32, I64, I64, I64, I32, P, I64, P, I64, P, I64, P], I32),
@@ -405,6 +407,13 @@ def b16_grouped_tile(m_rows, n_experts, N, K):
 def b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K) -> int:
     """Bytes of workspace b16_grouped_wgrad needs (0: none)."""
     return lib().moe_b16_grouped_wgrad_workspace_size(m_rows, n_experts, N, K)
+
+
+def b16_grouped_wgrad_plan(m_rows, n_experts, N, K):
+    """(tile rows, tile columns, rows of a chunk or 0) that b16_grouped_wgrad takes."""
+    t = (ctypes.c_int32 * 3)()
+    _check("moe_b16_grouped_wgrad_plan", lib().moe_b16_grouped_wgrad_plan(m_rows, n_experts, N, K, t))
+    return tuple(t)
 
 
 def b16_grouped_wgrad(dy, a, expert_offsets, dw, *, a_s=None, m_rows=None, accumulate=False, workspace=None,

@@ -493,6 +493,16 @@ extern "C" size_t moe_b16_grouped_wgrad_workspace_size(int64_t m_rows, int64_t n
     return rows > 0 ? (size_t)b16::wgrad_max_chunks(m_rows, n_experts, rows) * N * K * 4 : 0;
 }
 
+extern "C" int moe_b16_grouped_wgrad_plan(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K, int32_t plan[3]) {
+    if (!plan) return MOE_ERR_NULL;
+    if (!b16::wgrad_shape_ok(m_rows, n_experts, N, K)) return MOE_ERR_SHAPE;
+    const b16::WgradPlan p = b16::wgrad_plan(m_rows, n_experts, N, K);
+    plan[0] = b16::kWgradCosts[p.tile].bp;
+    plan[1] = b16::kWgradCosts[p.tile].bq;
+    plan[2] = p.chunk_rows;
+    return MOE_OK;
+}
+
 extern "C" int moe_b16_grouped_wgrad(const void* dy, int64_t dy_stride, int dt, const void* a, int64_t a_stride,
                                      int a_dt, const float* a_s, int64_t a_s_stride, const int32_t* expert_offsets,
                                      int64_t n_experts, int64_t N, int64_t K, int64_t m_rows, void* dw, int dw_dt,
