@@ -134,14 +134,12 @@ template <int T, int NW>
 struct KMajor {
     static constexpr int BYTES = T * kStep * 2;
     static constexpr int GROUPS = T / 8;                                    // 8-row groups, one DMA each
-    static constexpr int LOADS = (GROUPS + NW - 1) / NW;                    // per wave and step
-    static_assert(GROUPS % NW == 0 || NW % GROUPS == 0, "waves cover the rows evenly");
+    static constexpr int LOADS = GROUPS / NW;                               // per wave and step
+    static_assert(GROUPS % NW == 0, "waves cover the rows evenly");
     const char* p[LOADS];
     int k0;                                                                 // first k of this lane's pieces
 
-    // With fewer groups than waves the waves repeat each other's groups (the same bytes to the same place), so
-    // every wave has the same number of loads in flight.
-    __device__ __forceinline__ static int group(int j, int wave) { return GROUPS < NW ? wave % GROUPS : j * NW + wave; }
+    __device__ __forceinline__ static int group(int j, int wave) { return j * NW + wave; }
 
     // Rows base + r * stride (bytes); rows from `valid` on repeat the last one (their results are dropped).
     __device__ __forceinline__ void set(const void* base, int64_t stride, int valid, int wave, int lane) {
