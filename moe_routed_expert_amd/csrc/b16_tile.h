@@ -56,10 +56,10 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 
 // 64 lanes x 16 bytes from each lane's src to the LDS bytes [dst, dst + 1024) in lane order.  The instruction
 // writes no register, so nothing the compiler allocates can be overwritten by it; its completion is waited for
-// with wait_loads before the barrier that publishes the stage.  m0 holds the LDS address and nothing else in
-// these kernels uses it; the s_nop is the wait state between an m0 write and an LDS-direct load.
+// with wait_loads before the barrier that publishes the stage.  m0 holds the LDS address, and the compiler is told so:
+// it keeps nothing of its own there; the s_nop is the wait state between an m0 write and an LDS-direct load.
 __device__ __forceinline__ void dma16(const void* src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }
 
 // Waits until at most N of this wave's vector memory operations are in flight (they retire in order).
