@@ -501,8 +501,9 @@ int moe_b16_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K
  *   dy   [m_rows][dy_stride] of dt (MOE_BF16 or MOE_F16), N used
  *   a    [m_rows][a_stride] of a_dt: dt, or MOE_E4M3 for rows saved in 8 bits: codes, and a_s
  *        [m_rows][a_s_stride] fp32 scales (ceil(K/128) used).  A saved operand is round_dt(code * scale);
- *        with moe_act_checkpoint's power-of-two scales that product is exact in bf16 (and in fp16 within its
- *        range), with moe_act_quant's it is rounded once to dt.  In fp16 a product past its range is held at 65504,
+ *        with moe_act_checkpoint's power-of-two scales that product is exact in bf16 for scales of 2^-124 and more
+ *        (below, products under 2^-133, bf16's least value, round once more), and in fp16 within its range; with
+ *        moe_act_quant's it is rounded once to dt.  In fp16 a product past its range is held at 65504,
  *        so finite rows saved by moe_act_checkpoint stay finite; a NaN code stays a NaN.  a_s is ignored otherwise.
  *   dw   element (e, n, k) at e*dw_stride_e + n*dw_stride_n + k, of dw_dt (MOE_BF16, MOE_F16 or MOE_F32)
  *   expert_offsets as moe_b16_grouped_gemm: rows beyond the last are not read, and offsets that decrease

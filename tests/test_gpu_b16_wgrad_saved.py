@@ -56,3 +56,20 @@ def test_values_past_fp16_are_held_and_nan_stays():
         assert np.isnan(got[7]) and np.isnan(got[9])
         assert got[0] == np.clip(scale, -65504, 65504)
         assert got[5] == np.clip(448 * scale, -65504, 65504) and got[11] == np.clip(-448 * scale, -65504, 65504)
+
+
+@pytest.mark.parametrize("e", [-126, -125, -124, -123])
+def test_the_least_scales(e):
+    """code * scale is a bf16 value from a scale of 2^-124 on; below, it is rounded to bf16's least step, 2^-133."""
+    rng = np.random.default_rng(0)
+    codes = rng.integers(0, 256, (3, 256)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 1
+    codes[0, :8] = [1, 2, 3, 0x81, 4, 5, 0x83, 8]                       # the smallest codes: multiples of 2^-9
+    q, s = to_dev(codes), torch.full((3, 2), 2.0 ** e, device=dev())
+    dy = torch.diag(torch.full((8,), 2.0 ** 100))[:3].to(BF)            # row r of the gradient is 2^100 times row r
+    dw = torch.empty((1, 8, 256), dtype=F32, device=dev())
+    m.b16_grouped_wgrad(dy.to(dev()), q, to_dev(np.array([0, 3], np.int32)), dw, a_s=s)
+    v = torch.from_numpy(codes).view(torch.float8_e4m3fn).double() * 2.0 ** e
+    held = v.to(BF).double()
+    assert torch.equal(held, v) == (e >= -124)
+    assert np.array_equal(f64(dw)[0, :3], (held * 2.0 ** 100).numpy()) and not f64(dw)[0, 3:].any()
