@@ -347,11 +347,12 @@ _UNIT = "unit column stride expected"
 
 def _call(fn, tensors, args, stream):
     """Calls C entry point fn(*args, stream) for tensors of one GPU, with that GPU current; stream None is its
-    current stream."""
+    current stream, any other has to be one of that GPU's."""
     dev = tensors[0].get_device()
     assert dev >= 0, "tensors on a GPU expected"
     for t in tensors:
         assert t is None or t.get_device() == dev, "tensors of one GPU expected"
+    assert stream is None or stream.device.index == dev, "a stream of the tensors' GPU expected"
     f = _entry.get(fn) or _entry.setdefault(fn, getattr(lib(), fn))
     if dev == _current_device():
         st = f(*args, _current_stream(dev) if stream is None else stream.cuda_stream)
