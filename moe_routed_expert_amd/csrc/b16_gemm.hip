@@ -11,11 +11,11 @@
 //  * Tiles are numbered in panels of kPanel M tiles, M fastest, and tile t of round s goes to workgroup t % G
 //    with the workgroups of one XCD next to each other: the tiles that an XCD works on at one time form a
 //    patch whose A rows and weight columns meet in its L2.
-//  * Bound by the bank's bytes where experts have few rows: 256 experts of 2048 x 4096 and 24576 rows take 742 us
-//    (6.2 TB/s over banks, rows and output).  Bound by the MFMAs' feed where they have many: 8 experts of 2048 rows,
+//  * Bound by the bank's bytes where experts have few rows: 256 experts of 2048 x 4096 and 24576 rows take 754 us
+//    (6.1 TB/s over banks, rows and output).  Bound by the MFMAs' feed where they have many: 8 experts of 2048 rows,
 //    4096 x 8192 take 860 us (1.28 PFLOP/s; the matrix units are busy two thirds of the cycles, and zeros as data
-//    take 771 us).  Bound by latency where there is little: 333 rows over 16 experts, 1000 x 520 take 9.5 us, of which
-//    6.5 are there at K = 8 already.
+//    take 771 us).  Bound by latency where there is little: 333 rows over 16 experts, 1000 x 520 take 10.3 us a call and 9.5
+//    in a graph of such calls, of which 6.4 are there at K = 8 already.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -336,9 +336,9 @@ int launch_form(hipStream_t st, bool trans, bool f16, const GemmArgs& g) {
 // The tile is the one with the least estimated time, in us: rounds of workgroups times (k steps times a step's time
 // plus 4 for a tile's start and stores), but no less than the bytes at 5.7 TB/s.  A step's time and the workgroups
 // that the device's 256 CUs hold are measured per tile; the tiles are estimated from rows per expert alone, since
-// the counts are on the device.  Over 36 problems from 1 to 24576 rows and 1 to 256 experts the choice took 3 % more
-// time than the best tile in the mean and 12 % at most; a rule by rows per expert alone (16, 64, 128, 256 rows a tile
-// up to 16, 64, 256 and more) took 31 % more in the mean and 2.8 times at most.
+// the counts are on the device.  Over 36 problems from 1 to 24576 rows and 1 to 256 experts the choice took 1.6 % more
+// time than the best tile in the mean and 14 % at most; a rule by rows per expert alone (64, 128, 256 rows a tile up to
+// 64, 256 and more) 25 % more in the mean and 2.9 times at most.
 struct TileCost {
     int bp, bq, slots;
     double step;

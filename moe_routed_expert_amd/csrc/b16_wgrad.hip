@@ -13,8 +13,10 @@
 // and read once more, so a cut pays only where the device would be far from full.
 //
 // Two transposing reads a fragment and both operands' loads bound it where experts have many rows (8 experts, 16384
-// rows, 8192 x 4096 in fp32: 995 us, 1.10 PFLOP/s), the gradient's stores where they have few (256 experts, 24576 rows
-// from 8 bits, 2048 x 4096 in bf16: 1240 us for 4.3 GB, which a kernel of such stores alone writes in 772 us).
+// rows, 8192 x 4096 in fp32: 1000 us, 1.10 PFLOP/s), the gradient's stores where they have few (256 experts, 24576 rows
+// from 8 bits, 2048 x 4096 in bf16: 1235 us for 4.3 GB, which a kernel of such stores alone writes in 772 us).
+// A gradient that is added on is read element by element and stored by half lines: on one set of inputs the first takes
+// 1000 us written and 1170 added on, the second 1040 and 3060.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -439,9 +441,8 @@ constexpr WgradCost kWgradCosts[] = {{128, 128, 512, 0.80, 1.07}, {256, 128, 256
 // ranges are taken as 1.12 of the average expert's, 1.35 where one round has to wait for the longest (the counts are
 // on the device); a cut adds half a chunk an expert.  Chunks are tried that fill the device once or twice, and the
 // length at which steps and join would balance.  A tenth of the work is added so that tiles bound by the same bytes are
-// told apart.  Over 42 problems from 2 to 100000 rows and 1 to 224 experts the plan took 3 % more time than the best of
-// all tiles and chunk lengths in the mean and 17 % at most; cutting whenever the 128 x 128 tiles left the device
-// unfilled took 13 % more over 18 of them and 44 % at most (2 x 4096 rows of 2048 x 1024: 82 us against 59 whole).
+// told apart.  Over 42 problems from 2 to 100000 rows and 1 to 224 experts the plan took 2.1 % more time than the best of
+// all tiles and chunk lengths in the mean and 12 % at most.
 WgradPlan wgrad_plan(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     const double R = (double)m_rows, E = (double)n_experts, NK = (double)N * (double)K;
     WgradPlan best{0, 0};
