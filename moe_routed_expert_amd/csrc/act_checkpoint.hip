@@ -3,7 +3,8 @@
 // moe_act_checkpoint saves rows as e4m3 codes with one scale per 1 x 128 group, as moe_act_quant does, but the
 // scale is a power of two: the smallest s with amax / s <= 448.  A division by s and a product with s are then
 // exact, so a value has one rounding (3 mantissa bits) and code * s is a bf16 value (from s = 2^-124 on), which the
-// weight gradient takes as an operand without a second rounding.  The cost is at most one bit of range at a group's small end.
+// weight gradient takes as an operand without a second rounding.  The cost is at most one bit of range at a group's
+// small end.
 // The gated forms save [gate | up] of the gate/up product and write h = act(gate) * up beside it, in one pass.
 // moe_gated_act_backward reads dh and the saved gate and up, and forms d gate = dh up act'(gate),
 // d up = dh act(gate) and, for the down projection's weight gradient, h again, so the forward keeps no h.

@@ -454,7 +454,7 @@ b16_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
 template <bool F16, int COLS, int UNROLL>
 int slot_launch_cols(hipStream_t st, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
     const int64_t groups = ceil_div(g.N, COLS * kSlotWaves);
-    if (groups * g.m_rows >= ((int64_t)1 << 32) / (64 * kSlotWaves)) return MOE_ERR_SHAPE;   // a grid's threads fit 32 bits (in the header)
+    if (groups * g.m_rows >= ((int64_t)1 << 32) / (64 * kSlotWaves)) return MOE_ERR_SHAPE;   // a grid's threads fit 32 bits
     hipLaunchKernelGGL((b16_slot_kernel<F16, COLS, UNROLL>), dim3((unsigned)(groups * g.m_rows)), dim3(64 * kSlotWaves), 0, st, g,
                        slots, a_row_div, (int)groups);
     return launch_status();

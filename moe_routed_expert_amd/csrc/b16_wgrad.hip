@@ -3,7 +3,8 @@
 // loads of b16_tile.h and nothing is transposed in memory.  A may be the 8-bit checkpoint of a forward pass:
 // its e4m3 codes and 1 x 128 scales are read (half the bytes), and each 16-bit operand value
 // round(code * scale) is formed once per workgroup on its way into LDS.  With power-of-two scales
-// (moe_act_checkpoint; from 2^-124 on) that product is exact in bf16 and no rounding is added.  (In fp16 its top value is held in range.)
+// (moe_act_checkpoint; from 2^-124 on) that product is exact in bf16 and no rounding is added.  (In fp16
+// its top value is held in range.)
 //
 // Persistent workgroups walk the tiles of every expert, expert by expert, so experts of unequal length are
 // shared by all of them; an expert without rows gets zeros.  Where the gradient has few tiles and many rows
