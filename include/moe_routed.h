@@ -586,6 +586,133 @@ int moe_topk_reduce_backward(const uint16_t* dout_bf16, int64_t dout_stride, con
 int moe_route_prep_backward(const int32_t* expert_ids, const float* weights, const float* dweights, int64_t T,
                             int64_t E, int64_t topk, float* dlogits, int64_t dlogits_stride, void* stream);
 
+/*
+ * The router in its general form, and experts in MXFP4 on both sides
+ *   The entry points from here on are not steps of the pages' method either.  moe_router is moe_route_prep with sigmoid or
+ *   softmax scores, a balance bias, expert groups, masked experts and 16-bit logits, moe_router_backward its gradient.
+ *   moe_mx4_* serve experts whose weights and activations are both MXFP4 (E2M1 codes, two a byte with the even element in
+ *   the low nibble, one E8M0 scale byte per 32 elements: the format of moe_mxfp4_grouped_gemm's weights).  A prefill step is
+ *     moe_router(logits);  xq = moe_mx4_quant(x);
+ *     hq = moe_mx4_grouped_gemm_act_quant(xq, W13, a_rows = dst2src);  y = moe_mx4_grouped_gemm(hq, W2);
+ *     out = moe_topk_reduce(y, slot_ids = expert_ids, route_rows)
+ *   and a decode step the same in MOE_MODE_SLOT with slot_ids = expert_ids and a_row_div = topk instead of the maps.
+ */
+
+/* Scores of a router: s = softmax(logits) over the experts, or 1 / (1 + exp(-logit)) of each. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+/* Scale of an MXFP4 group: 2^(floor(log2 amax) - 2) (OCP MX; values above 6 scales saturate), or the least power of two
+ * that holds amax without saturation (amax <= 6 scales). */
+typedef enum { MOE_MX_FLOOR = 0, MOE_MX_CEIL = 1 } moe_mx_rule;
+
+/*
+ * moe_router  -- scores, choice, weights and route maps
+ *   logits   DEVICE [T][logits_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32), E used.  -inf and NaN mask their expert for that
+ *            token (its score is 0); +inf counts as fp32's largest value.
+ *   s        scores of the logits (moe_score).  The masked experts take no part in the softmax.
+ *   c        choices s + bias (bias DEVICE fp32 [E]; a bias of -inf or NaN takes its expert from every choice), or, with bias
+ *            NULL, the order of the logits themselves.
+ *   groups   n_group groups of E / n_group consecutive experts; a group's value is its largest choice (group_top = 1) or
+ *            the sum of its two largest (group_top = 2; a group with one choosable expert: that one's).  The topk_group
+ *            groups of largest value stay.  (topk_group = n_group, as n_group = 1: all stay.)
+ *   expert_ids [T][topk] int32: the topk largest choices in the groups that stay, descending; -1 where no choosable
+ *            expert is left (an inactive route for every other entry point).
+ *   weights  [T][topk] fp32: scale * s_j, or scale * s_j / sum_i s_i over the token's routes (renorm = 1; formed as
+ *            ratios, so scores that underflow still divide); +0 where the id is -1.
+ *   scores   [T][E] fp32: s, for an auxiliary loss; NULL: not wanted.
+ *   Ties go to the lower index, of experts and of groups.  Choices and sums of two are formed in 64 bits and rounded to 43
+ *   significant bits for the comparison.
+ *   dst2src, route_rows [T*topk], expert_offsets [E+1] int32: the route maps of moe_route_prep over the active routes;
+ *   inactive routes have no row: their route_rows entry is -1, and the expert_offsets[E] rows are followed by dst2src
+ *   entries of -1 (moe_gather_rows_scales and a_rows take these as rows of zeros).  All three NULL: not wanted.
+ *   workspace: moe_router_workspace_size(T, E) bytes, 16-byte aligned, no initialization; 0 bytes (NULL allowed) up to
+ *   64 tokens, and not used without maps.  Scratch within one call: overlapping calls need their own.
+ *   Requirements: T <= 2^27, 1 <= E <= 1024, 1 <= topk <= min(E, 64), T * topk < 2^31; n_group <= 64 divides E,
+ *   topk_group * (E / n_group) >= topk; scale positive and finite.  T == 0 with maps writes the zero offsets.
+ */
+size_t moe_router_workspace_size(int64_t T, int64_t E);
+int moe_router(const void* logits, int dt, int64_t logits_stride, int64_t T, int64_t E, int64_t topk, int score,
+               const float* bias, int64_t n_group, int64_t topk_group, int group_top, int renorm, float scale,
+               int32_t* expert_ids, float* weights, float* scores, int32_t* dst2src, int32_t* route_rows,
+               int32_t* expert_offsets, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_router_backward  -- gradient of the logits from the weights' and the scores'
+ *   With n_j = w_j / scale and the sums over the token's routes (ids outside [0, E) are left out):
+ *     renorm, softmax:  dl[e_j] += scale n_j (dw_j - sum_i n_i dw_i);   sigmoid: the same times (1 - s_j)
+ *     not renorm:       u[e_j] += scale dw_j
+ *   and u[e] += dscores[t, e] unless dscores is NULL; then dl[e] += s_e (u_e - sum_i s_i u_i) (softmax) or
+ *   u_e s_e (1 - s_e) (sigmoid).  Masked experts' entries are +0.  bias and groups choose, they have no gradient.
+ *   logits as moe_router's;  expert_ids, weights, dweights [T][topk];  dscores fp32 [T][dscores_stride], stride 0: one
+ *   row for all tokens (an auxiliary loss on the batch's mean scores);  dlogits [T][dlogits_stride] of dt, E written.
+ *   score, renorm, scale as in the forward call.  fp32 inside.  T == 0 launches nothing.
+ */
+int moe_router_backward(const void* logits, int dt, int64_t logits_stride, const int32_t* expert_ids, const float* weights,
+                        const float* dweights, const float* dscores, int64_t dscores_stride, int64_t T, int64_t E,
+                        int64_t topk, int score, int renorm, float scale, void* dlogits, int64_t dlogits_stride,
+                        void* stream);
+
+/*
+ * moe_mx4_quant  -- rows, or a gated activation of them, to MXFP4
+ *   act = MOE_ACT_IDENTITY: v = in[r, c];  moe_act 1..5: in row is [gate(0:n) | up(n:2n)], v = act(gate) * up in fp32.
+ *   Per group of 32 columns (the last may be shorter): scale by `rule` (moe_mx_rule), at least 2^-127 (byte 0, also that
+ *   of a group of zeros); codes e2m1_rne(v / scale), the quotient exact, saturating at 6.  Bit-exact for IDENTITY, RELU and
+ *   MUL; the transcendental gates are within a few ulp of their fp32 value.  A group that holds an infinity or NaN takes
+ *   scale byte 255 (NaN) and codes 0: every value of it reads as NaN.
+ *   in [rows][in_stride] of dt;  out_q [rows][q_stride] bytes, n/2 written;  out_s [rows][s_stride] bytes, ceil(n/32) written.
+ *   Requirements: n even; in aligned to its type.  16-byte aligned rows with n % 8 == 0 and 4-byte aligned code rows take
+ *   the vector path.  The products want scale rows at multiples of 4 bytes.
+ */
+int moe_mx4_quant(const void* in, int dt, int64_t in_stride, int64_t rows, int64_t n, int act, int rule,
+                  uint8_t* out_q, int64_t q_stride, uint8_t* out_s, int64_t s_stride, void* stream);
+
+/*
+ * moe_mx4_dequant  -- MXFP4 rows back to values
+ *   out[r, c] = code * scale, rounded once to out_dt: exact in fp32 (subnormals included) and bf16 (scales of 2^-126 and
+ *   more); fp16 overflows to infinity past 65504.  NaN under scale byte 255.  Layouts as moe_mx4_quant.
+ */
+int moe_mx4_dequant(const uint8_t* q, int64_t q_stride, const uint8_t* s, int64_t s_stride, int64_t rows, int64_t n,
+                    void* out, int out_dt, int64_t out_stride, void* stream);
+
+/*
+ * moe_mx4_grouped_gemm  -- the expert GEMM with MXFP4 on both sides
+ *   out[r, n] = sum_k A[ar, k] 2^(a_s[ar, k/32] - 127) W[e, n, k] 2^(w_s[e, n, k/32] - 127), products exact, sums in fp32
+ *   (the MFMA's, within 2^-23 of the sum of magnitudes per 128 products), one rounding to out_dt.
+ *   a_q  [a_n][a_stride] codes (K/2 used), a_s [a_n][a_s_stride] scale bytes (K/32 used)
+ *   w_q  codes of (e, n) at e*w_stride_e + n*w_stride_n, w_s scale bytes at e*w_s_stride_e + n*w_s_stride_n
+ *   mode, expert_offsets, slot_ids, m_rows: as moe_b16_grouped_gemm (offsets that decrease somewhere leave all of out
+ *        untouched; a slot outside [0, n_experts) writes a +0 row and reads nothing of it).
+ *   ar   a_rows[r] (DEVICE int32 [m_rows]) if a_rows is given: an entry outside [0, a_n) is a row of zeros; else row r in
+ *        grouped and r / a_row_div in slot mode, which have to lie below a_n.
+ *   A scale byte of 255 makes exactly the outputs NaN whose sums hold it.
+ *   Requirements: N % 8 == 0, K % 32 == 0, 8 <= N, 32 <= K, both <= 2^20; m_rows <= 2^31 - 1; 1 <= n_experts <= 1024 in
+ *   grouped mode (0 allowed in slot mode); code rows 16-byte aligned; scale rows at multiples of 4 bytes and readable to the
+ *   next one (strides >= 4 * ceil(K/128); what pads a row is not used); out aligned to its type.  Slot mode:
+ *   m_rows * ceil(N / 16) < 2^24.  MOE_ERR_SHAPE, MOE_ERR_ALIGN otherwise.  m_rows == 0 launches nothing.
+ */
+int moe_mx4_grouped_gemm(const uint8_t* a_q, int64_t a_stride, const uint8_t* a_s, int64_t a_s_stride, int64_t a_n,
+                         const int32_t* a_rows, const uint8_t* w_q, int64_t w_stride_e, int64_t w_stride_n,
+                         const uint8_t* w_s, int64_t w_s_stride_e, int64_t w_s_stride_n, int64_t n_experts, int64_t N,
+                         int64_t K, int mode, const int32_t* expert_offsets, const int32_t* slot_ids, int64_t m_rows,
+                         int64_t a_row_div, void* out, int out_dt, int64_t out_stride, void* stream);
+
+/* The output tile (rows, columns) that moe_mx4_grouped_gemm's grouped mode takes; pure function, as moe_b16_grouped_tile. */
+int moe_mx4_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K, int32_t tile[2]);
+
+/*
+ * moe_mx4_grouped_gemm_act_quant  -- the gate/up GEMM with the gated activation and its MXFP4 requant in the epilogue
+ *   c1 is the fp32 result of moe_mx4_grouped_gemm with N = 2I (W13 rows 0..I-1 gate, I..2I-1 up), never stored; out_q, out_s
+ *   are moe_mx4_quant's of it with `act` (1..5) and `rule`.  The results equal moe_mx4_grouped_gemm with MOE_F32 output
+ *   followed by moe_mx4_quant, bit for bit.  Both modes; an inactive route gets codes 0 and scale bytes 0.
+ *   Requirements: I % 32 == 0; out_q and q_stride even; slot mode: m_rows * I / 32 < 2^22; the rest as
+ *   moe_mx4_grouped_gemm with N = 2I.
+ */
+int moe_mx4_grouped_gemm_act_quant(const uint8_t* a_q, int64_t a_stride, const uint8_t* a_s, int64_t a_s_stride, int64_t a_n,
+                                   const int32_t* a_rows, const uint8_t* w_q, int64_t w_stride_e, int64_t w_stride_n,
+                                   const uint8_t* w_s, int64_t w_s_stride_e, int64_t w_s_stride_n, int64_t n_experts,
+                                   int64_t I, int64_t K, int mode, const int32_t* expert_offsets, const int32_t* slot_ids,
+                                   int64_t m_rows, int64_t a_row_div, int act, int rule, uint8_t* out_q, int64_t q_stride,
+                                   uint8_t* out_s, int64_t s_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,7 @@ torch.float16.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -26,6 +27,8 @@ MOE_BF16, MOE_F32, MOE_F16, MOE_E4M3 = 0, 1, 2, 3
 MOE_ACT_IDENTITY, MOE_ACT_SILU_MUL, MOE_ACT_GELU_MUL, MOE_ACT_RELU_MUL, MOE_ACT_SIGMOID_MUL, MOE_ACT_MUL = 0, 1, 2, 3, 4, 5
 MOE_MODE_GROUPED, MOE_MODE_SLOT = 0, 1
 MOE_W_PACKED = -1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_MX_FLOOR, MOE_MX_CEIL = 0, 1
 
 EXPORTS = (
     "moe_abi_version", "moe_status_string", "moe_last_hip_error", "moe_gather_rows_scales", "moe_act_quant",
@@ -36,6 +39,8 @@ EXPORTS = (
     "moe_grouped_block_m", "moe_b16_grouped_gemm", "moe_b16_grouped_tile", "moe_b16_grouped_wgrad", "moe_b16_grouped_wgrad_workspace_size",
     "moe_b16_grouped_wgrad_plan",
     "moe_act_checkpoint", "moe_gated_act_backward", "moe_topk_reduce_backward", "moe_route_prep_backward",
+    "moe_router_workspace_size", "moe_router", "moe_router_backward", "moe_mx4_quant", "moe_mx4_dequant",
+    "moe_mx4_grouped_gemm", "moe_mx4_grouped_tile", "moe_mx4_grouped_gemm_act_quant",
 )
 
 _lib = None
@@ -97,6 +102,18 @@ def lib():
             "moe_topk_reduce_backward": ([P, I64, P, I32, I64, I64, P, P, P, I64, I64, I64, P, I64, P, P], I32),
             "moe_route_prep_backward": ([P, P, P, I64, I64, I64, P, I64, P], I32),
         }
+        F32 = ctypes.c_float
+        mx4_operands = [P, I64, P, I64, I64, P, P, I64, I64, P, I64, I64, I64, I64, I64, I32, P, P, I64, I64]
+        sig.update({
+            "moe_router_workspace_size": ([I64, I64], SZ),
+            "moe_router": ([P, I32, I64, I64, I64, I64, I32, P, I64, I64, I32, I32, F32, P, P, P, P, P, P, P, SZ, P], I32),
+            "moe_router_backward": ([P, I32, I64, P, P, P, P, I64, I64, I64, I64, I32, I32, F32, P, I64, P], I32),
+            "moe_mx4_quant": ([P, I32, I64, I64, I64, I32, I32, P, I64, P, I64, P], I32),
+            "moe_mx4_dequant": ([P, I64, P, I64, I64, I64, P, I32, I64, P], I32),
+            "moe_mx4_grouped_gemm": (mx4_operands + [P, I32, I64, P], I32),
+            "moe_mx4_grouped_tile": ([I64, I64, I64, I64, P], I32),
+            "moe_mx4_grouped_gemm_act_quant": (mx4_operands + [I32, I32, P, I64, P, I64, P], I32),
+        })
         for name, (args, res) in sig.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -544,3 +561,180 @@ def route_prep_backward(expert_ids, weights, dweights, dlogits, stream=None):
     assert dlogits.dtype is _F32 and rows == T and l_1 == 1, "dlogits: [T, E] float32"
     _call("moe_route_prep_backward", (expert_ids, weights, dweights, dlogits), (
         expert_ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), T, E, topk, dlogits.data_ptr(), l_r), stream)
+
+
+# ---------------------------------------------------------------------------
+# The router in its general form, and experts in MXFP4 on both sides
+
+RouterOut = collections.namedtuple("RouterOut", "expert_ids weights dst2src route_rows expert_offsets scores")
+
+
+def router_workspace_size(T, E) -> int:
+    """Bytes of workspace router needs for its maps (0: none)."""
+    return lib().moe_router_workspace_size(T, E)
+
+
+def router(logits, topk, *, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=2, renorm=True,
+           scale=1.0, maps=True, want_scores=False, out=None, workspace=None, stream=None):
+    """Routes logits [T, E] (bf16, fp16 or fp32; -inf masks an expert): RouterOut of expert_ids [T, topk] i32 (-1: no
+    route), weights [T, topk] f32, the route maps dst2src, route_rows [T*topk] and expert_offsets [E+1] i32 (None
+    unless maps), and scores [T, E] f32 (None unless want_scores).  out: such a tuple to write into, whose None entries
+    say what is not wanted; workspace: uint8 tensor of router_workspace_size bytes; both are allocated here when None."""
+    T, E = logits.shape
+    l_r, l_1 = logits.stride()
+    assert l_1 == 1 or E == 1, _UNIT
+    size = router_workspace_size(T, E)
+    if out is None or (workspace is None and size):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(logits.device)):
+            if out is None:
+                new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
+                out = (new((T, topk), _I32T), new((T, topk), _F32)) + (
+                    (new(T * topk, _I32T), new(T * topk, _I32T), new(E + 1, _I32T)) if maps else (None, None, None)) + (
+                    new((T, E), _F32) if want_scores else None,)
+            if workspace is None and size and out[4] is not None:
+                workspace = torch.empty(size, dtype=_U8, device=logits.device)
+    ids, w, d2s, rr, offs, scores = out
+    routes = (T, topk)
+    assert ids.dtype is _I32T and ids.shape == routes and ids.is_contiguous(), "expert_ids: [T, topk] int32"
+    assert w.dtype is _F32 and w.shape == routes and w.is_contiguous(), "weights: [T, topk] float32"
+    d_p = r_p = o_p = s_p = b_p = None
+    if offs is not None:
+        _i32(d2s, T * topk, "dst2src")
+        _i32(rr, T * topk, "route_rows")
+        _i32(offs, E + 1, "expert_offsets")
+        d_p, r_p, o_p = d2s.data_ptr(), rr.data_ptr(), offs.data_ptr()
+    else:
+        assert d2s is None and rr is None, "all three maps or none"
+    if scores is not None:
+        assert scores.dtype is _F32 and scores.shape == (T, E) and scores.is_contiguous(), "scores: [T, E] float32"
+        s_p = scores.data_ptr()
+    if bias is not None:
+        assert bias.dtype is _F32 and bias.shape == (E,) and bias.is_contiguous(), "bias: [E] float32"
+        b_p = bias.data_ptr()
+    if workspace is not None:
+        assert workspace.is_contiguous() and workspace.element_size() == 1, "workspace: contiguous bytes"
+    _call("moe_router", (logits, bias, ids, w, d2s, rr, offs, scores, workspace), (
+        logits.data_ptr(), _DT[logits.dtype], max(l_r, E) if T == 1 else l_r, T, E, topk, score, b_p, n_group, topk_group, group_top, 1 if renorm else 0, scale,
+        ids.data_ptr(), w.data_ptr(), s_p, d_p, r_p, o_p, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel()), stream)
+    return out if type(out) is RouterOut else RouterOut(ids, w, d2s, rr, offs, scores)
+
+
+def router_backward(logits, expert_ids, weights, dweights, dlogits, *, score=MOE_SCORE_SOFTMAX, renorm=True, scale=1.0,
+                    dscores=None, stream=None):
+    """Gradient of router's logits: dlogits [T, E] (logits' type) from dweights [T, topk] and, for an auxiliary loss,
+    dscores [T, E] f32 (a row expanded over the tokens is read as one row).  score, renorm, scale as in the forward."""
+    T, E = logits.shape
+    routes = expert_ids.shape
+    topk = routes[1]
+    l_r, l_1 = logits.stride()
+    d_r, d_1 = dlogits.stride()
+    _i32(expert_ids, T * topk, "expert_ids")
+    assert weights.dtype is _F32 and weights.is_contiguous() and weights.shape == routes, "weights do not match"
+    assert dweights.dtype is _F32 and dweights.is_contiguous() and dweights.shape == routes, "dweights do not match"
+    assert dlogits.dtype is logits.dtype and dlogits.shape == (T, E), "dlogits do not match logits"
+    assert (l_1 == 1 and d_1 == 1) or E == 1, _UNIT
+    s_p, s_r = None, 0
+    if dscores is not None:
+        s_r, s_1 = dscores.stride()
+        assert dscores.dtype is _F32 and dscores.shape == (T, E) and (s_1 == 1 or E == 1), "dscores: [T, E] float32"
+        s_p = dscores.data_ptr()
+    if T == 1:
+        l_r, d_r, s_r = max(l_r, E), max(d_r, E), 0
+    _call("moe_router_backward", (logits, expert_ids, weights, dweights, dscores, dlogits), (
+        logits.data_ptr(), _DT[logits.dtype], l_r, expert_ids.data_ptr(), weights.data_ptr(), dweights.data_ptr(), s_p, s_r,
+        T, E, topk, score, 1 if renorm else 0, scale, dlogits.data_ptr(), d_r), stream)
+
+
+def mx4_quant(x, out_q, out_s, act=MOE_ACT_IDENTITY, rule=MOE_MX_FLOOR, stream=None):
+    """Rows x to MXFP4: codes out_q [rows, n/2] and scale bytes out_s [rows, ceil(n/32)] (uint8).  With a gated act, x =
+    [gate | up] of width 2n and act(gate) * up is quantised.  rule: MOE_MX_FLOOR (OCP MX) or MOE_MX_CEIL."""
+    rows, width = x.shape
+    n = width if act == MOE_ACT_IDENTITY else width // 2
+    x_r, x_1 = x.stride()
+    q_r, q_1 = out_q.stride()
+    s_r, s_1 = out_s.stride()
+    assert width == (n if act == MOE_ACT_IDENTITY else 2 * n) and n % 2 == 0, "an even width, gate and up of one width"
+    assert out_q.dtype is _U8 and out_s.dtype is _U8, "codes and scales are uint8"
+    assert out_q.shape == (rows, n // 2) and out_s.shape == (rows, (n + 31) // 32), "outputs do not match"
+    assert x_1 == 1 and q_1 == 1 and (s_1 == 1 or n <= 32), _UNIT
+    _call("moe_mx4_quant", (x, out_q, out_s), (
+        x.data_ptr(), _DT[x.dtype], x_r, rows, n, act, rule, out_q.data_ptr(), q_r, out_s.data_ptr(), s_r), stream)
+
+
+def mx4_dequant(q, s, out, stream=None):
+    """Values of MXFP4 rows: out [rows, n] (bf16, fp16 or fp32) from codes q [rows, n/2] and scale bytes s."""
+    rows, n = out.shape
+    o_r, o_1 = out.stride()
+    q_r, q_1 = q.stride()
+    s_r, s_1 = s.stride()
+    assert q.dtype is _U8 and s.dtype is _U8, "codes and scales are uint8"
+    assert n % 2 == 0 and q.shape == (rows, n // 2) and s.shape == (rows, (n + 31) // 32), "operands do not match"
+    assert o_1 == 1 and q_1 == 1 and (s_1 == 1 or n <= 32), _UNIT
+    _call("moe_mx4_dequant", (q, s, out), (q.data_ptr(), q_r, s.data_ptr(), s_r, rows, n, out.data_ptr(), _DT[out.dtype], o_r),
+          stream)
+
+
+def _mx4_operands(a_q, a_s, w_q, w_s, mode, expert_offsets, slot_ids, a_rows, rows, a_row_div, N):
+    """The operand arguments that both MXFP4 products take, checked; N: output columns (the bank holds N or 2N rows)."""
+    E, _, k2 = w_q.shape
+    w_e, w_r, w_1 = w_q.stride()
+    v_e, v_r, v_1 = w_s.stride()
+    a_n, a_cols = a_q.shape
+    a_r, a_1 = a_q.stride()
+    s_r, s_1 = a_s.stride()
+    groups = k2 // 16
+    assert a_q.dtype is _U8 and a_s.dtype is _U8 and w_q.dtype is _U8 and w_s.dtype is _U8, "codes and scales are uint8"
+    assert k2 % 16 == 0, "whole groups of 32 expected"
+    assert a_cols == k2 and a_s.shape == (a_n, groups) and w_s.shape == (E, w_q.shape[1], groups), "operands do not match"
+    assert w_1 == 1 and a_1 == 1 and ((s_1 == 1 and v_1 == 1) or groups == 1), _UNIT
+    if groups % 4:                      # the kernels read a scale row to its next multiple of four bytes
+        for t in (a_s, w_s):
+            last = t.storage_offset() + sum((n - 1) * st for n, st in zip(t.shape[:-1], t.stride()[:-1])) + (groups + 3) // 4 * 4
+            assert not t.numel() or last <= t.untyped_storage().nbytes(), "scale rows padded to a multiple of four bytes expected"
+    if a_rows is not None:
+        _i32(a_rows, rows, "a_rows")
+    if mode == MOE_MODE_SLOT:
+        _i32(slot_ids, rows, "slot_ids")
+    else:
+        _i32(expert_offsets, E + 1, "expert_offsets")
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return (a_q.data_ptr(), a_r, a_s.data_ptr(), s_r, a_n, p(a_rows), w_q.data_ptr(), w_e, w_r, w_s.data_ptr(), v_e, v_r, E, N,
+            2 * k2, mode, p(expert_offsets), p(slot_ids), rows, a_row_div)
+
+
+def mx4_grouped_gemm(a_q, a_s, w_q, w_s, out, *, mode, expert_offsets=None, slot_ids=None, a_rows=None, m_rows=None,
+                     a_row_div=1, stream=None):
+    """MXFP4 grouped GEMM out[r] = a[ar] @ w[e].T: a_q [rows, K/2] codes, a_s [rows, K/32] scale bytes, w_q [E, N, K/2],
+    w_s [E, N, K/32] (uint8), out [rows, N] bf16, fp16 or fp32; rows by expert_offsets [E+1] (grouped) or slot_ids [m_rows]
+    (slot mode).  ar: a_rows[r] (i32 [m_rows], outside a: zeros) when given, else r (grouped) or r // a_row_div (slot)."""
+    o_rows, N = out.shape
+    o_r, o_1 = out.stride()
+    rows = o_rows if m_rows is None else m_rows
+    assert w_q.shape[1] == N and o_1 == 1 and 0 <= rows <= o_rows, "out does not match"
+    args = _mx4_operands(a_q, a_s, w_q, w_s, mode, expert_offsets, slot_ids, a_rows, rows, a_row_div, N)
+    _call("moe_mx4_grouped_gemm", (a_q, a_s, w_q, w_s, out, expert_offsets, slot_ids, a_rows),
+          args + (out.data_ptr(), _DT[out.dtype], o_r), stream)
+
+
+def mx4_grouped_tile(m_rows, n_experts, N, K):
+    """(rows, columns) of the output tile that mx4_grouped_gemm's grouped mode takes."""
+    t = (ctypes.c_int32 * 2)()
+    _check("moe_mx4_grouped_tile", lib().moe_mx4_grouped_tile(m_rows, n_experts, N, K, t))
+    return t[0], t[1]
+
+
+def mx4_grouped_gemm_act_quant(a_q, a_s, w13_q, w13_s, out_q, out_s, *, mode, expert_offsets=None, slot_ids=None,
+                               a_rows=None, m_rows=None, a_row_div=1, act=MOE_ACT_SILU_MUL, rule=MOE_MX_FLOOR, stream=None):
+    """Gate/up mx4_grouped_gemm with act(gate)*up and its MXFP4 requant in the epilogue: w13_q [E, 2I, K/2] (gate rows, then
+    up rows), out_q [rows, I/2] codes and out_s [rows, I/32] scale bytes; the rest as mx4_grouped_gemm."""
+    o_rows, i2 = out_q.shape
+    q_r, q_1 = out_q.stride()
+    s_r, s_1 = out_s.stride()
+    rows = o_rows if m_rows is None else m_rows
+    assert out_q.dtype is _U8 and out_s.dtype is _U8, "codes and scales are uint8"
+    assert i2 % 16 == 0 and out_s.shape == (o_rows, i2 // 16) and w13_q.shape[1] == 4 * i2 and 0 <= rows <= o_rows, "outputs do not match"
+    assert q_1 == 1 and (s_1 == 1 or i2 == 16), _UNIT
+    args = _mx4_operands(a_q, a_s, w13_q, w13_s, mode, expert_offsets, slot_ids, a_rows, rows, a_row_div, 2 * i2)
+    _call("moe_mx4_grouped_gemm_act_quant", (a_q, a_s, w13_q, w13_s, out_q, out_s, expert_offsets, slot_ids, a_rows),
+          args + (act, rule, out_q.data_ptr(), q_r, out_s.data_ptr(), s_r), stream)

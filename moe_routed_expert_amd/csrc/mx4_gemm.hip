@@ -1,0 +1,550 @@
+// Grouped products with MXFP4 on both sides, and the gate/up product with the gated activation and its MXFP4 requant in
+// the epilogue.  Rows are sorted by expert; out[r, n] = sum_k A[r, k] W[e(r)][n, k].  Slot mode is the decode form: every
+// row streams its own expert.
+//
+// MI355X design of the grouped mode (the tile engine is mx4_tile.h): persistent workgroups walk the tiles in panels, as
+// b16_gemm.hip does, and the load pipeline runs on across tiles.  A rows may be named by a map, so the tokens' codes are
+// read in place and no gathered copy is written.
+// The fused form's tile holds 32 gate columns and the matching 32 up columns in every wave (MQ = 4 sub-tiles: two of
+// gate, two of up), so a lane forms act(gate) * up from its own accumulators, the four lanes of a row hold a whole scale
+// group of 32, and its maximum is two lane moves.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "mx4_tile.h"
+
+namespace moe {
+namespace mx4 {
+namespace {
+
+using b16::kMaxExperts;
+using b16::kMaxWidth;
+using b16::kPanel;
+using b16::kXcds;
+
+constexpr int kStagger = 5;                   // an expert's tiles walk k in rotation from step kStagger * e (b16_gemm.hip)
+
+struct GemmArgs {
+    const char* a;
+    int64_t a_stride;                         // bytes, as all strides of codes and scales
+    const char* a_s;
+    int64_t a_s_stride;
+    int64_t a_n;                              // rows of a, for the map's bounds
+    const int32_t* a_rows;
+    const char* w;
+    int64_t w_stride_e, w_stride_n;
+    const char* w_s;
+    int64_t w_s_stride_e, w_s_stride_n;
+    int n_experts;
+    int64_t N, K;                             // fused: N = I, the act columns
+    const int32_t* offsets;
+    int m_rows;
+    int n_tiles;
+    void* out;                                // fused: codes
+    int out_dt;
+    int64_t out_stride;                       // elements (fused: bytes)
+    uint8_t* s;                               // fused: scale bytes
+    int64_t s_stride;
+    int act, ceil;
+};
+
+__device__ __forceinline__ uint32_t max_lanes16_32(uint32_t v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = a[0] > a[1] ? a[0] : a[1];
+    const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return b[0] > b[1] ? b[0] : b[1];
+}
+
+// The fused epilogue of a wave: rows row0 + 16m + lane % 16 (below `rows`), act columns col0 .. col0 + 31 (below `cols`).
+template <int ACT, int MP>
+__device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP][4], int64_t row0, int rows, int64_t col0, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < MP; m++) {
+        if (m * 16 >= rows) break;                                          // wave-uniform
+        float h[8];
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) h[4 * n + i] = gated<ACT>(acc[m][n][i], acc[m][n + 2][i]);
+        const uint32_t byte = scale_byte(max_lanes16_32(max_bits8(h)), g.ceil != 0);
+        const uint32_t codes = encode8(h, byte);
+        if (m * 16 + r < rows) {
+            const int64_t row = row0 + m * 16 + r;
+            uint8_t* out = (uint8_t*)g.out + row * g.out_stride + col0 / 2 + 2 * q;
+            *reinterpret_cast<uint16_t*>(out) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t*>(out + 8) = (uint16_t)(codes >> 16);
+            if (q == 0) g.s[row * g.s_stride + col0 / kGroup] = (uint8_t)byte;
+        }
+    }
+}
+
+template <int MP>
+__device__ __forceinline__ void store_act_of(const GemmArgs& g, const v4f (&acc)[MP][4], int64_t row0, int rows, int64_t col0, int lane) {
+    switch (g.act) {
+        case 1: return store_act<1>(g, acc, row0, rows, col0, lane);
+        case 2: return store_act<2>(g, acc, row0, rows, col0, lane);
+        case 3: return store_act<3>(g, acc, row0, rows, col0, lane);
+        case 4: return store_act<4>(g, acc, row0, rows, col0, lane);
+        default: return store_act<5>(g, acc, row0, rows, col0, lane);
+    }
+}
+
+template <class C, bool FUSED>
+__global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(const GemmArgs g) {
+    constexpr int S = C::S, LPS = C::LOADS;
+    constexpr int COLS = FUSED ? C::BQ / 2 : C::BQ;    // output columns of a tile
+    static_assert(C::MQ == 4, "a wave holds 32 gate and 32 up columns, or 64 columns");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::STAGE];
+    __shared__ int first_tile[kMaxExperts + 1];        // M tiles before expert e
+    __shared__ uint32_t wave_sum[2 * C::NW];
+    __shared__ int decreases;
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int E = g.n_experts;
+    auto clamped = [&](int e) { return min(max(g.offsets[e], 0), g.m_rows); };
+
+    {                                                  // the tile table: EPT consecutive experts per thread
+        constexpr int EPT = kMaxExperts / C::THREADS;
+        uint32_t count[EPT], tiles = 0, down = 0;
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            count[i] = 0;
+            if (e < E) {
+                const int lo = clamped(e), to = clamped(e + 1);
+                count[i] = (uint32_t)pieces(max(to, lo) - lo, C::BP);
+                down += to < lo;
+            }
+            tiles += count[i];
+        }
+        uint32_t w = tiles, d = down;
+        b16::block_exclusive_scan2<C::NW>(w, d, wave_sum, lane, wave);
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            if (e < E) first_tile[e] = (int)w;
+            w += count[i];
+            if (e == E - 1) first_tile[E] = (int)w;
+        }
+        if (tid == C::THREADS - 1) decreases = (int)(d + down);
+        __syncthreads();
+    }
+    // Experts that overlap may have more tiles than the host counted on, and share rows: nothing is computed.
+    if (__builtin_amdgcn_readfirstlane(decreases) != 0) return;
+    const int m_tiles = __builtin_amdgcn_readfirstlane(first_tile[E]);
+    const int tiles = m_tiles * g.n_tiles;
+    const int G = gridDim.x;
+    const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
+
+    struct Tile {
+        int expert, row0, rows, n0;
+    };
+    auto locate = [&](int t) {
+        const int per = kPanel * g.n_tiles;
+        const int panel = t / per, r = t - panel * per;
+        const int height = min(kPanel, m_tiles - panel * kPanel);
+        const int nt = r / height, mt = panel * kPanel + r - nt * height;
+        const int e = last_at_most([&](int i) { return first_tile[i]; }, E, mt, lane);
+        Tile ti;
+        ti.expert = e;
+        const int from = __builtin_amdgcn_readfirstlane(clamped(e)), end = __builtin_amdgcn_readfirstlane(clamped(e + 1));
+        ti.row0 = from + (mt - __builtin_amdgcn_readfirstlane(first_tile[e])) * C::BP;
+        ti.rows = min(end - ti.row0, C::BP);
+        ti.n0 = nt * COLS;
+        return ti;
+    };
+
+    const uint32_t lds = lds_offset(ring);
+    const int steps = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup);
+
+    // Producer, as in b16_gemm.hip: past the last tile it goes on with zeros into stages that nobody reads, so the loads in
+    // flight can be counted the same way to the end.
+    CodeRows<C::P_LOADS, C::NW> p;
+    CodeRows<C::Q_LOADS, C::NW> q;
+    const char* sc[C::S_LOADS];                        // this lane's scale words: row and half
+    int prod_t = start, prod_left = 0, prod_kt = 0, prod_stage = 0;
+    int64_t prod_k = 0;                                // elements: K, or 0 past the last tile
+    auto aim = [&]() {
+        prod_k = prod_t < tiles ? g.K : 0;
+        if (prod_t >= tiles) return;
+        const Tile ti = locate(prod_t);
+        const int l = fresh(lane);
+        prod_left = steps;
+        prod_kt = ti.expert * kStagger % steps;
+        // A row of tile row r: rows past the tile's repeat the last one (their results are dropped), rows whose map entry
+        // is no row of a are zeros.
+        auto a_row = [&](int r) -> int64_t {
+            const int64_t at = ti.row0 + min(r, ti.rows - 1);
+            if (!g.a_rows) return at;
+            const int64_t m = g.a_rows[at];
+            return m >= 0 && m < g.a_n ? m : -1;
+        };
+        // W row of tile row r: a fused tile's wave has 32 gate rows and then the 32 up rows of the same columns.  Columns past
+        // the last repeat it.
+        auto w_row = [&](int r) -> int64_t {
+            if (!FUSED) return min(ti.n0 + r, (int)g.N - 1);
+            const int c = min(ti.n0 + (r >> 6) * 32 + (r & 31), (int)g.N - 1);
+            return c + (r & 32 ? g.N : 0);
+        };
+        p.set([&](int r) -> const char* {
+            const int64_t m = a_row(r);
+            return m < 0 ? nullptr : g.a + m * g.a_stride;
+        }, wave, l);
+        const char* w = g.w + ti.expert * g.w_stride_e;
+        q.set([&](int r) -> const char* { return w + w_row(r) * g.w_stride_n; }, wave, l);
+        const char* w_s = g.w_s + ti.expert * g.w_s_stride_e;
+#pragma unroll
+        for (int j = 0; j < C::S_LOADS; j++) {
+            const int r = (j * C::NW + wave) % C::S_GROUPS * 32 + l / 2;
+            const char* at;
+            if (r < C::BP) {
+                const int64_t m = a_row(r);
+                at = m < 0 ? nullptr : g.a_s + m * g.a_s_stride;
+            } else {
+                at = w_s + w_row(r - C::BP) * g.w_s_stride_n;
+            }
+            sc[j] = at ? at + (l & 1) * 4 : nullptr;
+        }
+    };
+    auto part = [&](int j) {
+        const uint32_t dst = lds + prod_stage * C::STAGE;
+        if (j < C::P_LOADS) {
+            p.issue(j, dst, prod_kt, prod_k / 2, wave);
+        } else if (j < C::P_LOADS + C::Q_LOADS) {
+            q.issue(j - C::P_LOADS, dst + C::BP * kRowBytes, prod_kt, prod_k / 2, wave);
+        } else {
+            const int i = j - C::P_LOADS - C::Q_LOADS;
+            const int64_t at = (int64_t)prod_kt * kRowScales;
+            const bool in = (lane & 1) * 4 < prod_k / kGroup - at && sc[i] != nullptr;
+            dma4(in ? sc[i] + at : (const char*)&b16::kZeroPiece, dst + C::CODES + (i * C::NW + wave) % C::S_GROUPS * 256);
+        }
+        if (j == LPS - 1) {
+            prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
+            prod_kt = prod_kt + 1 == steps ? 0 : prod_kt + 1;
+            if (--prod_left <= 0) {
+                prod_t += G;
+                aim();
+            }
+        }
+    };
+    auto produce = [&]() {
+#pragma unroll
+        for (int j = 0; j < LPS; j++) part(j);
+    };
+    if (start >= tiles) return;
+    aim();
+#pragma unroll 1
+    for (int i = 0; i < S - 1; i++) produce();
+
+    CodeFrag fp, fq;
+    ScaleFrag sp, sq;
+    const int wp = wave / C::WQ, wq = wave % C::WQ;
+    fp.set(wp * C::MP, lane);
+    fq.set(wq * C::MQ, lane);
+    sp.set(wp * C::MP, lane);
+    sq.set(wq * C::MQ, lane);
+
+    int stage = 0;
+#pragma unroll 1
+    for (int t = start; t < tiles; t += G) {
+        const Tile ti = locate(t);
+        const int rows = ti.rows - wp * C::MP * 16;    // of this wave
+        v4f acc[C::MP][C::MQ];
+#pragma unroll
+        for (int m = 0; m < C::MP; m++)
+#pragma unroll
+            for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        int kt = ti.expert * kStagger % steps;
+#pragma unroll 1
+        for (int i = 0; i < steps; i++) {
+            const uint32_t at = lds + stage * C::STAGE;
+            stage = stage + 1 == S ? 0 : stage + 1;
+            arrive<S, LPS>();
+            produce();                                 // into the stage that the step before this one read
+            step_plain<C>(acc, fp, fq, sp, sq, at, scale_mask(blocks - kt * kRowScales, lane));
+            kt = kt + 1 == steps ? 0 : kt + 1;
+        }
+        const int64_t c0 = ti.n0 + wq * (COLS / C::WQ);
+        const int cols = (int)min(g.N - c0, (int64_t)(COLS / C::WQ));
+        const int64_t r0 = ti.row0 + wp * C::MP * 16;
+        if (rows > 0 && cols > 0) {
+            if constexpr (FUSED) store_act_of(g, acc, r0, rows, c0, fresh(lane));
+            else b16::store_wave_dt(g.out, g.out_dt, false, r0 * g.out_stride + c0, g.out_stride, rows, cols, acc, fresh(lane));
+        }
+    }
+    wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
+}
+
+template <class C, bool FUSED>
+int resident_blocks() {
+    static std::atomic<int> cached[64];   // concurrent first calls may both fill it, with the same value
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+    int c = cached[dev].load(std::memory_order_relaxed);
+    if (c == 0) {
+        int per_cu = 0, cus = 0;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, mx4_gemm_kernel<C, FUSED>, C::THREADS, 0) != hipSuccess ||
+            hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+            return 0;
+        c = per_cu * cus;
+        if (c > 0) cached[dev].store(c, std::memory_order_relaxed);
+    }
+    return c;
+}
+
+using Tile256 = Cfg<256, 256, 2, 4, 2, 1>;
+using Tile128 = Cfg<128, 256, 2, 4, 3, 1>;
+using Tile64 = Cfg<64, 256, 2, 4, 3, 1>;
+using Tile64x64 = Cfg<64, 64, 4, 1, 3, 2>;
+using Tile32x64 = Cfg<32, 64, 2, 1, 4, 2>;
+
+template <class C, bool FUSED>
+int launch_cfg(hipStream_t st, GemmArgs g) {
+    const int64_t n_tiles = ceil_div(g.N, FUSED ? C::BQ / 2 : C::BQ);
+    const int64_t most = (g.m_rows / C::BP + std::min<int64_t>(g.n_experts, g.m_rows)) * n_tiles;
+    if (most > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
+    int wgs = resident_blocks<C, FUSED>() / kXcds * kXcds;
+    if (wgs < kXcds) return MOE_ERR_HIP;
+    wgs = (int)std::min<int64_t>(wgs, ceil_div(most, kXcds) * kXcds);
+    g.n_tiles = (int)n_tiles;
+    hipLaunchKernelGGL((mx4_gemm_kernel<C, FUSED>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
+    return launch_status();
+}
+
+struct TileCost {
+    int bp, bq, slots;
+    double step;
+};
+constexpr TileCost kCosts[] = {{32, 64, 512, 0.5}, {64, 64, 512, 0.50}, {64, 256, 256, 0.68}, {128, 256, 256, 0.88}, {256, 256, 256, 1.45}};
+
+int pick_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
+    const double E = (double)n_experts, R = (double)m_rows, steps = (double)ceil_div(K, kStepK);
+    const double used = n_experts == 1 ? 1.0 : std::min(R, E * (1.0 - std::pow(1.0 - 1.0 / E, R)));   // experts with rows
+    const double r = R / used;
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < 5; i++) {
+        const TileCost& c = kCosts[i];
+        const double per = n_experts == 1 ? std::ceil(r / c.bp) : (r <= 0.5 * c.bp ? 1.0 : r / c.bp + 0.5);   // M tiles of one
+        const double tiles = used * per * (double)ceil_div(N, c.bq) * (n_experts == 1 ? 1.0 : 1.05);
+        const double work = std::ceil(tiles / c.slots - 1e-9) * (steps * c.step + 4.0);
+        const double bytes = (used * (double)N * (double)K * std::ceil(per / kPanel) + R * (double)K) * 0.53125 + 2.0 * R * (double)N;
+        const double t = std::max(work, bytes / 5.7e6) + 0.1 * work;
+        if (i == 0 || t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    return best;
+}
+
+// N: rows of an expert's bank (fused: 2I).
+template <bool FUSED>
+int grouped_launch(hipStream_t st, const GemmArgs& g) {
+    switch (pick_tile(g.m_rows, g.n_experts, FUSED ? 2 * g.N : g.N, g.K)) {
+        case 0: return launch_cfg<Tile32x64, FUSED>(st, g);
+        case 1: return launch_cfg<Tile64x64, FUSED>(st, g);
+        case 2: return launch_cfg<Tile64, FUSED>(st, g);
+        case 3: return launch_cfg<Tile128, FUSED>(st, g);
+        default: return launch_cfg<Tile256, FUSED>(st, g);
+    }
+}
+
+// ------------------------------------------------------------------ slot mode
+// A group of KS waves holds 16 columns of one row, each wave a part of k; W is the MFMA's row operand and the row of A
+// stands in all 16 columns of the other.  The sums of the waves meet in LDS in order.
+template <int KS, bool FUSED>
+__global__ void __launch_bounds__(64 * KS * (FUSED ? 4 : 1))
+mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_row_div, int col_groups) {
+    constexpr int SUBS = FUSED ? 4 : 1;                // 16-column sub-tiles of a workgroup (fused: two of gate, two of up)
+    __shared__ float part[SUBS][KS][16];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int sub = wave / KS, ks = wave % KS;
+    const int l16 = lane & 15, quad = lane >> 4;
+    const int64_t r = blockIdx.x / (unsigned)col_groups;
+    const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)col_groups) * (FUSED ? 32 : 16);
+    const int slot = slots[r];
+    const int64_t ar = g.a_rows ? (int64_t)g.a_rows[r] : r / a_row_div;
+    const bool live = slot >= 0 && slot < g.n_experts && ar >= 0 && ar < g.a_n;
+    if (live) {
+        const int64_t col = FUSED ? n0 + (sub & 1) * 16 : n0;
+        const int64_t row = min(col + l16, g.N - 1) + (FUSED && sub >= 2 ? g.N : 0);
+        const char* w = g.w + slot * g.w_stride_e + row * g.w_stride_n;
+        const char* ws = g.w_s + slot * g.w_s_stride_e + row * g.w_s_stride_n;
+        const char* a = g.a + ar * g.a_stride;
+        const char* as = g.a_s + ar * g.a_s_stride;
+        const int windows = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup);
+        const int per = (windows + KS - 1) / KS;
+        v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = ks * per; t < min((ks + 1) * per, windows); t++) {
+            // this lane's blocks 8t + 2 quad and the next; past the end the last block is read and counted as zero
+            const int b = 8 * t + 2 * quad;
+            const int b0 = min(b, blocks - 1), b1 = min(b + 1, blocks - 1);
+            v4i w0 = *reinterpret_cast<const v4i*>(w + b0 * 16), w1 = *reinterpret_cast<const v4i*>(w + b1 * 16);
+            v4i x0 = *reinterpret_cast<const v4i*>(a + b0 * 16), x1 = *reinterpret_cast<const v4i*>(a + b1 * 16);
+            uint32_t s0 = (uint8_t)ws[b0], s1 = (uint8_t)ws[b1], u0 = (uint8_t)as[b0], u1 = (uint8_t)as[b1];
+            const v4i zero = {0, 0, 0, 0};
+            if (b >= blocks) { w0 = zero; x0 = zero; s0 = 0; u0 = 0; }
+            if (b + 1 >= blocks) { w1 = zero; x1 = zero; s1 = 0; u1 = 0; }
+            acc = mfma<0>(w0, s0, x0, u0, acc);
+            acc = mfma<0>(w1, s1, x1, u1, acc);
+        }
+        if (l16 == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) part[sub][ks][4 * quad + i] = acc[i];
+        }
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    auto total = [&](int s, int c) {
+        float v = live ? part[s][0][c] : 0.0f;
+#pragma unroll
+        for (int k = 1; k < KS; k++) v += live ? part[s][k][c] : 0.0f;
+        return v;
+    };
+    if constexpr (FUSED) {
+        // lanes 0..3 hold eight columns each
+        float h[8] = {};
+        if (lane < 4) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int c = 8 * lane + i;
+                const float gt = total(c / 16, c % 16), up = total(2 + c / 16, c % 16);
+                switch (g.act) {
+                    case 1: h[i] = gated<1>(gt, up); break;
+                    case 2: h[i] = gated<2>(gt, up); break;
+                    case 3: h[i] = gated<3>(gt, up); break;
+                    case 4: h[i] = gated<4>(gt, up); break;
+                    default: h[i] = gated<5>(gt, up); break;
+                }
+            }
+        }
+        uint32_t top = max_bits8(h);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 1, kWave));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 2, kWave));
+        const uint32_t byte = live ? scale_byte(top, g.ceil != 0) : 0u;
+        const uint32_t codes = live ? encode8(h, byte) : 0u;
+        if (lane < 4) {
+            uint8_t* out = (uint8_t*)g.out + r * g.out_stride + n0 / 2 + 4 * lane;
+            *reinterpret_cast<uint16_t*>(out) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t*>(out + 2) = (uint16_t)(codes >> 16);
+            if (lane == 0) g.s[r * g.s_stride + n0 / kGroup] = (uint8_t)byte;
+        }
+    } else if (lane < 16 && n0 + lane < g.N) {
+        const float v = total(0, lane);
+        const int64_t o = r * g.out_stride + n0 + lane;
+        if (g.out_dt == MOE_F32) store_from_f32<kF32>(g.out, o, v);
+        else if (g.out_dt == MOE_BF16) store_from_f32<kBF16>(g.out, o, v);
+        else store_from_f32<kF16>(g.out, o, v);
+    }
+}
+
+template <int KS, bool FUSED>
+int slot_launch_ks(hipStream_t st, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
+    constexpr int THREADS = 64 * KS * (FUSED ? 4 : 1);
+    const int64_t groups = ceil_div(g.N, FUSED ? 32 : 16);
+    if (groups * g.m_rows >= (int64_t)1 << (FUSED ? 22 : 24)) return MOE_ERR_SHAPE;   // a grid's threads fit 32 bits, whatever KS
+    hipLaunchKernelGGL((mx4_slot_kernel<KS, FUSED>), dim3((unsigned)(groups * g.m_rows)), dim3(THREADS), 0, st, g, slots, a_row_div,
+                       (int)groups);
+    return launch_status();
+}
+
+// The parts of k go by K alone, so that the fused form's sums are those of the plain one.
+template <bool FUSED>
+int slot_launch(hipStream_t st, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
+    return g.K > 2 * kStepK ? slot_launch_ks<4, FUSED>(st, g, slots, a_row_div) : slot_launch_ks<1, FUSED>(st, g, slots, a_row_div);
+}
+
+// Checks that both products share; MOE_OK when the call may go on.  bank_rows: N, or 2I.
+int check_operands(const GemmArgs& g, int64_t n_experts, int64_t m_rows, int64_t bank_rows, int mode, const int32_t* slot_ids,
+                   int64_t a_row_div) {
+    if (n_experts > 0) {
+        if (!g.a || !g.a_s || !g.w || !g.w_s) return MOE_ERR_NULL;
+        const int64_t codes = g.K / 2, scales = ceil_div(g.K, 128) * 4;
+        if (g.a_n < 1 || g.a_stride < codes || g.w_stride_n < codes || g.a_s_stride < scales || g.w_s_stride_n < scales) return MOE_ERR_SHAPE;
+        if (n_experts > 1 && (g.w_stride_e / g.w_stride_n < bank_rows || g.w_s_stride_e / g.w_s_stride_n < bank_rows)) return MOE_ERR_SHAPE;
+        if (!aligned16(g.a) || !aligned16(g.w) || g.a_stride % 16 || g.w_stride_n % 16 || g.w_stride_e % 16) return MOE_ERR_ALIGN;
+        if (reinterpret_cast<uintptr_t>(g.a_s) % 4 || reinterpret_cast<uintptr_t>(g.w_s) % 4 || g.a_s_stride % 4 || g.w_s_stride_n % 4 ||
+            g.w_s_stride_e % 4)
+            return MOE_ERR_ALIGN;
+    }
+    if (mode == MOE_MODE_SLOT) {
+        if (!slot_ids) return MOE_ERR_NULL;
+        if (a_row_div < 1) return MOE_ERR_SHAPE;
+        return n_experts > 0 && !g.a_rows && ceil_div(m_rows, a_row_div) > g.a_n ? MOE_ERR_SHAPE : MOE_OK;
+    }
+    if (n_experts < 1 || n_experts > kMaxExperts) return MOE_ERR_SHAPE;
+    if (!g.offsets) return MOE_ERR_NULL;
+    return !g.a_rows && m_rows > g.a_n ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+bool widths_ok(int64_t N, int64_t K, int64_t of) {
+    return N >= of && N <= kMaxWidth && N % of == 0 && K >= kGroup && K <= kMaxWidth && K % kGroup == 0;
+}
+
+}  // namespace
+}  // namespace mx4
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_mx4_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K, int32_t tile[2]) {
+    if (!tile) return MOE_ERR_NULL;
+    if (m_rows < 1 || m_rows > 0x7FFFFFFF || n_experts < 1 || n_experts > mx4::kMaxExperts || !mx4::widths_ok(N, K, 8)) return MOE_ERR_SHAPE;
+    const mx4::TileCost& c = mx4::kCosts[mx4::pick_tile(m_rows, n_experts, N, K)];
+    tile[0] = c.bp;
+    tile[1] = c.bq;
+    return MOE_OK;
+}
+
+extern "C" int moe_mx4_grouped_gemm(const uint8_t* a_q, int64_t a_stride, const uint8_t* a_s, int64_t a_s_stride, int64_t a_n,
+                                    const int32_t* a_rows, const uint8_t* w_q, int64_t w_stride_e, int64_t w_stride_n,
+                                    const uint8_t* w_s, int64_t w_s_stride_e, int64_t w_s_stride_n, int64_t n_experts, int64_t N,
+                                    int64_t K, int mode, const int32_t* expert_offsets, const int32_t* slot_ids, int64_t m_rows,
+                                    int64_t a_row_div, void* out, int out_dt, int64_t out_stride, void* stream) {
+    if (mode != MOE_MODE_GROUPED && mode != MOE_MODE_SLOT) return MOE_ERR_SHAPE;
+    if (!dtype_ok(out_dt)) return MOE_ERR_DTYPE;
+    if (m_rows < 0 || m_rows > 0x7FFFFFFF || n_experts < 0 || n_experts > 0x7FFFFFFF || !mx4::widths_ok(N, K, 8)) return MOE_ERR_SHAPE;
+    if (m_rows == 0) return MOE_OK;
+    if (!out) return MOE_ERR_NULL;
+    if (out_stride < N) return MOE_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(out) % (out_dt == MOE_F32 ? 4 : 2)) return MOE_ERR_ALIGN;
+    mx4::GemmArgs g{};
+    g.a = (const char*)a_q; g.a_stride = a_stride; g.a_s = (const char*)a_s; g.a_s_stride = a_s_stride; g.a_n = a_n; g.a_rows = a_rows;
+    g.w = (const char*)w_q; g.w_stride_e = w_stride_e; g.w_stride_n = w_stride_n;
+    g.w_s = (const char*)w_s; g.w_s_stride_e = w_s_stride_e; g.w_s_stride_n = w_s_stride_n;
+    g.n_experts = (int)n_experts; g.N = N; g.K = K; g.offsets = expert_offsets; g.m_rows = (int)m_rows;
+    g.out = out; g.out_dt = out_dt; g.out_stride = out_stride;
+    const int st = mx4::check_operands(g, n_experts, m_rows, N, mode, slot_ids, a_row_div);
+    if (st != MOE_OK) return st;
+    if (mode == MOE_MODE_SLOT) return mx4::slot_launch<false>(as_stream(stream), g, slot_ids, a_row_div);
+    return mx4::grouped_launch<false>(as_stream(stream), g);
+}
+
+extern "C" int moe_mx4_grouped_gemm_act_quant(const uint8_t* a_q, int64_t a_stride, const uint8_t* a_s, int64_t a_s_stride,
+                                              int64_t a_n, const int32_t* a_rows, const uint8_t* w_q, int64_t w_stride_e,
+                                              int64_t w_stride_n, const uint8_t* w_s, int64_t w_s_stride_e, int64_t w_s_stride_n,
+                                              int64_t n_experts, int64_t I, int64_t K, int mode, const int32_t* expert_offsets,
+                                              const int32_t* slot_ids, int64_t m_rows, int64_t a_row_div, int act, int rule,
+                                              uint8_t* out_q, int64_t q_stride, uint8_t* out_s, int64_t s_stride, void* stream) {
+    if (mode != MOE_MODE_GROUPED && mode != MOE_MODE_SLOT) return MOE_ERR_SHAPE;
+    if (act < MOE_ACT_SILU_MUL || act > MOE_ACT_MUL || (rule != MOE_MX_FLOOR && rule != MOE_MX_CEIL)) return MOE_ERR_SHAPE;
+    if (m_rows < 0 || m_rows > 0x7FFFFFFF || n_experts < 0 || n_experts > 0x7FFFFFFF || !mx4::widths_ok(I, K, mx4::kGroup)) return MOE_ERR_SHAPE;
+    if (m_rows == 0) return MOE_OK;
+    if (!out_q || !out_s) return MOE_ERR_NULL;
+    if (q_stride < I / 2 || s_stride < I / mx4::kGroup) return MOE_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(out_q) % 2 || q_stride % 2) return MOE_ERR_ALIGN;
+    mx4::GemmArgs g{};
+    g.a = (const char*)a_q; g.a_stride = a_stride; g.a_s = (const char*)a_s; g.a_s_stride = a_s_stride; g.a_n = a_n; g.a_rows = a_rows;
+    g.w = (const char*)w_q; g.w_stride_e = w_stride_e; g.w_stride_n = w_stride_n;
+    g.w_s = (const char*)w_s; g.w_s_stride_e = w_s_stride_e; g.w_s_stride_n = w_s_stride_n;
+    g.n_experts = (int)n_experts; g.N = I; g.K = K; g.offsets = expert_offsets; g.m_rows = (int)m_rows;
+    g.out = out_q; g.out_stride = q_stride; g.s = out_s; g.s_stride = s_stride; g.act = act; g.ceil = rule == MOE_MX_CEIL;
+    const int st = mx4::check_operands(g, n_experts, m_rows, 2 * I, mode, slot_ids, a_row_div);
+    if (st != MOE_OK) return st;
+    if (mode == MOE_MODE_SLOT) return mx4::slot_launch<true>(as_stream(stream), g, slot_ids, a_row_div);
+    return mx4::grouped_launch<true>(as_stream(stream), g);
+}
