@@ -91,7 +91,9 @@ __device__ __forceinline__ void store_act_of(const GemmArgs& g, const v4f (&acc)
     }
 }
 
-template <class C, bool FUSED>
+// BUF: the operands are read as buffers (every extent below kNowhere bytes, K a multiple of 128: scale words are whole); else
+// by 64-bit addresses, with the last words' scales masked.
+template <class C, bool FUSED, bool BUF>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(const GemmArgs g) {
     constexpr int S = C::S, LPS = C::LOADS;
     constexpr int COLS = FUSED ? C::BQ / 2 : C::BQ;    // output columns of a tile
@@ -162,80 +164,118 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
 
     // Producer, as in b16_gemm.hip: past the last tile it goes on with zeros into stages that nobody reads, so the loads in
     // flight can be counted the same way to the end.
-    CodeRows<C::P_LOADS, C::NW> p;
-    CodeRows<C::Q_LOADS, C::NW> q;
-    const char* sc[C::S_LOADS];                        // this lane's scale words: row and half
     int prod_t = start, prod_left = 0, prod_kt = 0, prod_stage = 0;
-    int64_t prod_k = 0;                                // elements: K, or 0 past the last tile
+    const int row_byte = code_byte(wave, lane);
+    // !BUF: each lane's source of every load, and the elements of k (0 past the last tile)
+    const char *p_src[BUF ? 1 : C::P_LOADS], *q_src[BUF ? 1 : C::Q_LOADS], *s_src[BUF ? 1 : C::S_LOADS];
+    int64_t prod_k = 0;
+    // BUF: each lane's offsets; what the step's lanes past the end of k (the last step's second half, or all of them past the
+    // last tile) take instead is or-ed in
+    uint32_t p_off[BUF ? C::P_LOADS : 1], q_off[BUF ? C::Q_LOADS : 1], s_off[BUF ? C::S_LOADS : 1], code_out = 0, scale_out = 0;
+    const bool half_step = BUF && g.K % kStepK != 0;
+    v4i a_buf, w_buf, s_buf[BUF ? C::S_LOADS : 1];
+    if constexpr (BUF) a_buf = buffer_of(g.a, (g.a_n - 1) * g.a_stride + g.K / 2);
+    auto outside = [&]() {
+        const uint32_t all = prod_t < tiles ? 0u : kNowhere;
+        const bool half = half_step && prod_kt == steps - 1;
+        code_out = all | (half && row_byte >= kRowBytes / 2 ? kNowhere : 0u);
+        scale_out = all | (half && (lane & 1) ? kNowhere : 0u);
+    };
     auto aim = [&]() {
         prod_k = prod_t < tiles ? g.K : 0;
-        if (prod_t >= tiles) return;
-        const Tile ti = locate(prod_t);
-        const int l = fresh(lane);
-        prod_left = steps;
-        prod_kt = ti.expert * kStagger % steps;
-        // A row of tile row r: rows past the tile's repeat the last one (their results are dropped), rows whose map entry
-        // is no row of a are zeros.
-        auto a_row = [&](int r) -> int64_t {
-            const int64_t at = ti.row0 + min(r, ti.rows - 1);
-            if (!g.a_rows) return at;
-            const int64_t m = g.a_rows[at];
-            return m >= 0 && m < g.a_n ? m : -1;
-        };
-        // W row of tile row r: a fused tile's wave has 32 gate rows and then the 32 up rows of the same columns.  Columns past
-        // the last repeat it.
-        auto w_row = [&](int r) -> int64_t {
-            if (!FUSED) return min(ti.n0 + r, (int)g.N - 1);
-            const int c = min(ti.n0 + (r >> 6) * 32 + (r & 31), (int)g.N - 1);
-            return c + (r & 32 ? g.N : 0);
-        };
-        p.set([&](int r) -> const char* {
-            const int64_t m = a_row(r);
-            return m < 0 ? nullptr : g.a + m * g.a_stride;
-        }, wave, l);
-        const char* w = g.w + ti.expert * g.w_stride_e;
-        q.set([&](int r) -> const char* { return w + w_row(r) * g.w_stride_n; }, wave, l);
-        const char* w_s = g.w_s + ti.expert * g.w_s_stride_e;
+        if (prod_t < tiles) {
+            const Tile ti = locate(prod_t);
+            const int l = fresh(lane);
+            prod_left = steps;
+            prod_kt = ti.expert * kStagger % steps;
+            // A row of tile row r: rows past the tile's repeat the last one (their results are dropped), rows whose map entry
+            // is no row of a are zeros.
+            auto a_row = [&](int r) -> int64_t {
+                const int64_t at = ti.row0 + min(r, ti.rows - 1);
+                if (!g.a_rows) return at;
+                const int64_t m = g.a_rows[at];
+                return m >= 0 && m < g.a_n ? m : -1;
+            };
+            // W row of tile row r: a fused tile's wave has 32 gate rows and then the 32 up rows of the same columns.  Columns
+            // past the last repeat it.
+            auto w_row = [&](int r) -> int64_t {
+                if (!FUSED) return min(ti.n0 + r, (int)g.N - 1);
+                const int c = min(ti.n0 + (r >> 6) * 32 + (r & 31), (int)g.N - 1);
+                return c + (r & 32 ? g.N : 0);
+            };
+            const char *w = g.w + ti.expert * g.w_stride_e, *w_s = g.w_s + ti.expert * g.w_s_stride_e;
+            if constexpr (BUF) {
+                const int64_t bank = FUSED ? 2 * g.N : g.N;
+                w_buf = buffer_of(w, (bank - 1) * g.w_stride_n + g.K / 2);
 #pragma unroll
-        for (int j = 0; j < C::S_LOADS; j++) {
-            const int r = (j * C::NW + wave) % C::S_GROUPS * 32 + l / 2;
-            const char* at;
-            if (r < C::BP) {
-                const int64_t m = a_row(r);
-                at = m < 0 ? nullptr : g.a_s + m * g.a_s_stride;
+                for (int j = 0; j < C::P_LOADS; j++) {
+                    const int64_t m = a_row(code_row<C::NW>(j, wave, l));
+                    p_off[j] = m < 0 ? kNowhere : (uint32_t)(m * g.a_stride) + row_byte;
+                }
+#pragma unroll
+                for (int j = 0; j < C::Q_LOADS; j++) q_off[j] = (uint32_t)(w_row(code_row<C::NW>(j, wave, l)) * g.w_stride_n) + row_byte;
+#pragma unroll
+                for (int j = 0; j < C::S_LOADS; j++) {
+                    const int g0 = (j * C::NW + wave) % C::S_GROUPS * 32, r = g0 + l / 2;
+                    const bool is_a = g0 < C::BP;                        // wave-uniform
+                    s_buf[j] = is_a ? buffer_of(g.a_s, (g.a_n - 1) * g.a_s_stride + g.K / kGroup) : buffer_of(w_s, (bank - 1) * g.w_s_stride_n + g.K / kGroup);
+                    const int64_t m = is_a ? a_row(r) : w_row(r - C::BP);
+                    s_off[j] = m < 0 ? kNowhere : (uint32_t)(m * (is_a ? g.a_s_stride : g.w_s_stride_n)) + (l & 1) * 4;
+                }
             } else {
-                at = w_s + w_row(r - C::BP) * g.w_s_stride_n;
+#pragma unroll
+                for (int j = 0; j < C::P_LOADS; j++) {
+                    const int64_t m = a_row(code_row<C::NW>(j, wave, l));
+                    p_src[j] = m < 0 ? nullptr : g.a + m * g.a_stride + row_byte;
+                }
+#pragma unroll
+                for (int j = 0; j < C::Q_LOADS; j++) q_src[j] = w + w_row(code_row<C::NW>(j, wave, l)) * g.w_stride_n + row_byte;
+#pragma unroll
+                for (int j = 0; j < C::S_LOADS; j++) {
+                    const int g0 = (j * C::NW + wave) % C::S_GROUPS * 32, r = g0 + l / 2;
+                    const int64_t m = g0 < C::BP ? a_row(r) : w_row(r - C::BP);
+                    s_src[j] = m < 0 ? nullptr : (g0 < C::BP ? g.a_s + m * g.a_s_stride : w_s + m * g.w_s_stride_n) + (l & 1) * 4;
+                }
             }
-            sc[j] = at ? at + (l & 1) * 4 : nullptr;
         }
+        if constexpr (BUF) outside();
     };
+    // Load j of the step that is requested next.
     auto part = [&](int j) {
         const uint32_t dst = lds + prod_stage * C::STAGE;
-        if (j < C::P_LOADS) {
-            p.issue(j, dst, prod_kt, prod_k / 2, wave);
-        } else if (j < C::P_LOADS + C::Q_LOADS) {
-            q.issue(j - C::P_LOADS, dst + C::BP * kRowBytes, prod_kt, prod_k / 2, wave);
+        const int i = j - C::P_LOADS - C::Q_LOADS;
+        if constexpr (BUF) {
+            if (j < C::P_LOADS) buf16(p_off[j] | code_out, a_buf, prod_kt * kRowBytes, dst + wave * 1024 + j * C::NW * 1024);
+            else if (i < 0) buf16(q_off[j - C::P_LOADS] | code_out, w_buf, prod_kt * kRowBytes, dst + wave * 1024 + j * C::NW * 1024);
+            else buf4(s_off[i] | scale_out, s_buf[i], prod_kt * kRowScales, dst + C::CODES + (i * C::NW + wave) % C::S_GROUPS * 256);
+        } else if (i < 0) {
+            const int64_t at = (int64_t)prod_kt * kRowBytes;
+            const char* src = j < C::P_LOADS ? p_src[j] : q_src[j - C::P_LOADS];
+            b16::dma16(row_byte < prod_k / 2 - at && src ? src + at : (const char*)&b16::kZeroPiece, dst + wave * 1024 + j * C::NW * 1024);
         } else {
-            const int i = j - C::P_LOADS - C::Q_LOADS;
             const int64_t at = (int64_t)prod_kt * kRowScales;
-            const bool in = (lane & 1) * 4 < prod_k / kGroup - at && sc[i] != nullptr;
-            dma4(in ? sc[i] + at : (const char*)&b16::kZeroPiece, dst + C::CODES + (i * C::NW + wave) % C::S_GROUPS * 256);
+            const bool in = (lane & 1) * 4 < prod_k / kGroup - at && s_src[i];
+            dma4(in ? s_src[i] + at : (const char*)&b16::kZeroPiece, dst + C::CODES + (i * C::NW + wave) % C::S_GROUPS * 256);
         }
-        if (j == LPS - 1) {
-            prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
-            prod_kt = prod_kt + 1 == steps ? 0 : prod_kt + 1;
-            if (--prod_left <= 0) {
-                prod_t += G;
-                aim();
-            }
+    };
+    auto advance = [&]() {                             // past the step whose loads have gone out
+        prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
+        prod_kt = prod_kt + 1 == steps ? 0 : prod_kt + 1;
+        if (--prod_left <= 0) {
+            prod_t += G;
+            aim();
+        } else if (half_step) {
+            outside();
         }
     };
     auto produce = [&]() {
 #pragma unroll
         for (int j = 0; j < LPS; j++) part(j);
+        advance();
     };
     if (start >= tiles) return;
     aim();
+    constexpr bool PIPED = C::MP >= 4;                 // a wave's MFMAs are worth the software pipeline
 #pragma unroll 1
     for (int i = 0; i < S - 1; i++) produce();
 
@@ -248,6 +288,11 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
     sq.set(wq * C::MQ, lane);
 
     int stage = 0;
+    Frags<C> f;
+    if constexpr (PIPED) {
+        arrive<S, LPS>();
+        f.first(fp, fq, sp, sq, lds);
+    }
 #pragma unroll 1
     for (int t = start; t < tiles; t += G) {
         const Tile ti = locate(t);
@@ -262,9 +307,15 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
         for (int i = 0; i < steps; i++) {
             const uint32_t at = lds + stage * C::STAGE;
             stage = stage + 1 == S ? 0 : stage + 1;
-            arrive<S, LPS>();
-            produce();                                 // into the stage that the step before this one read
-            step_plain<C>(acc, fp, fq, sp, sq, at, scale_mask(blocks - kt * kRowScales, lane));
+            const uint32_t mask = BUF ? 0xFFFFu : scale_mask(blocks - kt * kRowScales, lane);
+            if constexpr (PIPED) {
+                step_pipelined<C, !BUF>(acc, f, fp, fq, sp, sq, at, lds + stage * C::STAGE, mask, part);
+                advance();
+            } else {
+                arrive<S, LPS>();
+                produce();                             // into the stage that the step before this one read
+                step_plain<C, !BUF>(acc, fp, fq, sp, sq, at, mask);
+            }
             kt = kt + 1 == steps ? 0 : kt + 1;
         }
         const int64_t c0 = ti.n0 + wq * (COLS / C::WQ);
@@ -278,7 +329,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
-template <class C, bool FUSED>
+template <class C, bool FUSED, bool BUF>
 int resident_blocks() {
     static std::atomic<int> cached[64];   // concurrent first calls may both fill it, with the same value
     int dev = 0;
@@ -286,7 +337,7 @@ int resident_blocks() {
     int c = cached[dev].load(std::memory_order_relaxed);
     if (c == 0) {
         int per_cu = 0, cus = 0;
-        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, mx4_gemm_kernel<C, FUSED>, C::THREADS, 0) != hipSuccess ||
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, mx4_gemm_kernel<C, FUSED, BUF>, C::THREADS, 0) != hipSuccess ||
             hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
             return 0;
         c = per_cu * cus;
@@ -301,17 +352,25 @@ using Tile64 = Cfg<64, 256, 2, 4, 3, 1>;
 using Tile64x64 = Cfg<64, 64, 4, 1, 3, 2>;
 using Tile32x64 = Cfg<32, 64, 2, 1, 4, 2>;
 
-template <class C, bool FUSED>
-int launch_cfg(hipStream_t st, GemmArgs g) {
+template <class C, bool FUSED, bool BUF>
+int launch_form(hipStream_t st, GemmArgs g) {
     const int64_t n_tiles = ceil_div(g.N, FUSED ? C::BQ / 2 : C::BQ);
     const int64_t most = (g.m_rows / C::BP + std::min<int64_t>(g.n_experts, g.m_rows)) * n_tiles;
     if (most > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
-    int wgs = resident_blocks<C, FUSED>() / kXcds * kXcds;
+    int wgs = resident_blocks<C, FUSED, BUF>() / kXcds * kXcds;
     if (wgs < kXcds) return MOE_ERR_HIP;
     wgs = (int)std::min<int64_t>(wgs, ceil_div(most, kXcds) * kXcds);
     g.n_tiles = (int)n_tiles;
-    hipLaunchKernelGGL((mx4_gemm_kernel<C, FUSED>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
+    hipLaunchKernelGGL((mx4_gemm_kernel<C, FUSED, BUF>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
     return launch_status();
+}
+
+template <class C, bool FUSED>
+int launch_cfg(hipStream_t st, const GemmArgs& g) {
+    const int64_t bank = (FUSED ? 2 : 1) * g.N, scales = g.K / kGroup;
+    const bool buf = g.K % 128 == 0 && std::max({(g.a_n - 1) * g.a_stride + g.K / 2, (g.a_n - 1) * g.a_s_stride + scales,
+                                                 (bank - 1) * g.w_stride_n + g.K / 2, (bank - 1) * g.w_s_stride_n + scales}) < (int64_t)kNowhere;
+    return buf ? launch_form<C, FUSED, true>(st, g) : launch_form<C, FUSED, false>(st, g);
 }
 
 struct TileCost {

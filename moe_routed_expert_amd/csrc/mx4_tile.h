@@ -24,7 +24,6 @@ using b16::block_barrier;
 using b16::fresh;
 using b16::last_at_most;
 using b16::lds_offset;
-using b16::parts_per_group;
 using b16::pieces;
 using b16::wait_loads;
 
@@ -45,49 +44,50 @@ struct Cfg {
     static constexpr int S_GROUPS = (BP + BQ) / 32;                          // 4-byte DMAs of a step, 32 rows each
     static constexpr int S_LOADS = (S_GROUPS + NW - 1) / NW;                 // of a wave (some twice, the same words)
     static constexpr int LOADS = P_LOADS + Q_LOADS + S_LOADS;
-    static_assert(BP % 32 == 0 && BQ % 32 == 0 && (BP / 8) % NW == 0 && (BQ / 8) % NW == 0, "waves cover the rows evenly");
+    static constexpr int PER = (LOADS + 2 * MP - 3) / (2 * MP - 2) > 1 ? 2 : 1;   // loads of a group of the pipelined step
+    static_assert(NW % 2 == 0 && BP % 32 == 0 && BQ % 32 == 0 && (BP / 8) % NW == 0 && (BQ / 8) % NW == 0, "waves cover the rows evenly");
 };
 
-// 64 lanes x 4 bytes from each lane's src to the LDS bytes [dst, dst + 256) in lane order (see b16::dma16).
+// Piece c (16 bytes, one block of 32) of tile row r lies in slot slot_of(c) ^ ((r >> 1) & 7) of the row's eight: the lanes
+// that one LDS cycle serves (eight rows of one quarter of the wave, eight other rows of the next) fall into different banks.
+__device__ __forceinline__ int slot_of(int c) { return (c >> 1) | ((c & 1) << 2); }
+__device__ __forceinline__ int piece_in(int slot) { return ((slot & 3) << 1) | (slot >> 2); }
+
+// The loads into LDS, 64 lanes of 16 or 4 bytes in lane order, written in asm as b16::dma16 is: the compiler would wait for
+// all of them before any LDS read.
+//   dma16 / dma4  from an address of each lane's own: operands of any extent.
+//   buf16 / buf4  from a buffer (base and extent in scalar registers) at a 32-bit offset of each lane's own plus a scalar one:
+//                 no vector instruction per load, and an offset of kNowhere or more is out of range, which reads as zeros.
 __device__ __forceinline__ void dma4(const void* src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ v4i buffer_of(const char* base, int64_t extent) {
+    const uint64_t b = (uint64_t)base;
+    return v4i{(int)(uint32_t)b, (int)(uint32_t)(b >> 32), (int)extent, 0x00020000};
+}
+__device__ __forceinline__ void buf16(uint32_t off, const v4i& buf, uint32_t at, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(off), "s"(buf), "s"(dst), "s"(at) : "memory", "m0");
+}
+__device__ __forceinline__ void buf4(uint32_t off, const v4i& buf, uint32_t at, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %3 offen lds" ::"v"(off), "s"(buf), "s"(dst), "s"(at) : "memory", "m0");
+}
 
-// The 8-row groups of an operand that a wave stages.  A row that does not exist (nullptr) is a row of zeros.
-template <int LOADS, int NW>
-struct CodeRows {
-    const char* p[LOADS];
-    int k0;                                                                 // first byte of this lane's pieces
-
-    // row(r): the codes of tile row r, or nullptr.
-    template <class Row>
-    __device__ __forceinline__ void set(const Row& row, int wave, int lane) {
-#pragma unroll
-        for (int j = 0; j < LOADS; j++) {
-            const int r = (j * NW + wave) * 8 + lane / 8;
-            const int c = (lane % 8) ^ ((r >> 1) & 7);                      // the same for every j
-            const char* at = row(r);
-            p[j] = at ? at + c * 16 : nullptr;
-            k0 = c * 16;
-        }
-    }
-    // Load j of step kt of rows of `bytes` codes (0: zeros), into the operand's part of the stage at LDS byte dst.
-    __device__ __forceinline__ void issue(int j, uint32_t dst, int kt, int64_t bytes, int wave) const {
-        const int64_t at = (int64_t)kt * kRowBytes;
-        const bool in = k0 < bytes - at && p[j] != nullptr;
-        b16::dma16(in ? p[j] + at : (const char*)&b16::kZeroPiece, dst + (j * NW + wave) * 1024);
-    }
-};
+// DMA j of a wave's code loads takes tile rows 8 (j NW + wave) .. + 7, a row per 8 lanes; the byte of the row's 128 that the
+// lane's slot holds is the same for every j, since NW is even.
+template <int NW>
+__device__ __forceinline__ int code_row(int j, int wave, int lane) { return (j * NW + wave) * 8 + lane / 8; }
+__device__ __forceinline__ int code_byte(int wave, int lane) { return 16 * piece_in((lane % 8) ^ ((wave * 4 + lane / 16) & 7)); }
 
 // This lane's fragment addresses in a stage: sub-tile m of 16 rows from row 16 * sub0; MFMA ks takes piece 2q + ks.
 struct CodeFrag {
     uint32_t a;
     __device__ __forceinline__ void set(int sub0, int lane) {
         const int r = lane & 15, q = lane >> 4;
-        a = (uint32_t)(sub0 * 2048 + r * 128 + (((2 * q) ^ (r >> 1)) << 4));
+        a = (uint32_t)(sub0 * 2048 + r * 128 + ((q ^ (r >> 1)) << 4));
     }
     __device__ __forceinline__ v4i read(uint32_t part, int m, int ks) const {
-        return *(const MOE_LDS v4i*)(uintptr_t)(part + (a ^ (ks << 4)) + m * 2048);
+        return *(const MOE_LDS v4i*)(uintptr_t)(part + (a ^ (ks << 6)) + m * 2048);
     }
 };
 
@@ -122,15 +122,15 @@ struct StageParts {
 
 // One step of a wave's MP x MQ sub-tiles.  Q is the MFMA's row operand, so lane l holds of sub-tile (m, n) the element
 // p = 16m + l % 16, q = 16n + 4 (l / 16) + 0..3.
-template <class C>
+template <class C, bool MASKED>
 __device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeFrag& fp, const CodeFrag& fq, const ScaleFrag& sp,
                                            const ScaleFrag& sq, uint32_t at, uint32_t mask) {
     const StageParts<C> st(at);
     uint32_t qs[C::MQ], ps[C::MP];
 #pragma unroll
-    for (int n = 0; n < C::MQ; n++) qs[n] = sq.read(st.sq, n) & mask;
+    for (int n = 0; n < C::MQ; n++) qs[n] = sq.read(st.sq, n) & (MASKED ? mask : 0xFFFFu);
 #pragma unroll
-    for (int m = 0; m < C::MP; m++) ps[m] = sp.read(st.sp, m) & mask;
+    for (int m = 0; m < C::MP; m++) ps[m] = sp.read(st.sp, m) & (MASKED ? mask : 0xFFFFu);
 #pragma unroll
     for (int ks = 0; ks < 2; ks++) {
         v4i q[C::MQ];
@@ -144,6 +144,74 @@ __device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeF
                 acc[m][n] = ks == 0 ? mfma<0>(q[n], qs[n], p, ps[m], acc[m][n]) : mfma<1>(q[n], qs[n], p, ps[m], acc[m][n]);
         }
     }
+}
+
+// The same step as a software pipeline (b16::step_pipelined), for tiles whose MFMAs are the bound: 2 MP groups of MQ MFMAs,
+// each group's P fragment and scales read while the group before it is multiplied; the workgroup meets before the last
+// group, which covers the first reads of the next stage; the loads of the stage that takes the last one's place are spread
+// over the first groups, PER each.  No branch lies within a step (the producer moves on between steps) and the accumulators are
+// named at its end: the compiler would sink the MFMAs past a branch, and the loads before it would go out all at once.
+template <class C>
+struct Frags {
+    v4i p[2], q[2][C::MQ];
+    uint32_t ps[C::MP], qs[C::MQ], qn[C::MQ];          // scales; qn: the next stage's
+    __device__ __forceinline__ void first(const CodeFrag& fp, const CodeFrag& fq, const ScaleFrag& sp, const ScaleFrag& sq, uint32_t at) {
+        const StageParts<C> st(at);
+#pragma unroll
+        for (int n = 0; n < C::MQ; n++) q[0][n] = fq.read(st.q, n, 0);
+        p[0] = fp.read(st.p, 0, 0);
+#pragma unroll
+        for (int n = 0; n < C::MQ; n++) qn[n] = sq.read(st.sq, n);
+        ps[0] = sp.read(st.sp, 0);
+    }
+};
+
+template <class C, bool MASKED, class Part>
+__device__ __forceinline__ void step_pipelined(v4f (&acc)[C::MP][C::MQ], Frags<C>& f, const CodeFrag& fp, const CodeFrag& fq,
+                                               const ScaleFrag& sp, const ScaleFrag& sq, uint32_t at, uint32_t next, uint32_t mask,
+                                               const Part& part) {
+    constexpr int MP = C::MP, MQ = C::MQ, G = 2 * MP, PARTS = C::LOADS, PER = C::PER;
+    static_assert((G - 2) * PER >= PARTS, "all loads of a step go out before the workgroup meets");
+    constexpr int Q1 = MP > MQ ? MP - 1 - MQ : 0;         // from this group on, one fragment of Q's second half each
+    static_assert(MP >= 4 && MP >= MQ, "Q's second half is read before its first group");
+    const StageParts<C> st(at);
+#pragma unroll
+    for (int i = 0; i < G; i++) {
+        const int m = i % MP, ks = i / MP;
+        if (i == G - 1) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            arrive<C::S, PARTS>();
+        }
+#pragma unroll
+        for (int u = 0; u < PER; u++) {
+            const int j = i * PER + u;
+            if (j < PARTS) part(j);
+        }
+        if (ks == 0) {
+            if (m == 0) {
+#pragma unroll
+                for (int n = 0; n < MQ; n++) f.qs[n] = MASKED ? f.qn[n] & mask : f.qn[n];
+            }
+            if constexpr (MASKED) f.ps[m] &= mask;
+        }
+        if (i < G - 1) {
+            if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(st.q, i - Q1, 1);
+            f.p[(i + 1) % 2] = fp.read(st.p, (i + 1) % MP, (i + 1) / MP);
+            if (i + 1 < MP) f.ps[i + 1] = sp.read(st.sp, i + 1);
+        } else {
+            f.first(fp, fq, sp, sq, next);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < MQ; n++)
+            acc[m][n] = ks == 0 ? mfma<0>(f.q[0][n], f.qs[n], f.p[i % 2], f.ps[m], acc[m][n])
+                                : mfma<1>(f.q[1][n], f.qs[n], f.p[i % 2], f.ps[m], acc[m][n]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int m = 0; m < MP; m++)
+#pragma unroll
+        for (int n = 0; n < MQ; n++) asm volatile("" : "+v"(acc[m][n]));
 }
 
 }  // namespace mx4
