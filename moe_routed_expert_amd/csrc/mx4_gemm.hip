@@ -18,79 +18,6 @@ namespace moe {
 namespace mx4 {
 namespace {
 
-using b16::kMaxExperts;
-using b16::kMaxWidth;
-using b16::kPanel;
-using b16::kXcds;
-
-constexpr int kStagger = 5;                   // an expert's tiles walk k in rotation from step kStagger * e (b16_gemm.hip)
-
-struct GemmArgs {
-    const char* a;
-    int64_t a_stride;                         // bytes, as all strides of codes and scales
-    const char* a_s;
-    int64_t a_s_stride;
-    int64_t a_n;                              // rows of a, for the map's bounds
-    const int32_t* a_rows;
-    const char* w;
-    int64_t w_stride_e, w_stride_n;
-    const char* w_s;
-    int64_t w_s_stride_e, w_s_stride_n;
-    int n_experts;
-    int64_t N, K;                             // fused: N = I, the act columns
-    const int32_t* offsets;
-    int m_rows;
-    int n_tiles;
-    void* out;                                // fused: codes
-    int out_dt;
-    int64_t out_stride;                       // elements (fused: bytes)
-    uint8_t* s;                               // fused: scale bytes
-    int64_t s_stride;
-    int act, ceil;
-};
-
-__device__ __forceinline__ uint32_t max_lanes16_32(uint32_t v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    v = a[0] > a[1] ? a[0] : a[1];
-    const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    return b[0] > b[1] ? b[0] : b[1];
-}
-
-// The fused epilogue of a wave: rows row0 + 16m + lane % 16 (below `rows`), act columns col0 .. col0 + 31 (below `cols`).
-template <int ACT, int MP>
-__device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP][4], int64_t row0, int rows, int64_t col0, int lane) {
-    const int r = lane & 15, q = lane >> 4;
-#pragma unroll
-    for (int m = 0; m < MP; m++) {
-        if (m * 16 >= rows) break;                                          // wave-uniform
-        float h[8];
-#pragma unroll
-        for (int n = 0; n < 2; n++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) h[4 * n + i] = gated<ACT>(acc[m][n][i], acc[m][n + 2][i]);
-        const uint32_t byte = scale_byte(max_lanes16_32(max_bits8(h)), g.ceil != 0);
-        const uint32_t codes = encode8(h, byte);
-        if (m * 16 + r < rows) {
-            const int64_t row = row0 + m * 16 + r;
-            uint8_t* out = (uint8_t*)g.out + row * g.out_stride + col0 / 2 + 2 * q;
-            *reinterpret_cast<uint16_t*>(out) = (uint16_t)codes;
-            *reinterpret_cast<uint16_t*>(out + 8) = (uint16_t)(codes >> 16);
-            if (q == 0) g.s[row * g.s_stride + col0 / kGroup] = (uint8_t)byte;
-        }
-    }
-}
-
-template <int MP>
-__device__ __forceinline__ void store_act_of(const GemmArgs& g, const v4f (&acc)[MP][4], int64_t row0, int rows, int64_t col0, int lane) {
-    switch (g.act) {
-        case 1: return store_act<1>(g, acc, row0, rows, col0, lane);
-        case 2: return store_act<2>(g, acc, row0, rows, col0, lane);
-        case 3: return store_act<3>(g, acc, row0, rows, col0, lane);
-        case 4: return store_act<4>(g, acc, row0, rows, col0, lane);
-        default: return store_act<5>(g, acc, row0, rows, col0, lane);
-    }
-}
-
 // BUF: the operands are read as buffers (every extent below kNowhere bytes, K a multiple of 128: scale words are whole); else
 // by 64-bit addresses, with the last words' scales masked.
 template <class C, bool FUSED, bool BUF>
@@ -98,231 +25,221 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
     constexpr int S = C::S, LPS = C::LOADS;
     constexpr int COLS = FUSED ? C::BQ / 2 : C::BQ;    // output columns of a tile
     static_assert(C::MQ == 4, "a wave holds 32 gate and 32 up columns, or 64 columns");
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::STAGE];
-    __shared__ int first_tile[kMaxExperts + 1];        // M tiles before expert e
-    __shared__ uint32_t wave_sum[2 * C::NW];
-    __shared__ int decreases;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::CODES + C::CHUNK];
+    __shared__ int first_tile[kMaxExperts];
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int E = g.n_experts;
-    auto clamped = [&](int e) { return min(max(g.offsets[e], 0), g.m_rows); };
+    Walk<C, COLS> walk(g, first_tile, reinterpret_cast<uint32_t*>(ring), tid, lane, wave);
+    if (walk.start >= walk.tiles) return;
 
-    {                                                  // the tile table: EPT consecutive experts per thread
-        constexpr int EPT = kMaxExperts / C::THREADS;
-        uint32_t count[EPT], tiles = 0, down = 0;
-#pragma unroll
-        for (int i = 0; i < EPT; i++) {
-            const int e = tid * EPT + i;
-            count[i] = 0;
-            if (e < E) {
-                const int lo = clamped(e), to = clamped(e + 1);
-                count[i] = (uint32_t)pieces(max(to, lo) - lo, C::BP);
-                down += to < lo;
-            }
-            tiles += count[i];
-        }
-        uint32_t w = tiles, d = down;
-        b16::block_exclusive_scan2<C::NW>(w, d, wave_sum, lane, wave);
-#pragma unroll
-        for (int i = 0; i < EPT; i++) {
-            const int e = tid * EPT + i;
-            if (e < E) first_tile[e] = (int)w;
-            w += count[i];
-            if (e == E - 1) first_tile[E] = (int)w;
-        }
-        if (tid == C::THREADS - 1) decreases = (int)(d + down);
-        __syncthreads();
-    }
-    // Experts that overlap may have more tiles than the host counted on, and share rows: nothing is computed.
-    if (__builtin_amdgcn_readfirstlane(decreases) != 0) return;
-    const int m_tiles = __builtin_amdgcn_readfirstlane(first_tile[E]);
-    const int tiles = m_tiles * g.n_tiles;
-    const int G = gridDim.x;
-    const int start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
+    const uint32_t lds = lds_offset(ring), chunk_at = lds + S * C::CODES;
+    const int steps = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup), words = (blocks + 3) / 4;
+    const int chunks = (steps + kChunk - 1) / kChunk;
+    auto first_chunk = [&](int expert) { return expert * kStagger % chunks; };
 
-    struct Tile {
-        int expert, row0, rows, n0;
-    };
-    auto locate = [&](int t) {
-        const int per = kPanel * g.n_tiles;
-        const int panel = t / per, r = t - panel * per;
-        const int height = min(kPanel, m_tiles - panel * kPanel);
-        const int nt = r / height, mt = panel * kPanel + r - nt * height;
-        const int e = last_at_most([&](int i) { return first_tile[i]; }, E, mt, lane);
-        Tile ti;
-        ti.expert = e;
-        const int from = __builtin_amdgcn_readfirstlane(clamped(e)), end = __builtin_amdgcn_readfirstlane(clamped(e + 1));
-        ti.row0 = from + (mt - __builtin_amdgcn_readfirstlane(first_tile[e])) * C::BP;
-        ti.rows = min(end - ti.row0, C::BP);
-        ti.n0 = nt * COLS;
-        return ti;
+    // The tile last looked up: the producers and the consumer come to a tile one after the other.
+    Tile near{};
+    int near_t = -1;
+    auto tile_of = [&](int t) __attribute__((always_inline)) {
+        if (t != near_t) {
+            near = walk.locate(t, lane);
+            near_t = t;
+        }
+        return near;
     };
 
-    const uint32_t lds = lds_offset(ring);
-    const int steps = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup);
-
-    // Producer, as in b16_gemm.hip: past the last tile it goes on with zeros into stages that nobody reads, so the loads in
-    // flight can be counted the same way to the end.
-    int prod_t = start, prod_left = 0, prod_kt = 0, prod_stage = 0;
+    // Producer of codes: the step that is requested next.  Past the last tile it goes on with zeros into stages that nobody
+    // reads, so the loads in flight can be counted the same way to the end.
+    int prod_t = walk.start, prod_left = 0, prod_kt = 0, prod_stage = 0;
     const int row_byte = code_byte(wave, lane);
-    // !BUF: each lane's source of every load, and the elements of k (0 past the last tile)
+    // !BUF: each lane's source of every load, and the bytes of a row (0 past the last tile)
     const char *p_src[BUF ? 1 : C::P_LOADS], *q_src[BUF ? 1 : C::Q_LOADS], *s_src[BUF ? 1 : C::S_LOADS];
-    int64_t prod_k = 0;
+    int64_t prod_bytes = 0;
     // BUF: each lane's offsets; what the step's lanes past the end of k (the last step's second half, or all of them past the
     // last tile) take instead is or-ed in
-    uint32_t p_off[BUF ? C::P_LOADS : 1], q_off[BUF ? C::Q_LOADS : 1], s_off[BUF ? C::S_LOADS : 1], code_out = 0, scale_out = 0;
+    uint32_t p_off[BUF ? C::P_LOADS : 1], q_off[BUF ? C::Q_LOADS : 1], s_off[BUF ? C::S_LOADS : 1], code_out = 0;
     const bool half_step = BUF && g.K % kStepK != 0;
-    v4i a_buf, w_buf, s_buf[BUF ? C::S_LOADS : 1];
-    if constexpr (BUF) a_buf = buffer_of(g.a, (g.a_n - 1) * g.a_stride + g.K / 2);
-    auto outside = [&]() {
-        const uint32_t all = prod_t < tiles ? 0u : kNowhere;
-        const bool half = half_step && prod_kt == steps - 1;
-        code_out = all | (half && row_byte >= kRowBytes / 2 ? kNowhere : 0u);
-        scale_out = all | (half && (lane & 1) ? kNowhere : 0u);
+    v4i a_buf, as_buf, w_buf, ws_buf;
+    if constexpr (BUF) {
+        a_buf = buffer_of(g.a, (g.a_n - 1) * g.a_stride + g.K / 2);
+        as_buf = buffer_of(g.a_s, (g.a_n - 1) * g.a_s_stride + blocks);
+    }
+    const int64_t bank = FUSED ? 2 * g.N : g.N;
+    auto outside = [&]() __attribute__((always_inline)) {
+        code_out = prod_t >= walk.tiles || (half_step && prod_kt == steps - 1 && row_byte >= kRowBytes / 2) ? kNowhere : 0u;
     };
-    auto aim = [&]() {
-        prod_k = prod_t < tiles ? g.K : 0;
-        if (prod_t < tiles) {
-            const Tile ti = locate(prod_t);
+    auto aim = [&]() __attribute__((always_inline)) {
+        prod_bytes = prod_t < walk.tiles ? g.K / 2 : 0;
+        if (prod_t < walk.tiles) {
+            const Tile ti = tile_of(prod_t);
             const int l = fresh(lane);
             prod_left = steps;
-            prod_kt = ti.expert * kStagger % steps;
-            // A row of tile row r: rows past the tile's repeat the last one (their results are dropped), rows whose map entry
-            // is no row of a are zeros.
-            auto a_row = [&](int r) -> int64_t {
-                const int64_t at = ti.row0 + min(r, ti.rows - 1);
-                if (!g.a_rows) return at;
-                const int64_t m = g.a_rows[at];
-                return m >= 0 && m < g.a_n ? m : -1;
-            };
-            // W row of tile row r: a fused tile's wave has 32 gate rows and then the 32 up rows of the same columns.  Columns
-            // past the last repeat it.
-            auto w_row = [&](int r) -> int64_t {
-                if (!FUSED) return min(ti.n0 + r, (int)g.N - 1);
-                const int c = min(ti.n0 + (r >> 6) * 32 + (r & 31), (int)g.N - 1);
-                return c + (r & 32 ? g.N : 0);
-            };
-            const char *w = g.w + ti.expert * g.w_stride_e, *w_s = g.w_s + ti.expert * g.w_s_stride_e;
-            if constexpr (BUF) {
-                const int64_t bank = FUSED ? 2 * g.N : g.N;
-                w_buf = buffer_of(w, (bank - 1) * g.w_stride_n + g.K / 2);
+            prod_kt = first_chunk(ti.expert) * kChunk;
+            const char* w = g.w + ti.expert * g.w_stride_e;
+            if constexpr (BUF) w_buf = buffer_of(w, (bank - 1) * g.w_stride_n + g.K / 2);
 #pragma unroll
-                for (int j = 0; j < C::P_LOADS; j++) {
-                    const int64_t m = a_row(code_row<C::NW>(j, wave, l));
-                    p_off[j] = m < 0 ? kNowhere : (uint32_t)(m * g.a_stride) + row_byte;
-                }
+            for (int j = 0; j < C::P_LOADS; j++) {
+                const int64_t m = walk.a_row(ti, code_row<C::NW>(j, wave, l));
+                if constexpr (BUF) p_off[j] = m < 0 ? kNowhere : (uint32_t)(m * g.a_stride) + row_byte;
+                else p_src[j] = m < 0 ? nullptr : g.a + m * g.a_stride + row_byte;
+            }
 #pragma unroll
-                for (int j = 0; j < C::Q_LOADS; j++) q_off[j] = (uint32_t)(w_row(code_row<C::NW>(j, wave, l)) * g.w_stride_n) + row_byte;
-#pragma unroll
-                for (int j = 0; j < C::S_LOADS; j++) {
-                    const int g0 = (j * C::NW + wave) % C::S_GROUPS * 32, r = g0 + l / 2;
-                    const bool is_a = g0 < C::BP;                        // wave-uniform
-                    s_buf[j] = is_a ? buffer_of(g.a_s, (g.a_n - 1) * g.a_s_stride + g.K / kGroup) : buffer_of(w_s, (bank - 1) * g.w_s_stride_n + g.K / kGroup);
-                    const int64_t m = is_a ? a_row(r) : w_row(r - C::BP);
-                    s_off[j] = m < 0 ? kNowhere : (uint32_t)(m * (is_a ? g.a_s_stride : g.w_s_stride_n)) + (l & 1) * 4;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < C::P_LOADS; j++) {
-                    const int64_t m = a_row(code_row<C::NW>(j, wave, l));
-                    p_src[j] = m < 0 ? nullptr : g.a + m * g.a_stride + row_byte;
-                }
-#pragma unroll
-                for (int j = 0; j < C::Q_LOADS; j++) q_src[j] = w + w_row(code_row<C::NW>(j, wave, l)) * g.w_stride_n + row_byte;
-#pragma unroll
-                for (int j = 0; j < C::S_LOADS; j++) {
-                    const int g0 = (j * C::NW + wave) % C::S_GROUPS * 32, r = g0 + l / 2;
-                    const int64_t m = g0 < C::BP ? a_row(r) : w_row(r - C::BP);
-                    s_src[j] = m < 0 ? nullptr : (g0 < C::BP ? g.a_s + m * g.a_s_stride : w_s + m * g.w_s_stride_n) + (l & 1) * 4;
-                }
+            for (int j = 0; j < C::Q_LOADS; j++) {
+                const int64_t at = walk.template w_row<FUSED>(ti, code_row<C::NW>(j, wave, l)) * g.w_stride_n;
+                if constexpr (BUF) q_off[j] = (uint32_t)at + row_byte;
+                else q_src[j] = w + at + row_byte;
             }
         }
         if constexpr (BUF) outside();
     };
     // Load j of the step that is requested next.
-    auto part = [&](int j) {
-        const uint32_t dst = lds + prod_stage * C::STAGE;
-        const int i = j - C::P_LOADS - C::Q_LOADS;
+    auto part = [&](int j) __attribute__((always_inline)) {
+        const uint32_t dst = lds + prod_stage * C::CODES + wave * 1024 + j * C::NW * 1024;
         if constexpr (BUF) {
-            if (j < C::P_LOADS) buf16(p_off[j] | code_out, a_buf, prod_kt * kRowBytes, dst + wave * 1024 + j * C::NW * 1024);
-            else if (i < 0) buf16(q_off[j - C::P_LOADS] | code_out, w_buf, prod_kt * kRowBytes, dst + wave * 1024 + j * C::NW * 1024);
-            else buf4(s_off[i] | scale_out, s_buf[i], prod_kt * kRowScales, dst + C::CODES + (i * C::NW + wave) % C::S_GROUPS * 256);
-        } else if (i < 0) {
+            if (j < C::P_LOADS) buf16(p_off[j] | code_out, a_buf, prod_kt * kRowBytes, dst);
+            else buf16(q_off[j - C::P_LOADS] | code_out, w_buf, prod_kt * kRowBytes, dst);
+        } else {
             const int64_t at = (int64_t)prod_kt * kRowBytes;
             const char* src = j < C::P_LOADS ? p_src[j] : q_src[j - C::P_LOADS];
-            b16::dma16(row_byte < prod_k / 2 - at && src ? src + at : (const char*)&b16::kZeroPiece, dst + wave * 1024 + j * C::NW * 1024);
-        } else {
-            const int64_t at = (int64_t)prod_kt * kRowScales;
-            const bool in = (lane & 1) * 4 < prod_k / kGroup - at && s_src[i];
-            dma4(in ? s_src[i] + at : (const char*)&b16::kZeroPiece, dst + C::CODES + (i * C::NW + wave) % C::S_GROUPS * 256);
+            b16::dma16(row_byte < prod_bytes - at && src ? src + at : (const char*)&b16::kZeroPiece, dst);
         }
     };
-    auto advance = [&]() {                             // past the step whose loads have gone out
+    auto advance = [&]() __attribute__((always_inline)) {                      // past the step whose loads have gone out
         prod_stage = prod_stage + 1 == S ? 0 : prod_stage + 1;
         prod_kt = prod_kt + 1 == steps ? 0 : prod_kt + 1;
         if (--prod_left <= 0) {
-            prod_t += G;
+            prod_t += walk.G;
             aim();
         } else if (half_step) {
             outside();
         }
     };
-    auto produce = [&]() {
+    auto produce = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < LPS; j++) part(j);
         advance();
     };
-    if (start >= tiles) return;
+
+    // Producer of scales: the chunk that is requested next (a tile's chunks in the order of its steps).  DMA j of a wave takes
+    // eight rows, eight words of each; lane 8i + 4h + t: the word of step t's blocks 4h .. 4h+3, so that a lane of the
+    // consumer finds its four words next to each other.
+    int sc_t = walk.start, sc_left = 0, sc_c = 0;
+    const int sc_word = 2 * (lane & 3) + ((lane >> 2) & 1);
+    auto aim_scales = [&]() __attribute__((always_inline)) {
+        sc_left = chunks;
+        if (sc_t >= walk.tiles) return;
+        const Tile ti = tile_of(sc_t);
+        const int l = fresh(lane);
+        sc_c = first_chunk(ti.expert);
+        const char* w_s = g.w_s + ti.expert * g.w_s_stride_e;
+        if constexpr (BUF) ws_buf = buffer_of(w_s, (bank - 1) * g.w_s_stride_n + blocks);
+#pragma unroll
+        for (int j = 0; j < C::S_LOADS; j++) {
+            const int r0 = (wave * C::S_LOADS + j) * 8, r = r0 + l / 8;
+            const bool is_a = r0 < C::BP;              // wave-uniform
+            const int64_t m = is_a ? walk.a_row(ti, r) : walk.template w_row<FUSED>(ti, r - C::BP);
+            if constexpr (BUF) s_off[j] = m < 0 ? kNowhere : (uint32_t)(m * (is_a ? g.a_s_stride : g.w_s_stride_n)) + sc_word * 4;
+            else s_src[j] = m < 0 ? nullptr : (is_a ? g.a_s + m * g.a_s_stride : w_s + m * g.w_s_stride_n) + sc_word * 4;
+        }
+    };
+    auto request_scales = [&]() __attribute__((always_inline)) {
+        if (sc_left == 0) {
+            sc_t += walk.G;
+            aim_scales();
+        }
+        const bool in = sc_t < walk.tiles && sc_word < words - 2 * kChunk * sc_c;
+#pragma unroll
+        for (int j = 0; j < C::S_LOADS; j++) {
+            const uint32_t dst = chunk_at + (wave * C::S_LOADS + j) * 256;
+            const int64_t at = (int64_t)sc_c * (kChunk * kRowScales);
+            if constexpr (BUF) {
+                const uint32_t off = in ? s_off[j] : kNowhere;
+                if ((wave * C::S_LOADS + j) * 8 < C::BP) buf4(off, as_buf, (uint32_t)at, dst);
+                else buf4(off, ws_buf, (uint32_t)at, dst);
+            } else {
+                dma4(in && s_src[j] ? s_src[j] + at : (const char*)&b16::kZeroPiece, dst);
+            }
+        }
+        sc_c = sc_c + 1 == chunks ? 0 : sc_c + 1;
+        sc_left--;
+    };
+
+    aim_scales();
+    request_scales();
     aim();
     constexpr bool PIPED = C::MP >= 4;                 // a wave's MFMAs are worth the software pipeline
 #pragma unroll 1
     for (int i = 0; i < S - 1; i++) produce();
 
     CodeFrag fp, fq;
-    ScaleFrag sp, sq;
     const int wp = wave / C::WQ, wq = wave % C::WQ;
     fp.set(wp * C::MP, lane);
     fq.set(wq * C::MQ, lane);
-    sp.set(wp * C::MP, lane);
-    sq.set(wq * C::MQ, lane);
+    Scales<C::MP> sp;
+    Scales<C::MQ> sq;
+    const uint32_t sp_at = chunk_at + scale_lane(wp * C::MP, lane), sq_at = chunk_at + C::BP * kChunk * kRowScales + scale_lane(wq * C::MQ, lane);
 
     int stage = 0;
     Frags<C> f;
-    if constexpr (PIPED) {
-        arrive<S, LPS>();
-        f.first(fp, fq, sp, sq, lds);
-    }
+    wait_loads<0>();                                   // the first chunk, and (all of) the first stages
+    block_barrier();
+    if constexpr (PIPED) f.first(fp, fq, lds);
+    int before = kChunk;                               // steps of the chunk before
 #pragma unroll 1
-    for (int t = start; t < tiles; t += G) {
-        const Tile ti = locate(t);
+    for (int t = walk.start; t < walk.tiles; t += walk.G) {
+        const Tile ti = tile_of(t);
         const int rows = ti.rows - wp * C::MP * 16;    // of this wave
         v4f acc[C::MP][C::MQ];
 #pragma unroll
         for (int m = 0; m < C::MP; m++)
 #pragma unroll
             for (int n = 0; n < C::MQ; n++) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        int kt = ti.expert * kStagger % steps;
+        int c = first_chunk(ti.expert);
 #pragma unroll 1
-        for (int i = 0; i < steps; i++) {
-            const uint32_t at = lds + stage * C::STAGE;
-            stage = stage + 1 == S ? 0 : stage + 1;
-            const uint32_t mask = BUF ? 0xFFFFu : scale_mask(blocks - kt * kRowScales, lane);
-            if constexpr (PIPED) {
-                step_pipelined<C, !BUF>(acc, f, fp, fq, sp, sq, at, lds + stage * C::STAGE, mask, part);
-                advance();
-            } else {
-                arrive<S, LPS>();
-                produce();                             // into the stage that the step before this one read
-                step_plain<C, !BUF>(acc, fp, fq, sp, sq, at, mask);
+        for (int i = 0; i < chunks; i++) {
+            // The chunk's scales to registers.  It was requested in the second step of the chunk before, ahead of that step's
+            // codes: behind a whole chunk the waits for the steps since cover it.  (!PIPED: the workgroup meets at the
+            // start of a step, so the meeting that publishes it is here.)
+            if (before == 1) {
+                block_barrier();                       // everyone has read the one before
+                request_scales();
             }
-            kt = kt + 1 == steps ? 0 : kt + 1;
+            if (before < kChunk) {
+                wait_loads<0>();
+                block_barrier();
+            } else if constexpr (!PIPED) {
+                arrive<S, LPS>();
+            }
+            sp.read(sp_at, lane);
+            sq.read(sq_at, lane);
+            const int n_steps = min(kChunk, steps - c * kChunk);
+#pragma unroll 1
+            for (int u = 0; u < n_steps; u++) {
+                const uint32_t at = lds + stage * C::CODES;
+                stage = stage + 1 == S ? 0 : stage + 1;
+                const uint32_t mask = BUF ? 0u : scale_mask(blocks - (c * kChunk + u) * kRowScales, lane);
+                sp.template step<!BUF>(u, mask);
+                sq.template step<!BUF>(u, mask);
+                if constexpr (PIPED) {
+                    if (u == 1) request_scales();
+                    step_pipelined<C>(acc, f, fp, fq, sp, sq, at, lds + stage * C::CODES, part);
+                    advance();
+                } else {
+                    if (u > 0) arrive<S, LPS>();
+                    if (u == 1) request_scales();
+                    produce();                         // into the stage that the step before this one read
+                    step_plain<C>(acc, fp, fq, sp, sq, at);
+                }
+            }
+            before = n_steps;
+            c = c + 1 == chunks ? 0 : c + 1;
         }
         const int64_t c0 = ti.n0 + wq * (COLS / C::WQ);
         const int cols = (int)min(g.N - c0, (int64_t)(COLS / C::WQ));
         const int64_t r0 = ti.row0 + wp * C::MP * 16;
         if (rows > 0 && cols > 0) {
-            if constexpr (FUSED) store_act_of(g, acc, r0, rows, c0, fresh(lane));
+            if constexpr (FUSED) store_act_of(g, acc, 0, r0, rows, c0, fresh(lane));
             else b16::store_wave_dt(g.out, g.out_dt, false, r0 * g.out_stride + c0, g.out_stride, rows, cols, acc, fresh(lane));
         }
     }

@@ -27,9 +27,17 @@ using b16::lds_offset;
 using b16::pieces;
 using b16::wait_loads;
 
+using b16::kMaxExperts;
+using b16::kMaxWidth;
+using b16::kPanel;
+using b16::kXcds;
+
+constexpr int kStagger = 5;                   // an expert's tiles walk k in rotation from step kStagger * e (b16_gemm.hip)
+
 constexpr int kStepK = 256;                   // k per ring stage
 constexpr int kRowBytes = kStepK / 2;
 constexpr int kRowScales = kStepK / kGroup;
+constexpr int kChunk = 4;                     // steps whose scales are loaded at once
 
 // BP x BQ tile, WP x WQ waves, S ring stages, WGS workgroups resident on a CU.
 template <int BP_, int BQ_, int WP_, int WQ_, int S_, int WGS_>
@@ -39,19 +47,19 @@ struct Cfg {
     static constexpr int MP = BP / 16 / WP, MQ = BQ / 16 / WQ;
     static constexpr int WAVES_PER_EU = NW * WGS_ / 4 > 0 ? NW * WGS_ / 4 : 1;
     static constexpr int CODES = (BP + BQ) * kRowBytes;
-    static constexpr int STAGE = CODES + (BP + BQ) * kRowScales;
+    static constexpr int CHUNK = (BP + BQ) * kChunk * kRowScales;            // bytes of a chunk of scales
     static constexpr int P_LOADS = BP / 8 / NW, Q_LOADS = BQ / 8 / NW;       // 16-byte DMAs of a wave and step
-    static constexpr int S_GROUPS = (BP + BQ) / 32;                          // 4-byte DMAs of a step, 32 rows each
-    static constexpr int S_LOADS = (S_GROUPS + NW - 1) / NW;                 // of a wave (some twice, the same words)
-    static constexpr int LOADS = P_LOADS + Q_LOADS + S_LOADS;
+    static constexpr int LOADS = P_LOADS + Q_LOADS;
+    static constexpr int S_LOADS = (BP + BQ) / 8 / NW;                       // 4-byte DMAs of a wave and chunk, eight rows each
     static constexpr int PER = (LOADS + 2 * MP - 3) / (2 * MP - 2) > 1 ? 2 : 1;   // loads of a group of the pipelined step
     static_assert(NW % 2 == 0 && BP % 32 == 0 && BQ % 32 == 0 && (BP / 8) % NW == 0 && (BQ / 8) % NW == 0, "waves cover the rows evenly");
 };
 
-// Piece c (16 bytes, one block of 32) of tile row r lies in slot slot_of(c) ^ ((r >> 1) & 7) of the row's eight: the lanes
-// that one LDS cycle serves (eight rows of one quarter of the wave, eight other rows of the next) fall into different banks.
-__device__ __forceinline__ int slot_of(int c) { return (c >> 1) | ((c & 1) << 2); }
-__device__ __forceinline__ int piece_in(int slot) { return ((slot & 3) << 1) | (slot >> 2); }
+// Piece c (16 bytes, one block of 32) of tile row r lies in slot slot_of(c) ^ ((r >> 1) & 7) of the row's eight.  The slots
+// of four lanes next to each other then hold one 64-byte half of the row's line (spread over both halves, the loads take the
+// CU's address path twice as long), and the lanes that one LDS cycle serves (eight rows of one quarter of the wave, eight
+// others of the next, pieces two apart) fall into different banks.
+__device__ __forceinline__ int slot_of(int c) { return (c & 4) | ((c & 1) << 1) | ((c >> 1) & 1); }   // its own inverse
 
 // The loads into LDS, 64 lanes of 16 or 4 bytes in lane order, written in asm as b16::dma16 is: the compiler would wait for
 // all of them before any LDS read.
@@ -77,26 +85,48 @@ __device__ __forceinline__ void buf4(uint32_t off, const v4i& buf, uint32_t at, 
 // lane's slot holds is the same for every j, since NW is even.
 template <int NW>
 __device__ __forceinline__ int code_row(int j, int wave, int lane) { return (j * NW + wave) * 8 + lane / 8; }
-__device__ __forceinline__ int code_byte(int wave, int lane) { return 16 * piece_in((lane % 8) ^ ((wave * 4 + lane / 16) & 7)); }
+__device__ __forceinline__ int code_byte(int wave, int lane) { return 16 * slot_of((lane % 8) ^ ((wave * 4 + lane / 16) & 7)); }
 
 // This lane's fragment addresses in a stage: sub-tile m of 16 rows from row 16 * sub0; MFMA ks takes piece 2q + ks.
 struct CodeFrag {
     uint32_t a;
     __device__ __forceinline__ void set(int sub0, int lane) {
         const int r = lane & 15, q = lane >> 4;
-        a = (uint32_t)(sub0 * 2048 + r * 128 + ((q ^ (r >> 1)) << 4));
+        a = (uint32_t)(sub0 * 2048 + r * 128 + ((slot_of(2 * q) ^ (r >> 1)) << 4));
     }
     __device__ __forceinline__ v4i read(uint32_t part, int m, int ks) const {
-        return *(const MOE_LDS v4i*)(uintptr_t)(part + (a ^ (ks << 6)) + m * 2048);
+        return *(const MOE_LDS v4i*)(uintptr_t)(part + (a ^ (ks << 5)) + m * 2048);
     }
 };
 
-// The scales of blocks 2q and 2q + 1 of sub-tile m's row, in the low 16 bits.
-struct ScaleFrag {
-    uint32_t a;
-    __device__ __forceinline__ void set(int sub0, int lane) { a = (uint32_t)(sub0 * 128 + (lane & 15) * 8 + (lane >> 4) * 2); }
-    __device__ __forceinline__ uint32_t read(uint32_t part, int m) const {
-        return *(const MOE_LDS uint16_t*)(uintptr_t)(part + a + m * 128);
+// Byte of a chunk at which this lane's words of 16-row sub-tile sub0 lie: four steps' words of its row and half.
+__device__ __forceinline__ uint32_t scale_lane(int sub0, int lane) {
+    return (uint32_t)((sub0 * 16 + (lane & 15)) * (kChunk * kRowScales) + (lane >> 5) * (kChunk * 4));
+}
+
+// The scales of M sub-tiles' rows: of a chunk, two steps a word (the lane's pairs, of blocks 2q and 2q + 1), and of the step in
+// the low half of `now`.
+template <int M>
+struct Scales {
+    uint32_t first[M], second[M], now[M];                   // steps 0 and 1, steps 2 and 3
+    __device__ __forceinline__ void read(uint32_t at, int lane) {
+        const uint32_t sel = (lane >> 4) & 1 ? 0x07060302u : 0x05040100u;      // the quarter's half of either word
+#pragma unroll
+        for (int m = 0; m < M; m++) {
+            const v4i w = *(const MOE_LDS v4i*)(uintptr_t)(at + m * 16 * kChunk * kRowScales);
+            first[m] = __builtin_amdgcn_perm((uint32_t)w[1], (uint32_t)w[0], sel);
+            second[m] = __builtin_amdgcn_perm((uint32_t)w[3], (uint32_t)w[2], sel);
+        }
+    }
+    template <bool MASKED>
+    __device__ __forceinline__ void step(int u, uint32_t mask) {
+        const int shift = (u & 1) * 16;
+        const uint32_t late = u & 2 ? ~0u : 0u;        // (by bits: a choice between the arrays would put them into memory)
+#pragma unroll
+        for (int m = 0; m < M; m++) {
+            now[m] = ((second[m] & late) | (first[m] & ~late)) >> shift;
+            if constexpr (MASKED) now[m] &= mask;
+        }
     }
 };
 
@@ -112,69 +142,51 @@ __device__ __forceinline__ v4f mfma(const v4i& a, uint32_t sa, const v4i& b, uin
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, KS, (int)sa, KS, (int)sb);
 }
 
-// The parts of a stage.
-template <class C>
-struct StageParts {
-    uint32_t p, q, sp, sq;
-    __device__ __forceinline__ explicit StageParts(uint32_t at)
-        : p(at), q(at + C::BP * kRowBytes), sp(at + C::CODES), sq(at + C::CODES + C::BP * kRowScales) {}
-};
-
 // One step of a wave's MP x MQ sub-tiles.  Q is the MFMA's row operand, so lane l holds of sub-tile (m, n) the element
 // p = 16m + l % 16, q = 16n + 4 (l / 16) + 0..3.
-template <class C, bool MASKED>
-__device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeFrag& fp, const CodeFrag& fq, const ScaleFrag& sp,
-                                           const ScaleFrag& sq, uint32_t at, uint32_t mask) {
-    const StageParts<C> st(at);
-    uint32_t qs[C::MQ], ps[C::MP];
-#pragma unroll
-    for (int n = 0; n < C::MQ; n++) qs[n] = sq.read(st.sq, n) & (MASKED ? mask : 0xFFFFu);
-#pragma unroll
-    for (int m = 0; m < C::MP; m++) ps[m] = sp.read(st.sp, m) & (MASKED ? mask : 0xFFFFu);
+template <class C>
+__device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeFrag& fp, const CodeFrag& fq, const Scales<C::MP>& sp,
+                                           const Scales<C::MQ>& sq, uint32_t at) {
+    const uint32_t at_q = at + C::BP * kRowBytes;
 #pragma unroll
     for (int ks = 0; ks < 2; ks++) {
         v4i q[C::MQ];
 #pragma unroll
-        for (int n = 0; n < C::MQ; n++) q[n] = fq.read(st.q, n, ks);
+        for (int n = 0; n < C::MQ; n++) q[n] = fq.read(at_q, n, ks);
 #pragma unroll
         for (int m = 0; m < C::MP; m++) {
-            const v4i p = fp.read(st.p, m, ks);
+            const v4i p = fp.read(at, m, ks);
 #pragma unroll
             for (int n = 0; n < C::MQ; n++)
-                acc[m][n] = ks == 0 ? mfma<0>(q[n], qs[n], p, ps[m], acc[m][n]) : mfma<1>(q[n], qs[n], p, ps[m], acc[m][n]);
+                acc[m][n] = ks == 0 ? mfma<0>(q[n], sq.now[n], p, sp.now[m], acc[m][n]) : mfma<1>(q[n], sq.now[n], p, sp.now[m], acc[m][n]);
         }
     }
 }
 
 // The same step as a software pipeline (b16::step_pipelined), for tiles whose MFMAs are the bound: 2 MP groups of MQ MFMAs,
-// each group's P fragment and scales read while the group before it is multiplied; the workgroup meets before the last
-// group, which covers the first reads of the next stage; the loads of the stage that takes the last one's place are spread
-// over the first groups, PER each.  No branch lies within a step (the producer moves on between steps) and the accumulators are
-// named at its end: the compiler would sink the MFMAs past a branch, and the loads before it would go out all at once.
+// each group's P fragment read while the group before it is multiplied; the workgroup meets before the last group, which
+// covers the first reads of the next stage; the loads of the stage that takes the last one's place are spread over the first
+// groups, PER each.  No branch lies within a step (the producer moves on between steps) and the accumulators are named at its
+// end: the compiler would sink the MFMAs past a branch, and the loads before it would go out all at once.
 template <class C>
 struct Frags {
     v4i p[2], q[2][C::MQ];
-    uint32_t ps[C::MP], qs[C::MQ], qn[C::MQ];          // scales; qn: the next stage's
-    __device__ __forceinline__ void first(const CodeFrag& fp, const CodeFrag& fq, const ScaleFrag& sp, const ScaleFrag& sq, uint32_t at) {
-        const StageParts<C> st(at);
+    __device__ __forceinline__ void first(const CodeFrag& fp, const CodeFrag& fq, uint32_t at) {
 #pragma unroll
-        for (int n = 0; n < C::MQ; n++) q[0][n] = fq.read(st.q, n, 0);
-        p[0] = fp.read(st.p, 0, 0);
-#pragma unroll
-        for (int n = 0; n < C::MQ; n++) qn[n] = sq.read(st.sq, n);
-        ps[0] = sp.read(st.sp, 0);
+        for (int n = 0; n < C::MQ; n++) q[0][n] = fq.read(at + C::BP * kRowBytes, n, 0);
+        p[0] = fp.read(at, 0, 0);
     }
 };
 
-template <class C, bool MASKED, class Part>
+template <class C, class Part>
 __device__ __forceinline__ void step_pipelined(v4f (&acc)[C::MP][C::MQ], Frags<C>& f, const CodeFrag& fp, const CodeFrag& fq,
-                                               const ScaleFrag& sp, const ScaleFrag& sq, uint32_t at, uint32_t next, uint32_t mask,
+                                               const Scales<C::MP>& sp, const Scales<C::MQ>& sq, uint32_t at, uint32_t next,
                                                const Part& part) {
     constexpr int MP = C::MP, MQ = C::MQ, G = 2 * MP, PARTS = C::LOADS, PER = C::PER;
     static_assert((G - 2) * PER >= PARTS, "all loads of a step go out before the workgroup meets");
     constexpr int Q1 = MP > MQ ? MP - 1 - MQ : 0;         // from this group on, one fragment of Q's second half each
     static_assert(MP >= 4 && MP >= MQ, "Q's second half is read before its first group");
-    const StageParts<C> st(at);
+    const uint32_t at_q = at + C::BP * kRowBytes;
 #pragma unroll
     for (int i = 0; i < G; i++) {
         const int m = i % MP, ks = i / MP;
@@ -187,25 +199,17 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[C::MP][C::MQ], Frags<C
             const int j = i * PER + u;
             if (j < PARTS) part(j);
         }
-        if (ks == 0) {
-            if (m == 0) {
-#pragma unroll
-                for (int n = 0; n < MQ; n++) f.qs[n] = MASKED ? f.qn[n] & mask : f.qn[n];
-            }
-            if constexpr (MASKED) f.ps[m] &= mask;
-        }
         if (i < G - 1) {
-            if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(st.q, i - Q1, 1);
-            f.p[(i + 1) % 2] = fp.read(st.p, (i + 1) % MP, (i + 1) / MP);
-            if (i + 1 < MP) f.ps[i + 1] = sp.read(st.sp, i + 1);
+            if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(at_q, i - Q1, 1);
+            f.p[(i + 1) % 2] = fp.read(at, (i + 1) % MP, (i + 1) / MP);
         } else {
-            f.first(fp, fq, sp, sq, next);
+            f.first(fp, fq, next);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < MQ; n++)
-            acc[m][n] = ks == 0 ? mfma<0>(f.q[0][n], f.qs[n], f.p[i % 2], f.ps[m], acc[m][n])
-                                : mfma<1>(f.q[1][n], f.qs[n], f.p[i % 2], f.ps[m], acc[m][n]);
+            acc[m][n] = ks == 0 ? mfma<0>(f.q[0][n], sq.now[n], f.p[i % 2], sp.now[m], acc[m][n])
+                                : mfma<1>(f.q[1][n], sq.now[n], f.p[i % 2], sp.now[m], acc[m][n]);
         __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -213,6 +217,158 @@ __device__ __forceinline__ void step_pipelined(v4f (&acc)[C::MP][C::MQ], Frags<C
 #pragma unroll
         for (int n = 0; n < MQ; n++) asm volatile("" : "+v"(acc[m][n]));
 }
+
+struct GemmArgs {
+    const char* a;
+    int64_t a_stride;                         // bytes, as all strides of codes and scales
+    const char* a_s;
+    int64_t a_s_stride;
+    int64_t a_n;                              // rows of a, for the map's bounds
+    const int32_t* a_rows;
+    const char* w;
+    int64_t w_stride_e, w_stride_n;
+    const char* w_s;
+    int64_t w_s_stride_e, w_s_stride_n;
+    int n_experts;
+    int64_t N, K;                             // fused: N = I, the act columns
+    const int32_t* offsets;
+    int m_rows;
+    int n_tiles;
+    void* out;                                // fused: codes
+    int out_dt;
+    int64_t out_stride;                       // elements (fused: bytes)
+    uint8_t* s;                               // fused: scale bytes
+    int64_t s_stride;
+    int act, ceil;
+};
+
+__device__ __forceinline__ uint32_t max_lanes16_32(uint32_t v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = a[0] > a[1] ? a[0] : a[1];
+    const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return b[0] > b[1] ? b[0] : b[1];
+}
+
+// The fused epilogue of four of a wave's sub-tiles (two of gate, two of up, from n0 on): rows row0 + 16m + lane % 16 (below `rows`), act columns col0 .. col0 + 31 (below `cols`).
+template <int ACT, int MP, int MQ>
+__device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP][MQ], int n0, int64_t row0, int rows, int64_t col0, int lane) {
+    const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < MP; m++) {
+        if (m * 16 >= rows) break;                                          // wave-uniform
+        float h[8];
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) h[4 * n + i] = gated<ACT>(acc[m][n0 + n][i], acc[m][n0 + n + 2][i]);
+        const uint32_t byte = scale_byte(max_lanes16_32(max_bits8(h)), g.ceil != 0);
+        const uint32_t codes = encode8(h, byte);
+        if (m * 16 + r < rows) {
+            const int64_t row = row0 + m * 16 + r;
+            uint8_t* out = (uint8_t*)g.out + row * g.out_stride + col0 / 2 + 2 * q;
+            *reinterpret_cast<uint16_t*>(out) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t*>(out + 8) = (uint16_t)(codes >> 16);
+            if (q == 0) g.s[row * g.s_stride + col0 / kGroup] = (uint8_t)byte;
+        }
+    }
+}
+
+template <int MP, int MQ>
+__device__ __forceinline__ void store_act_of(const GemmArgs& g, const v4f (&acc)[MP][MQ], int n0, int64_t row0, int rows, int64_t col0, int lane) {
+    switch (g.act) {
+        case 1: return store_act<1>(g, acc, n0, row0, rows, col0, lane);
+        case 2: return store_act<2>(g, acc, n0, row0, rows, col0, lane);
+        case 3: return store_act<3>(g, acc, n0, row0, rows, col0, lane);
+        case 4: return store_act<4>(g, acc, n0, row0, rows, col0, lane);
+        default: return store_act<5>(g, acc, n0, row0, rows, col0, lane);
+    }
+}
+
+// A tile: rows row0 .. row0 + rows - 1 of an expert, output columns from n0.
+struct Tile {
+    int expert, row0, rows, n0;
+};
+
+// The tiles of a launch, COLS output columns each: numbered in panels of kPanel M tiles, M fastest, and dealt so that the
+// workgroups of an XCD stand next to each other (b16_gemm.hip).  Built by the whole workgroup from the device's offsets, with 2 NW + 2 words of scratch LDS.
+template <class C, int COLS>
+struct Walk {
+    const GemmArgs& g;
+    const int* first_tile;                    // LDS: M tiles before expert e
+    int m_tiles, tiles, G, start;
+
+    __device__ __forceinline__ int clamped(int e) const { return min(max(g.offsets[e], 0), g.m_rows); }
+
+    __device__ __forceinline__ Walk(const GemmArgs& args, int* table, uint32_t* scratch, int tid, int lane, int wave)
+        : g(args), first_tile(table) {
+        constexpr int EPT = kMaxExperts / C::THREADS;  // consecutive experts of a thread
+        const int E = g.n_experts;
+        uint32_t count[EPT], mine = 0, down = 0;
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            count[i] = 0;
+            if (e < E) {
+                const int lo = clamped(e), to = clamped(e + 1);
+                count[i] = (uint32_t)pieces(max(to, lo) - lo, C::BP);
+                down += to < lo;
+            }
+            mine += count[i];
+        }
+        uint32_t w = mine, d = down;
+        b16::block_exclusive_scan2<C::NW>(w, d, scratch, lane, wave);
+#pragma unroll
+        for (int i = 0; i < EPT; i++) {
+            const int e = tid * EPT + i;
+            if (e < E) table[e] = (int)w;
+            w += count[i];
+        }
+        if (tid == C::THREADS - 1) {
+            scratch[2 * C::NW] = w;
+            scratch[2 * C::NW + 1] = d + down;
+        }
+        __syncthreads();
+        m_tiles = __builtin_amdgcn_readfirstlane((int)scratch[2 * C::NW]);
+        // Experts that overlap may have more tiles than the host counted on, and share rows: nothing is computed.
+        tiles = __builtin_amdgcn_readfirstlane((int)scratch[2 * C::NW + 1]) != 0 ? 0 : m_tiles * g.n_tiles;
+        block_barrier();                       // the scratch words are free
+        G = gridDim.x;
+        start = (int)(blockIdx.x % kXcds) * (G / kXcds) + (int)(blockIdx.x / kXcds);
+    }
+
+    __device__ __forceinline__ Tile locate(int t, int lane) const {
+        const int per = kPanel * g.n_tiles;
+        const int panel = t / per, r = t - panel * per;
+        const int height = min(kPanel, m_tiles - panel * kPanel);
+        const int nt = r / height, mt = panel * kPanel + r - nt * height;
+        const int e = last_at_most([&](int i) { return first_tile[i]; }, g.n_experts, mt, lane);
+        Tile ti;
+        ti.expert = e;
+        uint32_t lo, hi;                       // (a vector load would wait for every load in flight)
+        scalar_read2(g.offsets + e, g.offsets + e + 1, lo, hi);
+        const int from = min(max((int)lo, 0), g.m_rows), end = min(max((int)hi, 0), g.m_rows);
+        ti.row0 = from + (mt - __builtin_amdgcn_readfirstlane(first_tile[e])) * C::BP;
+        ti.rows = min(end - ti.row0, C::BP);
+        ti.n0 = nt * COLS;
+        return ti;
+    }
+    // A's row of row r of a tile: rows past the tile's repeat the last one (their results are dropped); -1: a row of zeros,
+    // whose map entry is no row of A.
+    __device__ __forceinline__ int64_t a_row(const Tile& ti, int r) const {
+        const int64_t at = ti.row0 + min(r, ti.rows - 1);
+        if (!g.a_rows) return at;
+        const int64_t m = g.a_rows[at];
+        return m >= 0 && m < g.a_n ? m : -1;
+    }
+    // The bank's row of row r of a tile.  Fused: 32 gate rows, then the 32 up rows of the same columns, and so on.  Columns past
+    // the last repeat it.
+    template <bool FUSED>
+    __device__ __forceinline__ int64_t w_row(const Tile& ti, int r) const {
+        if (!FUSED) return min(ti.n0 + r, (int)g.N - 1);
+        const int c = min(ti.n0 + (r >> 6) * 32 + (r & 31), (int)g.N - 1);
+        return c + (r & 32 ? g.N : 0);
+    }
+};
 
 }  // namespace mx4
 }  // namespace moe
