@@ -6,17 +6,25 @@
 // route maps of route_prep.hip over the routes there are.
 //
 // MI355X design.
-//  * Choices are ranked as 64-bit keys: the order-preserving bits of the value above the inverted expert index, so one
-//    unsigned compare is "larger value, ties to the lower index".  Without a bias the order is the logits' own, which needs
-//    no exponential and is exact.  With one (or with group values that are sums) the scores are formed in 64 bits: in 32
-//    bits about one token in ten thousand has two choices next to each other that round to the wrong order.
+//  * What is ranked: the choice's order-preserving bits above the inverted expert index, so one unsigned compare is "larger
+//    value, ties to the lower index".  Without a bias the order is the logits' own, which needs no exponential.  With one (or
+//    with group values that are sums) scores have to be formed in 64 bits, for in 32 about one token in ten thousand has two
+//    choices next to each other that round to the wrong order; but 64-bit exponentials and 64-bit keys for every expert took
+//    86 us where this takes 52 (16384 tokens, 512 experts).  So keys are 32 bits: 22-bit steps over the token's own range, formed
+//    with 32-bit scores whose error is known in steps.  Where two keys that matter are closer than that, the candidates alone
+//    are ranked again in 64 bits (refine, one token in a hundred), and where groups are, all of the token (rank_exact).  16-bit
+//    logits fit a key as they are.
 //  * Up to 64 experts a token takes 16 lanes of a wave, beyond a whole wave; lanes hold experts lane, lane + LPT, ... .
-//    Round j takes the largest key below round j - 1's winner by DPP moves.
-//  * A workgroup takes 16 tokens at a time and sets one bit per (expert, token) in LDS, whose counts are the chunk's loads.
-//    Up to 64 tokens one workgroup does everything, maps included, in one launch.  Beyond, a second launch scatters: each of
-//    its workgroups adds up the counts of all chunks (bytes) for the experts' offsets and of the chunks before its own
-//    for its rows.  With more than kSumChunks chunks those sums come from a scan launched between.
+//    Every round's largest key is found by lane moves folded into the maximum, then struck out.
+//  * A workgroup takes 16 tokens at a time and counts its routes in LDS, the chunk's loads.  Up to 64 tokens one workgroup
+//    does everything, maps included, in one launch.  Beyond, a second launch scatters: each of its workgroups adds up the
+//    counts of all chunks (bytes) for the experts' offsets and of the chunks before its own for its rows.  With more than
+//    kSumChunks chunks those sums come from a scan launched between.
+//  * Bound by instruction issue and the latency of the rounds, not by bytes: 4096 tokens of 256 fp32 logits in 8 groups with
+//    maps take 20.6 us in two launches (780 vector instructions a token), 16384 of 512 bf16 ones with their scores 51.8 us in
+//    three (50 MB: 1 TB/s), eight of 64 experts 7.6 us, which is the call.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "host.h"
@@ -31,7 +39,7 @@ constexpr int kMaxGroups = 64;
 constexpr int kTok = 16;                        // tokens of a workgroup at one time
 constexpr int kSingle = 64;                     // tokens that one workgroup routes alone
 constexpr int kSumChunks = 512;                 // chunks whose counts every scattering workgroup adds up itself
-constexpr int kScatterThreads = 512;
+constexpr int kScatterThreads = 1024;
 constexpr int64_t kMaxT = 1 << 27;              // a chunk of 64 tokens is 1024 threads of a grid, which fit 32 bits
 
 struct Args {
@@ -59,19 +67,22 @@ __host__ __device__ inline int row_bytes(int E) { return (E + 15) / 16 * 16; }
 // A logit as the formulas take it: NaN masks as -inf does, +inf is the largest value.
 __device__ __forceinline__ float shown(float v) { return v != v ? -__builtin_inff() : __builtin_fminf(v, 3.402823466e38f); }
 
-__device__ __forceinline__ float load_logit(const Args& a, int64_t i) {
-    if (a.dt == MOE_F32) return shown(load_as_f32<kF32>(a.logits, i));
-    return shown(a.dt == MOE_BF16 ? load_as_f32<kBF16>(a.logits, i) : load_as_f32<kF16>(a.logits, i));
+// Logits i * LPT + l of a row as they are; past the last expert the row's last one.
+template <int LPT, int VPL>
+__device__ __forceinline__ void load_row(const Args& a, int t, int l, float (&v)[VPL]) {
+    const int64_t row = (int64_t)t * a.stride;
+    auto as = [&](auto type) {
+#pragma unroll
+        for (int i = 0; i < VPL; i++) v[i] = load_as_f32<decltype(type)::value>(a.logits, row + min(i * LPT + l, a.E - 1));
+    };
+    if (a.dt == MOE_F32) as(std::integral_constant<int, kF32>{});
+    else if (a.dt == MOE_BF16) as(std::integral_constant<int, kBF16>{});
+    else as(std::integral_constant<int, kF16>{});
 }
 
-// Logits i * LPT + l of a row, -inf past the last expert (the row's last one is read there).
-template <int DT, int LPT, int VPL>
-__device__ __forceinline__ void load_row(const Args& a, int64_t row, int l, float (&v)[VPL]) {
-    float x[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; i++) x[i] = load_as_f32<DT>(a.logits, row + min(i * LPT + l, a.E - 1));
-#pragma unroll
-    for (int i = 0; i < VPL; i++) v[i] = i * LPT + l < a.E ? shown(x[i]) : -__builtin_inff();
+__device__ __forceinline__ float load_logit(const Args& a, int64_t i) {
+    if (a.dt == MOE_F32) return load_as_f32<kF32>(a.logits, i);
+    return a.dt == MOE_BF16 ? load_as_f32<kBF16>(a.logits, i) : load_as_f32<kF16>(a.logits, i);
 }
 
 // Order-preserving maps to unsigned, larger value -> larger code; -0 as +0.
@@ -79,6 +90,7 @@ __device__ __forceinline__ uint32_t mono32(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float from_mono32(uint32_t u) { return __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u); }
 __device__ __forceinline__ uint64_t mono64(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -90,222 +102,500 @@ __device__ __forceinline__ uint64_t value_key(double c, int i) { return ((mono64
 __device__ __forceinline__ uint64_t logit_key(float v, int e) { return ((uint64_t)mono32(v) << 32) | (kLow - (uint64_t)e); }
 __device__ __forceinline__ int key_index(uint64_t key) { return (int)(kLow - (key & kLow)); }
 
+// Lane moves; a lane that a move leaves out (ROW_MASK) keeps `old`.  (Told that nothing is out of bounds, the compiler folds a
+// move into the operation that uses it.)
 template <int CTRL, int ROW_MASK = 0xF>
 __device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, CTRL, ROW_MASK, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, CTRL, ROW_MASK, 0xF, ROW_MASK == 0xF);
 }
-template <int CTRL, int ROW_MASK = 0xF>
-__device__ __forceinline__ uint64_t max_step(uint64_t k) {
-    const uint64_t o = ((uint64_t)dpp<CTRL, ROW_MASK>((uint32_t)(k >> 32), (uint32_t)(k >> 32)) << 32) |
-                       dpp<CTRL, ROW_MASK>((uint32_t)k, (uint32_t)k);
-    return o > k ? o : k;
-}
-// The largest key over the LPT lanes of a token, in every one of them.
-template <int LPT>
-__device__ __forceinline__ uint64_t token_max(uint64_t k) {
-    k = max_step<0xB1>(k);                      // quad_perm [1,0,3,2], [2,3,0,1], half-mirror, mirror: a row of 16
-    k = max_step<0x4E>(k);
-    k = max_step<0x141>(k);
-    k = max_step<0x140>(k);
+// f over the LPT lanes of a token, f commutative with the neutral word `none`; in every one of them.
+template <int LPT, class F>
+__device__ __forceinline__ uint32_t token_reduce(uint32_t x, uint32_t none, const F& f) {
+    x = f(x, dpp<0xB1>(none, x));               // quad_perm [1,0,3,2], [2,3,0,1], half-mirror, mirror: a row of 16
+    x = f(x, dpp<0x4E>(none, x));
+    x = f(x, dpp<0x141>(none, x));
+    x = f(x, dpp<0x140>(none, x));
     if constexpr (LPT == 64) {
-        k = max_step<0x142, 0xA>(k);            // row_bcast:15, row_bcast:31: the wave's in lane 63
-        k = max_step<0x143, 0xC>(k);
-        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), 63);
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, 63);
-        k = ((uint64_t)hi << 32) | lo;
+        x = f(x, dpp<0x142, 0xA>(none, x));     // row_bcast:15, row_bcast:31: the wave's in lane 63
+        x = f(x, dpp<0x143, 0xC>(none, x));
+        x = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
     }
-    return k;
-}
-template <int LPT, class T>
-__device__ __forceinline__ T token_sum(T x) {
-#pragma unroll
-    for (int m = 1; m < LPT; m <<= 1) x += __shfl_xor(x, m, kWave);
     return x;
 }
 template <int LPT>
-__device__ __forceinline__ float token_fmax(float x) {
-#pragma unroll
-    for (int m = 1; m < LPT; m <<= 1) x = __builtin_fmaxf(x, __shfl_xor(x, m, kWave));
-    return x;
+__device__ __forceinline__ uint32_t token_umax(uint32_t x) {
+    return token_reduce<LPT>(x, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
+template <int LPT>
+__device__ __forceinline__ float token_fmax(float x) { return from_mono32(token_umax<LPT>(mono32(x))); }
+template <int LPT>
+__device__ __forceinline__ float token_fsum(float x) {
+    return __uint_as_float(token_reduce<LPT>(__float_as_uint(x), 0u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+// The larger and the smaller of two numbers that are no NaN, in one instruction each.
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_amdgcn_fmed3f(x, y, __builtin_inff()); }
+__device__ __forceinline__ float smaller(float x, float y) { return __builtin_amdgcn_fmed3f(x, y, -__builtin_inff()); }
 
 __device__ __forceinline__ double sigmoid64(double l) {
     const double t = exp(-fabs(l)), r = 1.0 / (1.0 + t);
     return l >= 0.0 ? r : t * r;
+}
+// From the hardware exp2 and reciprocal, within an ulp each: e^x for x <= 0 is within (1.5 |x| + 2) 2^-24 of itself.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+__device__ __forceinline__ float fast_score(float l) {
+    const float t = fast_exp(-__builtin_fabsf(l)), r = __builtin_amdgcn_rcpf(1.0f + t);
+    return l >= 0.0f ? r : t * r;
 }
 __device__ __forceinline__ float sigmoid32(float l) {
     const float t = expf(-__builtin_fabsf(l)), r = 1.0f / (1.0f + t);
     return l >= 0.0f ? r : t * r;
 }
 
-// LDS of a token while it is routed.
-struct TokenLds {
-    uint64_t top1[kMaxGroups], top2[kMaxGroups];     // keys of each group's two largest choices
-    double val1[kMaxGroups], val2[kMaxGroups];       // and, for their sum, the choices
-    int32_t id[kMaxTopk];
+// e^(x - y) for x <= y, the difference as an exact sum of two floats, so that its rounding does not scale with it.
+__device__ __forceinline__ float exp_of_difference(float x, float y) {
+    const float d = x - y, yy = x - d, xx = d + yy;
+    const float rest = (x - xx) + (yy - y);
+    return expf(d) * (1.0f + rest);
+}
+
+// What a lane needs of its experts for every token: their biases and groups.
+template <int VPL>
+struct LaneExperts {
+    float bias[VPL];
+    int group[VPL];
 };
 
-// Routes token t with the LPT lanes of which this is `l`; ids go to lds.id and, with the weights, to memory.
-template <int LPT, int VPL, bool WIDE>
-__device__ __forceinline__ void route_token(const Args& a, int t, int l, TokenLds& lds) {
-    constexpr float kInf = __builtin_inff();
-    const int64_t row = (int64_t)t * a.stride;
+template <int LPT, int VPL>
+__device__ __forceinline__ LaneExperts<VPL> lane_experts(const Args& a, int l) {
+    LaneExperts<VPL> x;
+#pragma unroll
+    for (int i = 0; i < VPL; i++) x.bias[i] = a.bias ? a.bias[min(i * LPT + l, a.E - 1)] : 0.0f;
+    // (e + 1/2) / size is at least 1/2048 away from a whole number and below 64, 1 / size within 2^-22 of itself
+    const float per = __builtin_amdgcn_rcpf((float)(a.E / a.n_group));
+#pragma unroll
+    for (int i = 0; i < VPL; i++) x.group[i] = min((int)(((float)(i * LPT + l) + 0.5f) * per), kMaxGroups - 1);   // (past E: no key)
+    return x;
+}
+
+// The groups' largest and second choices while a token is ranked.
+struct GroupLds {
+    uint32_t top1[kMaxGroups], top2[kMaxGroups];
+};
+
+// What a token's scores are made of: its logits in this lane (-inf: masked), their largest, and the softmax's sum.
+template <int VPL>
+struct TokenScores {
     float v[VPL];
-    if (a.dt == MOE_F32) load_row<kF32, LPT>(a, row, l, v);
-    else if (a.dt == MOE_BF16) load_row<kBF16, LPT>(a, row, l, v);
-    else load_row<kF16, LPT>(a, row, l, v);
-    float top = v[0];
+    float top, z;
+};
+
+// ---------------------------------------------------------------- ranking in 32 bits
+// Values as 22-bit steps over the token's range, the index below: ranks are one unsigned compare and two values closer than
+// `near` steps may stand in the wrong order.  Where that is so the token is ranked again in 64 bits (rank_wide).
+struct Steps {
+    float lo, inv;
+    uint32_t near;
+    bool fine;
+};
+
+// lo is the smallest value (`all`: groups add values up, or few lanes), else the smallest of the lanes' largest: those below it,
+// cut to step 0, are hardly ever among the first.  A value x may be off by tol + 2^-23 |x|.
+template <int LPT, int VPL>
+__device__ __forceinline__ Steps steps_of(const float (&c)[VPL], bool all, float tol) {
+    constexpr float kInf = __builtin_inff();
+    float most = c[0], least = kInf;
 #pragma unroll
-    for (int i = 1; i < VPL; i++) top = __builtin_fmaxf(top, v[i]);
-    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-    double z64 = 0.0;
-    float z = 0.0f;
-    if (softmax) {
-        top = token_fmax<LPT>(top);
-        if constexpr (WIDE) {
+    for (int i = 1; i < VPL; i++) most = larger(most, c[i]);
+    if (all) {
 #pragma unroll
-            for (int i = 0; i < VPL; i++) z64 += v[i] > -kInf ? exp((double)v[i] - (double)top) : 0.0;
-            z64 = token_sum<LPT>(z64);
-            z = (float)z64;
-        } else if (a.scores || !a.renorm) {
-#pragma unroll
-            for (int i = 0; i < VPL; i++) z += v[i] > -kInf ? expf(v[i] - top) : 0.0f;
-            z = token_sum<LPT>(z);
-        }
+        for (int i = 0; i < VPL; i++) least = smaller(least, c[i] > -kInf ? c[i] : kInf);
+    } else {
+        least = most > -kInf ? most : kInf;
     }
-    if (a.scores) {
+    const float hi = token_fmax<LPT>(most);
+    Steps s;
+    s.lo = -token_fmax<LPT>(-least);
+    const float range = hi - s.lo;
+    s.inv = 4194301.0f * __builtin_amdgcn_rcpf(range);                 // (a step's width need not be exact)
+    s.fine = (range > 1e-30f && range < 1e30f) || hi == -kInf;         // no expert at all: nothing to rank
+    tol = 2.0f * (tol + 0x1p-23f * larger(__builtin_fabsf(hi), __builtin_fabsf(s.lo)));
+    s.near = hi > -kInf ? (uint32_t)smaller(tol * s.inv, 1e9f) + 3u : 0u;
+    return s;
+}
+__device__ __forceinline__ uint32_t step_key(const Steps& s, float c, int e) {
+    const float q = (c - s.lo) * s.inv;
+    return c > -__builtin_inff() ? (((uint32_t)larger(q, 0.0f) + 1u) << 10) | (1023u - (uint32_t)e) : 0u;
+}
+// A 16-bit logit's own order, exact: equal logits are true ties.
+__device__ __forceinline__ uint32_t half_key(float v, bool bf16, int e) {
+    uint32_t u;
+    if (bf16) u = __float_as_uint(v + 0.0f) >> 16;
+    else u = f32_to_f16(v + 0.0f);
+    u = u >> 15 ? 0xFFFFu & ~u : u | 0x8000u;
+    return v > -__builtin_inff() ? ((u + 1u) << 10) | (1023u - (uint32_t)e) : 0u;
+}
+
+// Ranks the token's experts by 32-bit keys: lane l gets the keys of ranks l, l + LPT, ... (0: none).  Of the n keys every other
+// expert is surely below; `close` if some of them may stand in the wrong order.  False if the groups, or more than 64 values,
+// are too near.
+template <int LPT, int VPL, bool WIDE>
+__device__ __forceinline__ bool rank_fast(const Args& a, const LaneExperts<VPL>& x, const TokenScores<VPL>& s, int l, GroupLds& lds,
+                                          uint32_t (&mine)[kMaxTopk / LPT], int& n, bool& close) {
+    constexpr float kInf = __builtin_inff();
+    const bool halves = a.dt != MOE_F32;
+    uint32_t key[VPL];
+    uint32_t near = 0u;
+    bool fine = true;
+    auto by_logit = [&]() {
+        if (halves) {
+#pragma unroll
+            for (int i = 0; i < VPL; i++) key[i] = half_key(s.v[i], a.dt == MOE_BF16, i * LPT + l);
+            near = 0u;
+        } else {
+            const Steps st = steps_of<LPT, VPL>(s.v, LPT == 16, 0.0f);
+#pragma unroll
+            for (int i = 0; i < VPL; i++) key[i] = step_key(st, s.v[i], i * LPT + l);
+            near = st.near;
+            fine = fine && st.fine;
+        }
+    };
+    if constexpr (WIDE) {
+        const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+        const float inv = softmax ? __builtin_amdgcn_rcpf(s.z) : 1.0f;
+        float c[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; i++) {
-            const int e = i * LPT + l;
-            const float s = v[i] > -kInf ? (softmax ? expf(v[i] - top) / z : sigmoid32(v[i])) : 0.0f;
-            if (e < a.E) a.scores[(int64_t)t * a.E + e] = s;
+            c[i] = (softmax ? fast_exp(s.v[i] - s.top) * inv : fast_score(s.v[i])) + x.bias[i];
+            c[i] = s.v[i] > -kInf && c[i] > -kInf ? c[i] : -kInf;
         }
-    }
-    uint64_t key[VPL];
-    double choice[WIDE ? VPL : 1];
+        // In units of 2^-24, with the hardware exp2 and reciprocal: a sigmoid is off by t (1.5 |x| + 2) / (1 + t)^2 < 1 for t, 1
+        // for 1 + t, 2 for its reciprocal, 1 for the product.  A softmax score is inv at most and off by inv times: e^-d (1.5 d +
+        // 2) < 3, 2 for the reciprocal, 1 for the product, and for the sum 1.5 ln E + 2 < 13 and 22 additions.  Then the bias's
+        // addition rounds.
+        const Steps st = steps_of<LPT, VPL>(c, a.n_group > 1 || LPT == 16, softmax ? 0x1p-18f * inv : 0x1p-21f);
 #pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = i * LPT + l;
-        if constexpr (WIDE) {
-            double c = softmax ? exp((double)v[i] - (double)top) / z64 : sigmoid64((double)v[i]);
-            if (a.bias) c += (double)a.bias[e < a.E ? e : a.E - 1];
-            const bool there = v[i] > -kInf && c > -(double)kInf;            // false for NaN too
-            key[i] = there ? value_key(c, e) : 0ull;
-            choice[i] = c;
-        } else {
-            key[i] = v[i] > -kInf ? logit_key(v[i], e) : 0ull;
-        }
+        for (int i = 0; i < VPL; i++) key[i] = step_key(st, c[i], i * LPT + l);
+        near = st.near;
+        fine = st.fine;
+    } else {
+        by_logit();
     }
-    if (a.n_group > 1) {                        // the best groups stay
+    if (a.n_group > 1) {
         const int size = a.E / a.n_group;
-        for (int g = l; g < a.n_group; g += LPT) lds.top1[g] = lds.top2[g] = 0ull;
+        uint32_t* top1 = lds.top1;
+        uint32_t* top2 = lds.top2;
+        for (int g = l; g < a.n_group; g += LPT) top1[g] = top2[g] = 0u;
         wave_lds_fence();
+        // groups of whole rows of 16 lanes: a row's largest by lane moves, then one lane of it goes to LDS
+        const bool rows = LPT == 64 && size % 16 == 0;
+        auto largest = [&](uint32_t* to, bool second) {
 #pragma unroll
-        for (int i = 0; i < VPL; i++)
-            if (key[i]) atomicMax((unsigned long long*)&lds.top1[(i * LPT + l) / size], (unsigned long long)key[i]);
-        wave_lds_fence();
-        if constexpr (WIDE) {
-            if (a.group_top == 2) {
-#pragma unroll
-                for (int i = 0; i < VPL; i++) {
-                    const int g = (i * LPT + l) / size;
-                    if (key[i] && key[i] == lds.top1[g]) lds.val1[g] = choice[i];
-                    else if (key[i]) atomicMax((unsigned long long*)&lds.top2[g], (unsigned long long)key[i]);
+            for (int i = 0; i < VPL; i++) {
+                const int g = x.group[i];
+                uint32_t k = key[i];
+                if (second) k = k == top1[g] ? 0u : k;
+                if (rows) {
+                    k = token_reduce<16>(k, 0u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+                    if ((l & 15) == 0 && k) atomicMax(&to[g], k);
+                } else if (k) {
+                    atomicMax(&to[g], k);
                 }
-                wave_lds_fence();
-#pragma unroll
-                for (int i = 0; i < VPL; i++) {
-                    const int g = (i * LPT + l) / size;
-                    if (key[i] && key[i] == lds.top2[g]) lds.val2[g] = choice[i];
-                }
-                wave_lds_fence();
             }
-        }
-        uint64_t gk[kMaxGroups / LPT];
+            wave_lds_fence();
+        };
+        largest(top1, false);
+        const bool two = WIDE && a.group_top == 2;
+        if (two) largest(top2, true);
+        uint32_t gk[kMaxGroups / LPT];
+        bool lone = false;
 #pragma unroll
         for (int j = 0; j < kMaxGroups / LPT; j++) {
             const int g = j * LPT + l;
-            gk[j] = 0ull;
-            if (g < a.n_group && lds.top1[g]) {
-                gk[j] = lds.top1[g];            // its index orders ties by group as well
-                if (WIDE && a.group_top == 2) gk[j] = value_key(lds.top2[g] ? lds.val1[g] + lds.val2[g] : lds.val1[g], g);
+            const uint32_t k1 = g < a.n_group ? top1[g] : 0u;
+            if (two) {
+                const uint32_t k2 = g < a.n_group ? top2[g] : 0u;
+                lone = lone || (k1 && !k2);                       // a group with one expert: its value is no sum
+                gk[j] = k1 ? (((k1 >> 10) + (k2 >> 10)) << 6) | (63u - (uint32_t)g) : 0u;
+            } else {
+                // (the group's index in the low six bits; its first expert's orders ties the same way)
+                gk[j] = k1 ? (k1 >> 10 << 6) | (63u - (uint32_t)g) : 0u;
             }
         }
-        uint64_t kept = 0ull, prev = ~0ull;
-        for (int n = 0; n < a.keep; n++) {
-            uint64_t best = 0ull;
+        fine = fine && !token_umax<LPT>(lone ? 1u : 0u);
+        uint64_t kept = 0ull;
+        uint32_t last = 0u;
+        for (int n = 0; n <= a.keep; n++) {
+            uint32_t best = 0u;
 #pragma unroll
-            for (int j = 0; j < kMaxGroups / LPT; j++) best = gk[j] < prev && gk[j] > best ? gk[j] : best;
-            best = token_max<LPT>(best);
-            if (best == 0ull) break;            // the same in the token's lanes; other tokens of the wave go on
-            prev = best;
-            kept |= 1ull << (WIDE && a.group_top == 2 ? key_index(best) : key_index(best) / size);
+            for (int j = 0; j < kMaxGroups / LPT; j++) best = gk[j] > best ? gk[j] : best;
+            best = token_umax<LPT>(best);
+            if (n == a.keep) {
+                if (near && best && last && (last >> 6) - (best >> 6) <= 2u * near) fine = false;
+            } else {
+                if (best) kept |= 1ull << (63u - (best & 63u));
+                last = best;
+#pragma unroll
+                for (int j = 0; j < kMaxGroups / LPT; j++) gk[j] = gk[j] == best ? 0u : gk[j];
+            }
+        }
+        if constexpr (WIDE) {
+            if (!a.bias) {                      // the groups went by scores, the order within them is the logits' own
+                uint32_t there = 0u;
+#pragma unroll
+                for (int i = 0; i < VPL; i++) there |= key[i] ? 1u << i : 0u;
+                by_logit();
+#pragma unroll
+                for (int i = 0; i < VPL; i++) key[i] = there >> i & 1u ? key[i] : 0u;
+            }
         }
 #pragma unroll
         for (int i = 0; i < VPL; i++)
-            if (!((kept >> ((i * LPT + l) / size & 63)) & 1ull)) key[i] = 0ull;
-        if constexpr (WIDE) {
-            if (!a.bias) {                      // the groups went by scores, the order within them is the logits' own
-#pragma unroll
-                for (int i = 0; i < VPL; i++) key[i] = key[i] ? logit_key(v[i], i * LPT + l) : 0ull;
-            }
-        }
+            if (!((kept >> x.group[i]) & 1ull)) key[i] = 0u;
         wave_lds_fence();
     }
-    uint64_t prev = ~0ull;
-    for (int j = 0; j < a.topk; j++) {
-        uint64_t f[VPL];                        // candidates of this round, then a depth-log2(VPL) max tree
 #pragma unroll
-        for (int i = 0; i < VPL; i++) f[i] = key[i] < prev ? key[i] : 0ull;
+    for (int q = 0; q < kMaxTopk / LPT; q++) mine[q] = 0u;
+    uint32_t last = 0u;
+    close = false;
+    for (n = 0; n < a.topk || near; n++) {
+        uint32_t best = key[0];
 #pragma unroll
-        for (int w = VPL / 2; w >= 1; w /= 2)
+        for (int i = 1; i < VPL; i++) best = key[i] > best ? key[i] : best;
+        best = token_umax<LPT>(best);
+        const bool same = near && best && last && (last >> 10) - (best >> 10) <= near;
+        if (n >= a.topk && !same) break;
+        if (n >= kMaxTopk) return false;
+        close = close || same;
+        last = best;
 #pragma unroll
-            for (int i = 0; i < w; i++) f[i] = f[i] > f[i + w] ? f[i] : f[i + w];
-        const uint64_t best = token_max<LPT>(f[0]);
-        prev = best ? best : 1ull;              // none left: every later round finds none
-        if (l == 0) lds.id[j] = best == 0ull ? -1 : key_index(best);
+        for (int i = 0; i < VPL; i++) key[i] = key[i] == best ? 0u : key[i];
+#pragma unroll
+        for (int q = 0; q < kMaxTopk / LPT; q++) mine[q] = n == q * LPT + l ? best : mine[q];
     }
-    wave_lds_fence();
-    // the weights, in 64 bits: lane l takes routes l, l + LPT, ...
+    return fine;
+}
+
+// ---------------------------------------------------------------- ranking in 64 bits
+// The key of expert e by its choice or, without one, by its logit v.
+template <bool WIDE>
+__device__ __forceinline__ uint64_t exact_key(const Args& a, int e, float v, float top, double z) {
+    if (!WIDE || !a.bias) return logit_key(v, e);
+    const double c = (a.score == MOE_SCORE_SOFTMAX ? exp((double)v - (double)top) / z : sigmoid64((double)v)) + (double)a.bias[e];
+    return value_key(c, e);
+}
+
+// Puts the first n keys of a token into their right order (about one token in a hundred has two that stand too close).
+template <int LPT, bool WIDE>
+__device__ __forceinline__ void refine(const Args& a, int t, int l, float top, int n, GroupLds& lds, uint32_t (&mine)[kMaxTopk / LPT]) {
     constexpr int RPL = kMaxTopk / LPT;
-    float lg[RPL];
-    double w[RPL], sum = 0.0;
-    float most = -kInf;
+    const int64_t row = (int64_t)t * a.stride;
+    double z = 0.0;
+    if (WIDE && a.bias && a.score == MOE_SCORE_SOFTMAX) {
+#pragma unroll 1
+        for (int e = l; e < a.E; e += LPT) {
+            const float v = shown(load_logit(a, row + e));
+            z += v > -__builtin_inff() ? exp((double)v - (double)top) : 0.0;
+        }
 #pragma unroll
-    for (int j = 0; j < RPL; j++) {
-        const int r = j * LPT + l;
-        const int id = r < a.topk ? lds.id[r] : -1;
-        lg[j] = id >= 0 ? load_logit(a, row + id) : -kInf;
-        most = __builtin_fmaxf(most, lg[j]);
+        for (int m = 1; m < LPT; m <<= 1) z += __shfl_xor(z, m, kWave);
     }
+    uint64_t key[RPL];
+    int rank[RPL];
+#pragma unroll
+    for (int q = 0; q < RPL; q++) {
+        const int e = (int)(1023u - (mine[q] & 1023u));
+        key[q] = 0ull;
+        if (mine[q]) key[q] = exact_key<WIDE>(a, e, shown(load_logit(a, row + e)), top, z);
+        rank[q] = 0;
+    }
+#pragma unroll
+    for (int q = 0; q < RPL; q++)
+        for (int j = 0; j < LPT && q * LPT + j < n; j++) {
+            const uint64_t k = (uint64_t)__shfl((long long)key[q], j, LPT);
+#pragma unroll
+            for (int p = 0; p < RPL; p++) rank[p] += k > key[p] ? 1 : 0;
+        }
+#pragma unroll
+    for (int q = 0; q < RPL; q++)
+        if (mine[q]) lds.top1[rank[q]] = mine[q];
+    wave_lds_fence();
+#pragma unroll
+    for (int q = 0; q < RPL; q++)
+        if (mine[q]) mine[q] = lds.top1[q * LPT + l];   // (the keys there are lead)
+}
+
+// All of a token in 64 bits, for the very few whose groups, or a great many of whose experts, stand close together: the
+// workgroup takes one at a time, an expert a thread.
+struct ExactLds {
+    uint64_t top1[kMaxGroups], top2[kMaxGroups];     // keys of each group's two largest choices
+    double val1[kMaxGroups], val2[kMaxGroups];       // and, for their sum, the choices
+    uint64_t part[2][kTok];
+    int32_t id[kMaxTopk];
+    float logit[kMaxTopk];                           // of the chosen experts
+};
+
+// The largest key of the workgroup.  `turn` alternates, so that the parts of one call are read before the next but one's.
+template <int THREADS>
+__device__ __forceinline__ uint64_t block_max(uint64_t k, ExactLds& lds, int& turn) {
+    // the largest upper half, then the largest lower half among those that have it
+    auto wave_max = [](uint64_t k) {
+        const uint32_t hi = token_umax<kWave>((uint32_t)(k >> 32));
+        const uint32_t lo = token_umax<kWave>((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+        return (uint64_t)hi << 32 | lo;
+    };
+    uint64_t* part = lds.part[turn];
+    turn ^= 1;
+    k = wave_max(k);
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = k;
+    __syncthreads();
+    return wave_max(part[threadIdx.x % (THREADS / kWave)]);
+}
+
+// Ranks token t: ids and logits of the ranks to lds.id and lds.logit, the softmax's largest logit and sum to top and z.
+template <int THREADS, bool WIDE>
+__device__ __forceinline__ void rank_exact(const Args& a, int t, ExactLds& lds, float& top, float& z) {
+    constexpr float kInf = __builtin_inff();
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    const int e = threadIdx.x, wave = threadIdx.x / kWave;
+    const float v = e < a.E ? shown(load_logit(a, (int64_t)t * a.stride + e)) : -kInf;
+    int turn = 0;
+    double sum = 1.0;
+    top = 0.0f;
+    if (softmax) {
+        top = from_mono32((uint32_t)block_max<THREADS>(mono32(v), lds, turn));
+        double part = v > -kInf ? exp((double)v - (double)top) : 0.0;
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) part += __shfl_xor(part, m, kWave);
+        uint64_t* parts = lds.part[turn];
+        turn ^= 1;
+        if (threadIdx.x % kWave == 0) parts[wave] = (uint64_t)__double_as_longlong(part);
+        __syncthreads();
+        sum = 0.0;
+#pragma unroll
+        for (int w = 0; w < THREADS / kWave; w++) sum += __longlong_as_double((long long)parts[w]);
+    }
+    z = (float)sum;
+    double c = 0.0;                             // the choice
+    uint64_t key = 0ull;
+    if (v > -kInf) {
+        if constexpr (WIDE) {
+            c = softmax ? exp((double)v - (double)top) / sum : sigmoid64((double)v);
+            if (a.bias) c += (double)a.bias[e];
+            key = c > -(double)kInf ? value_key(c, e) : 0ull;                       // (no key for NaN either)
+        } else {
+            key = logit_key(v, e);
+        }
+    }
+    if (a.n_group > 1) {                        // the best groups stay
+        const int size = a.E / a.n_group, g = min(e / size, kMaxGroups - 1);
+        const bool two = WIDE && a.group_top == 2;
+        if (e < a.n_group) lds.top1[e] = lds.top2[e] = 0ull;
+        __syncthreads();
+        if (key) atomicMax((unsigned long long*)&lds.top1[g], (unsigned long long)key);
+        __syncthreads();
+        if (two) {
+            if (key && key == lds.top1[g]) lds.val1[g] = c;
+            else if (key) atomicMax((unsigned long long*)&lds.top2[g], (unsigned long long)key);
+            __syncthreads();
+            if (key && key == lds.top2[g]) lds.val2[g] = c;
+            __syncthreads();
+        }
+        uint64_t gk = 0ull;
+        if (e < a.n_group && lds.top1[e]) {
+            gk = lds.top1[e];                   // its index orders ties by group as well
+            if (two) gk = value_key(lds.top2[e] ? lds.val1[e] + lds.val2[e] : lds.val1[e], e);
+        }
+        uint64_t kept = 0ull;
+        for (int n = 0; n < a.keep; n++) {
+            const uint64_t best = block_max<THREADS>(gk, lds, turn);
+            if (best == 0ull) break;
+            gk = gk == best ? 0ull : gk;
+            kept |= 1ull << (two ? key_index(best) : key_index(best) / size);
+        }
+        if (!(kept >> g & 1ull)) key = 0ull;
+        if constexpr (WIDE) {
+            if (!a.bias && key) key = logit_key(v, e);   // the groups went by scores, the order within them is the logits' own
+        }
+    }
+    for (int j = 0; j < a.topk; j++) {
+        const uint64_t best = block_max<THREADS>(key, lds, turn);
+        if (best ? key == best : e == 0) {
+            lds.id[j] = best ? e : -1;
+            lds.logit[j] = v;
+            key = 0ull;
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- a token
+// Scores' statistics of a token's logits in its lanes; the scores to memory where they are wanted.
+template <int LPT, int VPL, bool WIDE>
+__device__ __forceinline__ void score_token(const Args& a, const float (&v)[VPL], int t, int l, TokenScores<VPL>& s) {
+    constexpr float kInf = __builtin_inff();
+#pragma unroll
+    for (int i = 0; i < VPL; i++) s.v[i] = i * LPT + l < a.E ? shown(v[i]) : -kInf;
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    s.top = 0.0f;
+    s.z = 1.0f;
+    if (softmax && (WIDE || a.scores || !a.renorm)) {
+        float top = s.v[0];
+#pragma unroll
+        for (int i = 1; i < VPL; i++) top = larger(top, s.v[i]);
+        s.top = token_fmax<LPT>(top);
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) z += s.v[i] > -kInf ? fast_exp(s.v[i] - s.top) : 0.0f;
+        s.z = token_fsum<LPT>(z);
+    }
+    if (a.scores) {
+        const float inv = 1.0f / s.z;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            const int e = i * LPT + l;
+            const float p = s.v[i] > -kInf ? (softmax ? fast_exp(s.v[i] - s.top) * inv : fast_score(s.v[i])) : 0.0f;
+            if (e < a.E) a.scores[(int64_t)t * a.E + e] = p;
+        }
+    }
+}
+
+// Ids and weights of token t to memory: lane l has the ids (-1: none) and logits (-inf then) of routes l, l + LPT, ... .
+template <int LPT>
+__device__ __forceinline__ void weigh_token(const Args& a, int t, int l, const int (&id)[kMaxTopk / LPT], const float (&lg)[kMaxTopk / LPT],
+                                            float top, float z) {
+    constexpr float kInf = __builtin_inff();
+    constexpr int RPL = kMaxTopk / LPT;
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    float w[RPL], sum = 0.0f;
     if (a.renorm) {                             // ratios of scores: scaled by the largest one, nothing underflows as a whole
+        float most = lg[0];
+#pragma unroll
+        for (int j = 1; j < RPL; j++) most = larger(most, lg[j]);
         most = token_fmax<LPT>(most);
-        const float low = softmax ? most : __builtin_fminf(most, 0.0f);
+        const float low = softmax ? most : smaller(most, 0.0f);
 #pragma unroll
         for (int j = 0; j < RPL; j++) {
-            const double x = (double)lg[j];
-            w[j] = 0.0;
+            w[j] = 0.0f;
             if (lg[j] > -kInf) {
-                w[j] = exp(lg[j] >= 0.0f && !softmax ? 0.0 : x - (double)low);
-                if (!softmax) w[j] /= 1.0 + exp(-fabs(x));
+                w[j] = lg[j] >= 0.0f && !softmax ? 1.0f : exp_of_difference(lg[j], low);
+                if (!softmax) w[j] /= 1.0f + expf(-__builtin_fabsf(lg[j]));
             }
             sum += w[j];
         }
-        sum = token_sum<LPT>(sum);
+        sum = token_fsum<LPT>(sum);
     } else {
 #pragma unroll
-        for (int j = 0; j < RPL; j++) {
-            const double x = (double)lg[j];
-            w[j] = lg[j] > -kInf ? (softmax ? exp(x - (double)top) : sigmoid64(x)) : 0.0;
-        }
-        sum = softmax ? (WIDE ? z64 : (double)z) : 1.0;
+        for (int j = 0; j < RPL; j++) w[j] = lg[j] > -kInf ? (softmax ? exp_of_difference(lg[j], top) : sigmoid32(lg[j])) : 0.0f;
+        sum = softmax ? z : 1.0f;
     }
 #pragma unroll
     for (int j = 0; j < RPL; j++) {
         const int r = j * LPT + l;
         if (r < a.topk) {
-            a.ids[(int64_t)t * a.topk + r] = lds.id[r];
-            a.weights[(int64_t)t * a.topk + r] = lg[j] > -kInf ? (float)((double)a.scale * w[j] / sum) : 0.0f;
+            a.ids[(int64_t)t * a.topk + r] = id[j];
+            a.weights[(int64_t)t * a.topk + r] = lg[j] > -kInf ? a.scale * (w[j] / sum) : 0.0f;
         }
     }
 }
@@ -337,7 +627,10 @@ __device__ __forceinline__ int block_scan(int v, int* lds, int& total) {
 template <int LPT, int VPL, bool WIDE, bool SINGLE>
 __global__ void __launch_bounds__(kTok * LPT) route_kernel(const Args a) {
     constexpr int THREADS = kTok * LPT;
-    __shared__ TokenLds tok[kTok];
+    constexpr int RPL = kMaxTopk / LPT;
+    __shared__ GroupLds groups[kTok];
+    __shared__ ExactLds exact;
+    __shared__ int n_left, left[kSingle];              // tokens that 32 bits do not rank (a chunk has kSingle at most)
     __shared__ uint64_t mask[SINGLE ? kMaxE : 1];      // the tokens of each expert
     __shared__ uint32_t count[SINGLE ? 1 : kMaxE];
     __shared__ int32_t all_ids[SINGLE ? kSingle * kMaxTopk : 1];
@@ -346,26 +639,78 @@ __global__ void __launch_bounds__(kTok * LPT) route_kernel(const Args a) {
     const int l = threadIdx.x % LPT, w = threadIdx.x / LPT;
     const int t0 = blockIdx.x * a.chunk;
     const int n_tok = min(a.chunk, a.T - t0);
+    float next[VPL];                                   // the next token's logits are asked for before this one is ranked
+    if (w < n_tok) load_row<LPT>(a, t0 + w, l, next);
+    const LaneExperts<VPL> x = lane_experts<LPT, VPL>(a, l);
     for (int i = threadIdx.x; i < a.E; i += THREADS) {
         if constexpr (SINGLE) mask[i] = 0ull;
         else count[i] = 0u;
     }
+    if (threadIdx.x == 0) n_left = 0;
     __syncthreads();
+    auto count_routes = [&](int t, const int (&id)[RPL]) {
+#pragma unroll
+        for (int j = 0; j < RPL; j++) {
+            const int r = j * LPT + l;
+            if (r >= a.topk) continue;
+            if constexpr (SINGLE) {
+                all_ids[t * a.topk + r] = id[j];
+                if (id[j] >= 0) atomicOr((unsigned long long*)&mask[id[j]], 1ull << t);
+            } else {
+                if (id[j] >= 0) atomicAdd(&count[id[j]], 1u);
+            }
+        }
+    };
     for (int i = 0; i < n_tok; i += kTok) {
         if (i + w < n_tok) {                           // whole tokens are active or idle together
             const int t = t0 + i + w;
-            route_token<LPT, VPL, WIDE>(a, t, l, tok[w]);
-            for (int j = l; j < a.topk; j += LPT) {
-                const int e = tok[w].id[j];
-                if constexpr (SINGLE) {
-                    all_ids[t * a.topk + j] = e;
-                    if (e >= 0) atomicOr((unsigned long long*)&mask[e], 1ull << t);
-                } else if (e >= 0) {
-                    atomicAdd(&count[e], 1u);
+            TokenScores<VPL> s;
+            score_token<LPT, VPL, WIDE>(a, next, t, l, s);
+            if (i + kTok + w < n_tok) load_row<LPT>(a, t + kTok, l, next);
+            uint32_t mine[RPL];
+            int n;
+            bool close;
+            if (rank_fast<LPT, VPL, WIDE>(a, x, s, l, groups[w], mine, n, close)) {
+                if (close) refine<LPT, WIDE>(a, t, l, s.top, n, groups[w], mine);
+                int id[RPL];
+                float lg[RPL];
+#pragma unroll
+                for (int j = 0; j < RPL; j++) {
+                    id[j] = mine[j] && j * LPT + l < a.topk ? (int)(1023u - (mine[j] & 1023u)) : -1;
+                    lg[j] = -__builtin_inff();
+                    if (j * LPT >= a.topk) continue;
+#pragma unroll
+                    for (int k = 0; k < VPL; k++) {
+                        const float y = __shfl(s.v[k], id[j] & (LPT - 1), LPT);
+                        lg[j] = id[j] >= 0 && id[j] / LPT == k ? y : lg[j];
+                    }
                 }
+                weigh_token<LPT>(a, t, l, id, lg, s.top, s.z);
+                count_routes(t, id);
+            } else if (l == 0) {
+                left[atomicAdd(&n_left, 1)] = t;
             }
-            wave_lds_fence();                          // the ids are read before the next token's
+            wave_lds_fence();                          // the groups are read before the next token's
         }
+    }
+    __syncthreads();
+    for (int i = 0; i < n_left; i++) {                 // (each by itself: their order changes nothing)
+        const int t = left[i];
+        float top, z;
+        rank_exact<THREADS, WIDE>(a, t, exact, top, z);
+        if (threadIdx.x < LPT) {
+            int id[RPL];
+            float lg[RPL];
+#pragma unroll
+            for (int j = 0; j < RPL; j++) {
+                const int r = j * LPT + l;
+                id[j] = r < a.topk ? exact.id[r] : -1;
+                lg[j] = id[j] >= 0 ? exact.logit[r] : -__builtin_inff();
+            }
+            weigh_token<LPT>(a, t, l, id, lg, top, z);
+            count_routes(t, id);
+        }
+        __syncthreads();                               // before the next one's
     }
     if (!a.dst2src) return;
     __syncthreads();
@@ -435,12 +780,15 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const Args a) 
     __shared__ int total[kMaxE], base[kMaxE];
     __shared__ uint64_t mask[kMaxE];
     __shared__ int sums[kScatterThreads / kWave];
+    __shared__ uint4 sum4[SCANNED ? 1 : kScatterThreads];
     const int rw = row_bytes(a.E), c = blockIdx.x;
     const int t0 = c * a.chunk, n_tok = min(a.chunk, a.T - t0), n = n_tok * a.topk;
     const int32_t* ids = a.ids + (int64_t)t0 * a.topk;
     for (int e = threadIdx.x; e < a.E; e += kScatterThreads) {
-        total[e] = SCANNED ? a.before[(int64_t)a.nc * rw + e] : 0;
-        base[e] = SCANNED ? a.before[(int64_t)c * rw + e] : 0;
+        if constexpr (SCANNED) {
+            total[e] = a.before[(int64_t)a.nc * rw + e];
+            base[e] = a.before[(int64_t)c * rw + e];
+        }
         mask[e] = 0ull;
     }
     __syncthreads();
@@ -449,37 +797,34 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const Args a) 
         if (e >= 0) atomicOr((unsigned long long*)&mask[e], 1ull << (i / a.topk));
     }
     if constexpr (!SCANNED) {
-        // 16 experts a thread and load; sums of bytes as 16-bit pairs (at most 512 chunks of at most 64 tokens)
-        const int quads = rw / 16, parts = kScatterThreads / quads;
+        // Four experts a thread (a word of a chunk's counts), the chunks dealt over the parts of the workgroup; sums of bytes as
+        // 16-bit pairs (at most 512 chunks of at most 64 tokens), added up over the parts through LDS.
+        const int quads = rw / 4, parts = kScatterThreads / quads;
         const int qd = threadIdx.x % quads, part = threadIdx.x / quads;
+        uint32_t even = 0, odd = 0, even_b = 0, odd_b = 0;
         if (part < parts) {
-            uint32_t lo[4] = {}, hi[4] = {}, blo[4] = {}, bhi[4] = {};
+#pragma unroll 16
             for (int cc = part; cc < a.nc; cc += parts) {
-                const uint4 x = *reinterpret_cast<const uint4*>(a.counts + (int64_t)cc * rw + qd * 16);
-                const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-                const uint32_t early = cc < c ? 0xFFFFFFFFu : 0u;
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const uint32_t even = v[k] & 0x00FF00FFu, odd = v[k] >> 8 & 0x00FF00FFu;
-                    lo[k] += even;
-                    hi[k] += odd;
-                    blo[k] += even & early;
-                    bhi[k] += odd & early;
-                }
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(a.counts + (int64_t)cc * rw + qd * 4);
+                const uint32_t early = cc < c ? 0x00FF00FFu : 0u;
+                even += v & 0x00FF00FFu;
+                odd += v >> 8 & 0x00FF00FFu;
+                even_b += v & early;
+                odd_b += v >> 8 & early;
             }
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int e = qd * 16 + 4 * k;
-#pragma unroll
-                for (int b = 0; b < 4; b++) {
-                    const uint32_t s = (b & 1 ? hi[k] : lo[k]) >> (b & 2 ? 16 : 0) & 0xFFFFu;
-                    const uint32_t f = (b & 1 ? bhi[k] : blo[k]) >> (b & 2 ? 16 : 0) & 0xFFFFu;
-                    if (e + b < a.E && s) {
-                        atomicAdd(&total[e + b], (int)s);
-                        if (f) atomicAdd(&base[e + b], (int)f);
-                    }
-                }
+            sum4[threadIdx.x] = make_uint4(even, odd, even_b, odd_b);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += kScatterThreads) {
+            const int sh = (e & 2) * 8;
+            int all = 0, early = 0;
+            for (int p = 0; p < parts; p++) {
+                const uint4 v = sum4[p * quads + e / 4];
+                all += (e & 1 ? v.y : v.x) >> sh & 0xFFFFu;
+                early += (e & 1 ? v.w : v.z) >> sh & 0xFFFFu;
             }
+            total[e] = all;
+            base[e] = early;
         }
     }
     __syncthreads();
