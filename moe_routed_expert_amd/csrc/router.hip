@@ -10,7 +10,7 @@
 //    value, ties to the lower index".  Without a bias the order is the logits' own, which needs no exponential.  With one (or
 //    with group values that are sums) scores have to be formed in 64 bits, for in 32 about one token in ten thousand has two
 //    choices next to each other that round to the wrong order; but 64-bit exponentials and 64-bit keys for every expert took
-//    86 us where this takes 52 (16384 tokens, 512 experts).  So keys are 32 bits: 22-bit steps over the token's own range, formed
+//    86 us where this takes 46 (16384 tokens, 512 experts).  So keys are 32 bits: 22-bit steps over the token's own range, formed
 //    with 32-bit scores whose error is known in steps.  Where two keys that matter are closer than that, the candidates alone
 //    are ranked again in 64 bits (refine, one token in a hundred), and where groups are, all of the token (rank_exact).  16-bit
 //    logits fit a key as they are.
@@ -21,8 +21,8 @@
 //    counts of all chunks (bytes) for the experts' offsets and of the chunks before its own for its rows.  With more than
 //    kSumChunks chunks those sums come from a scan launched between.
 //  * Bound by instruction issue and the latency of the rounds, not by bytes: 4096 tokens of 256 fp32 logits in 8 groups with
-//    maps take 20.6 us in two launches (780 vector instructions a token), 16384 of 512 bf16 ones with their scores 51.8 us in
-//    three (50 MB: 1 TB/s), eight of 64 experts 7.6 us, which is the call.
+//    maps take 20.6 us in two launches (770 vector instructions a token), 16384 of 512 bf16 ones with their scores 46.1 us in
+//    three (50 MB: 1.1 TB/s), eight of 64 experts 7.6 us, which is the call.
 #include <algorithm>
 #include <type_traits>
 
@@ -240,7 +240,7 @@ __device__ __forceinline__ uint32_t half_key(float v, bool bf16, int e) {
 // Ranks the token's experts by 32-bit keys: lane l gets the keys of ranks l, l + LPT, ... (0: none).  Of the n keys every other
 // expert is surely below; `close` if some of them may stand in the wrong order.  False if the groups, or more than 64 values,
 // are too near.
-template <int LPT, int VPL, bool WIDE>
+template <int LPT, int VPL, bool WIDE, bool SOFT>
 __device__ __forceinline__ bool rank_fast(const Args& a, const LaneExperts<VPL>& x, const TokenScores<VPL>& s, int l, GroupLds& lds,
                                           uint32_t (&mine)[kMaxTopk / LPT], int& n, bool& close) {
     constexpr float kInf = __builtin_inff();
@@ -262,7 +262,7 @@ __device__ __forceinline__ bool rank_fast(const Args& a, const LaneExperts<VPL>&
         }
     };
     if constexpr (WIDE) {
-        const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+        constexpr bool softmax = SOFT;
         const float inv = softmax ? __builtin_amdgcn_rcpf(s.z) : 1.0f;
         float c[VPL];
 #pragma unroll
@@ -413,7 +413,12 @@ __device__ __forceinline__ void refine(const Args& a, int t, int l, float top, i
 #pragma unroll
     for (int q = 0; q < RPL; q++)
         for (int j = 0; j < LPT && q * LPT + j < n; j++) {
-            const uint64_t k = (uint64_t)__shfl((long long)key[q], j, LPT);
+            uint64_t k;
+            if constexpr (LPT == kWave)
+                k = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key[q] >> 32), j) << 32 |
+                    (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key[q], j);
+            else
+                k = (uint64_t)__shfl((long long)key[q], j, LPT);
 #pragma unroll
             for (int p = 0; p < RPL; p++) rank[p] += k > key[p] ? 1 : 0;
         }
@@ -532,12 +537,12 @@ __device__ __forceinline__ void rank_exact(const Args& a, int t, ExactLds& lds, 
 
 // ---------------------------------------------------------------- a token
 // Scores' statistics of a token's logits in its lanes; the scores to memory where they are wanted.
-template <int LPT, int VPL, bool WIDE>
+template <int LPT, int VPL, bool WIDE, bool SOFT>
 __device__ __forceinline__ void score_token(const Args& a, const float (&v)[VPL], int t, int l, TokenScores<VPL>& s) {
     constexpr float kInf = __builtin_inff();
 #pragma unroll
     for (int i = 0; i < VPL; i++) s.v[i] = i * LPT + l < a.E ? shown(v[i]) : -kInf;
-    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    constexpr bool softmax = SOFT;
     s.top = 0.0f;
     s.z = 1.0f;
     if (softmax && (WIDE || a.scores || !a.renorm)) {
@@ -562,12 +567,12 @@ __device__ __forceinline__ void score_token(const Args& a, const float (&v)[VPL]
 }
 
 // Ids and weights of token t to memory: lane l has the ids (-1: none) and logits (-inf then) of routes l, l + LPT, ... .
-template <int LPT>
+template <int LPT, bool SOFT>
 __device__ __forceinline__ void weigh_token(const Args& a, int t, int l, const int (&id)[kMaxTopk / LPT], const float (&lg)[kMaxTopk / LPT],
                                             float top, float z) {
     constexpr float kInf = __builtin_inff();
     constexpr int RPL = kMaxTopk / LPT;
-    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    constexpr bool softmax = SOFT;
     float w[RPL], sum = 0.0f;
     if (a.renorm) {                             // ratios of scores: scaled by the largest one, nothing underflows as a whole
         float most = lg[0];
@@ -624,7 +629,7 @@ __device__ __forceinline__ int block_scan(int v, int* lds, int& total) {
 }
 
 // SINGLE: one workgroup, T <= kSingle, maps too.  Else chunk blockIdx.x, whose counts are written when maps are wanted.
-template <int LPT, int VPL, bool WIDE, bool SINGLE>
+template <int LPT, int VPL, bool WIDE, bool SOFT, bool SINGLE>
 __global__ void __launch_bounds__(kTok * LPT) route_kernel(const Args a) {
     constexpr int THREADS = kTok * LPT;
     constexpr int RPL = kMaxTopk / LPT;
@@ -665,12 +670,12 @@ __global__ void __launch_bounds__(kTok * LPT) route_kernel(const Args a) {
         if (i + w < n_tok) {                           // whole tokens are active or idle together
             const int t = t0 + i + w;
             TokenScores<VPL> s;
-            score_token<LPT, VPL, WIDE>(a, next, t, l, s);
+            score_token<LPT, VPL, WIDE, SOFT>(a, next, t, l, s);
             if (i + kTok + w < n_tok) load_row<LPT>(a, t + kTok, l, next);
             uint32_t mine[RPL];
             int n;
             bool close;
-            if (rank_fast<LPT, VPL, WIDE>(a, x, s, l, groups[w], mine, n, close)) {
+            if (rank_fast<LPT, VPL, WIDE, SOFT>(a, x, s, l, groups[w], mine, n, close)) {
                 if (close) refine<LPT, WIDE>(a, t, l, s.top, n, groups[w], mine);
                 int id[RPL];
                 float lg[RPL];
@@ -685,7 +690,7 @@ __global__ void __launch_bounds__(kTok * LPT) route_kernel(const Args a) {
                         lg[j] = id[j] >= 0 && id[j] / LPT == k ? y : lg[j];
                     }
                 }
-                weigh_token<LPT>(a, t, l, id, lg, s.top, s.z);
+                weigh_token<LPT, SOFT>(a, t, l, id, lg, s.top, s.z);
                 count_routes(t, id);
             } else if (l == 0) {
                 left[atomicAdd(&n_left, 1)] = t;
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(kTok * LPT) route_kernel(const Args a) {
                 id[j] = r < a.topk ? exact.id[r] : -1;
                 lg[j] = id[j] >= 0 ? exact.logit[r] : -__builtin_inff();
             }
-            weigh_token<LPT>(a, t, l, id, lg, top, z);
+            weigh_token<LPT, SOFT>(a, t, l, id, lg, top, z);
             count_routes(t, id);
         }
         __syncthreads();                               // before the next one's
@@ -863,19 +868,25 @@ __global__ void zero_offsets_kernel(int E, int32_t* offsets) {
 
 int chunk_of(int64_t T) { return T <= kSingle ? kSingle : T <= (int64_t)kTok * kSumChunks ? kTok : 64; }
 
-template <int LPT, int VPL, bool WIDE>
+template <int LPT, int VPL, bool WIDE, bool SOFT>
 void launch_route(hipStream_t st, const Args& a) {
     const dim3 block(kTok * LPT);
-    if (a.T <= kSingle) hipLaunchKernelGGL((route_kernel<LPT, VPL, WIDE, true>), dim3(1), block, 0, st, a);
-    else hipLaunchKernelGGL((route_kernel<LPT, VPL, WIDE, false>), dim3((unsigned)a.nc), block, 0, st, a);
+    if (a.T <= kSingle) hipLaunchKernelGGL((route_kernel<LPT, VPL, WIDE, SOFT, true>), dim3(1), block, 0, st, a);
+    else hipLaunchKernelGGL((route_kernel<LPT, VPL, WIDE, SOFT, false>), dim3((unsigned)a.nc), block, 0, st, a);
+}
+
+template <bool WIDE, bool SOFT>
+void launch_route_e(hipStream_t st, const Args& a) {
+    if (a.E <= 64) launch_route<16, 4, WIDE, SOFT>(st, a);
+    else if (a.E <= 256) launch_route<64, 4, WIDE, SOFT>(st, a);
+    else if (a.E <= 512) launch_route<64, 8, WIDE, SOFT>(st, a);
+    else launch_route<64, 16, WIDE, SOFT>(st, a);
 }
 
 template <bool WIDE>
-void launch_route_e(hipStream_t st, const Args& a) {
-    if (a.E <= 64) launch_route<16, 4, WIDE>(st, a);
-    else if (a.E <= 256) launch_route<64, 4, WIDE>(st, a);
-    else if (a.E <= 512) launch_route<64, 8, WIDE>(st, a);
-    else launch_route<64, 16, WIDE>(st, a);
+void launch_route_score(hipStream_t st, const Args& a) {
+    if (a.score == MOE_SCORE_SOFTMAX) launch_route_e<WIDE, true>(st, a);
+    else launch_route_e<WIDE, false>(st, a);
 }
 
 // ------------------------------------------------------------------ the gradient
@@ -1063,8 +1074,8 @@ extern "C" int moe_router(const void* logits, int dt, int64_t logits_stride, int
         a.counts = (uint8_t*)workspace;
         a.before = (int32_t*)(a.counts + (int64_t)a.nc * router::row_bytes((int)E));
     }
-    if (bias || (a.n_group > 1 && group_top == 2)) router::launch_route_e<true>(st, a);
-    else router::launch_route_e<false>(st, a);
+    if (bias || (a.n_group > 1 && group_top == 2)) router::launch_route_score<true>(st, a);
+    else router::launch_route_score<false>(st, a);
     if (maps && T > router::kSingle) {
         const dim3 grid((unsigned)a.nc), block(router::kScatterThreads);
         if (a.nc > router::kSumChunks) {
