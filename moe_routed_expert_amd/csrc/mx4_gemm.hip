@@ -336,8 +336,8 @@ int grouped_launch(hipStream_t st, const GemmArgs& g) {
 
 // ------------------------------------------------------------------ slot mode
 // A group of KS waves holds 16 columns of one row, each wave a part of k; W is the MFMA's row operand and the row of A
-// stands in all 16 columns of the other.  The sums of the waves meet in LDS in order.
-template <int KS, bool FUSED>
+// stands in all 16 columns of the other.  The sums of the waves meet in LDS in order.  U windows of 256 of k are in flight.
+template <int KS, int U, bool FUSED>
 __global__ void __launch_bounds__(64 * KS * (FUSED ? 4 : 1))
 mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_row_div, int col_groups) {
     constexpr int SUBS = FUSED ? 4 : 1;                // 16-column sub-tiles of a workgroup (fused: two of gate, two of up)
@@ -359,19 +359,32 @@ mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
         const char* as = g.a_s + ar * g.a_s_stride;
         const int windows = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup);
         const int per = (windows + KS - 1) / KS;
+        const int end = min((ks + 1) * per, windows);
         v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int t = ks * per; t < min((ks + 1) * per, windows); t++) {
-            // this lane's blocks 8t + 2 quad and the next; past the end the last block is read and counted as zero
-            const int b = 8 * t + 2 * quad;
-            const int b0 = min(b, blocks - 1), b1 = min(b + 1, blocks - 1);
-            v4i w0 = *reinterpret_cast<const v4i*>(w + b0 * 16), w1 = *reinterpret_cast<const v4i*>(w + b1 * 16);
-            v4i x0 = *reinterpret_cast<const v4i*>(a + b0 * 16), x1 = *reinterpret_cast<const v4i*>(a + b1 * 16);
-            uint32_t s0 = (uint8_t)ws[b0], s1 = (uint8_t)ws[b1], u0 = (uint8_t)as[b0], u1 = (uint8_t)as[b1];
-            const v4i zero = {0, 0, 0, 0};
-            if (b >= blocks) { w0 = zero; x0 = zero; s0 = 0; u0 = 0; }
-            if (b + 1 >= blocks) { w1 = zero; x1 = zero; s1 = 0; u1 = 0; }
-            acc = mfma<0>(w0, s0, x0, u0, acc);
-            acc = mfma<0>(w1, s1, x1, u1, acc);
+        for (int t0 = ks * per; t0 < end; t0 += U) {
+            v4i w0[U], w1[U], x0[U], x1[U];
+            uint32_t sw[U], sx[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                // this lane's blocks 8t + 2 quad and the next, whose scales are one aligned pair of bytes; past the end the last
+                // block is read and counted as zero
+                const int b = t0 + u < end ? 8 * (t0 + u) + 2 * quad : blocks, b0 = min(b, blocks - 1), b1 = min(b + 1, blocks - 1);
+                w0[u] = *reinterpret_cast<const v4i*>(w + b0 * 16);
+                w1[u] = *reinterpret_cast<const v4i*>(w + b1 * 16);
+                sw[u] = *reinterpret_cast<const uint16_t*>(ws + (b0 & ~1));
+                x0[u] = *reinterpret_cast<const v4i*>(a + b0 * 16);
+                x1[u] = *reinterpret_cast<const v4i*>(a + b1 * 16);
+                sx[u] = *reinterpret_cast<const uint16_t*>(as + (b0 & ~1));
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int b = t0 + u < end ? 8 * (t0 + u) + 2 * quad : blocks;
+                const v4i zero = {0, 0, 0, 0};
+                if (b >= blocks) { w0[u] = zero; x0[u] = zero; sw[u] = 0; sx[u] = 0; }
+                if (b + 1 >= blocks) { w1[u] = zero; x1[u] = zero; sw[u] &= 255u; sx[u] &= 255u; }
+                acc = mfma<0>(w0[u], sw[u], x0[u], sx[u], acc);
+                acc = mfma<1>(w1[u], sw[u], x1[u], sx[u], acc);
+            }
         }
         if (l16 == 0) {
 #pragma unroll
@@ -387,22 +400,20 @@ mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
         return v;
     };
     if constexpr (FUSED) {
-        // lanes 0..3 hold eight columns each
-        float h[8] = {};
-        if (lane < 4) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int c = 8 * lane + i;
-                const float gt = total(c / 16, c % 16), up = total(2 + c / 16, c % 16);
-                switch (g.act) {
-                    case 1: h[i] = gated<1>(gt, up); break;
-                    case 2: h[i] = gated<2>(gt, up); break;
-                    case 3: h[i] = gated<3>(gt, up); break;
-                    case 4: h[i] = gated<4>(gt, up); break;
-                    default: h[i] = gated<5>(gt, up); break;
-                }
-            }
+        // a column a lane for the gate, eight a lane for the codes
+        const int c = lane & 31;
+        const float gt = total(c / 16, c % 16), up = total(2 + c / 16, c % 16);
+        float v = 0.0f;
+        switch (g.act) {
+            case 1: v = gated<1>(gt, up); break;
+            case 2: v = gated<2>(gt, up); break;
+            case 3: v = gated<3>(gt, up); break;
+            case 4: v = gated<4>(gt, up); break;
+            default: v = gated<5>(gt, up); break;
         }
+        float h[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) h[i] = __shfl(v, 8 * (lane & 3) + i, kWave);
         uint32_t top = max_bits8(h);
         top = max(top, (uint32_t)__shfl_xor((int)top, 1, kWave));
         top = max(top, (uint32_t)__shfl_xor((int)top, 2, kWave));
@@ -423,20 +434,25 @@ mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
     }
 }
 
-template <int KS, bool FUSED>
+template <int KS, int U, bool FUSED>
 int slot_launch_ks(hipStream_t st, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
     constexpr int THREADS = 64 * KS * (FUSED ? 4 : 1);
     const int64_t groups = ceil_div(g.N, FUSED ? 32 : 16);
     if (groups * g.m_rows >= (int64_t)1 << (FUSED ? 22 : 24)) return MOE_ERR_SHAPE;   // a grid's threads fit 32 bits, whatever KS
-    hipLaunchKernelGGL((mx4_slot_kernel<KS, FUSED>), dim3((unsigned)(groups * g.m_rows)), dim3(THREADS), 0, st, g, slots, a_row_div,
+    hipLaunchKernelGGL((mx4_slot_kernel<KS, U, FUSED>), dim3((unsigned)(groups * g.m_rows)), dim3(THREADS), 0, st, g, slots, a_row_div,
                        (int)groups);
     return launch_status();
 }
 
-// The parts of k go by K alone, so that the fused form's sums are those of the plain one.
+// The parts of k go by K alone, so that the fused form's sums are those of the plain one.  A wave asks for as many windows at
+// once as it has, two at most: one at a time, with the scales in single bytes, 64 rows of 4096 x 4096 took 137 us, two 105
+// (5.4 TB/s); four 105, and fused 133, for they leave half the waves a unit.  Where each of the four waves has one window,
+// asking for two of which one is not there costs 53 us instead of 29 (64 rows of 4096 x 1024).  Small calls are
+// latency: eight rows of 1536 x 2048 take 5.3 us (2.5 TB/s).
 template <bool FUSED>
 int slot_launch(hipStream_t st, const GemmArgs& g, const int32_t* slots, int64_t a_row_div) {
-    return g.K > 2 * kStepK ? slot_launch_ks<4, FUSED>(st, g, slots, a_row_div) : slot_launch_ks<1, FUSED>(st, g, slots, a_row_div);
+    if (g.K <= 2 * kStepK) return slot_launch_ks<1, 2, FUSED>(st, g, slots, a_row_div);
+    return g.K > 4 * kStepK ? slot_launch_ks<4, 2, FUSED>(st, g, slots, a_row_div) : slot_launch_ks<4, 1, FUSED>(st, g, slots, a_row_div);
 }
 
 // Checks that both products share; MOE_OK when the call may go on.  bank_rows: N, or 2I.
