@@ -349,14 +349,15 @@ mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
     const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)col_groups) * (FUSED ? 32 : 16);
     const int slot = slots[r];
     const int64_t ar = g.a_rows ? (int64_t)g.a_rows[r] : r / a_row_div;
-    const bool live = slot >= 0 && slot < g.n_experts && ar >= 0 && ar < g.a_n;
+    const bool live = slot >= 0 && slot < g.n_experts;
     if (live) {
+        const bool row_there = ar >= 0 && ar < g.a_n;  // else a row of zeros, which a NaN of the bank makes NaN all the same
         const int64_t col = FUSED ? n0 + (sub & 1) * 16 : n0;
         const int64_t row = min(col + l16, g.N - 1) + (FUSED && sub >= 2 ? g.N : 0);
         const char* w = g.w + slot * g.w_stride_e + row * g.w_stride_n;
         const char* ws = g.w_s + slot * g.w_s_stride_e + row * g.w_s_stride_n;
-        const char* a = g.a + ar * g.a_stride;
-        const char* as = g.a_s + ar * g.a_s_stride;
+        const char* a = g.a + (row_there ? ar : 0) * g.a_stride;
+        const char* as = g.a_s + (row_there ? ar : 0) * g.a_s_stride;
         const int windows = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup);
         const int per = (windows + KS - 1) / KS;
         const int end = min((ks + 1) * per, windows);
@@ -380,6 +381,7 @@ mx4_slot_kernel(const GemmArgs g, const int32_t* __restrict__ slots, int64_t a_r
             for (int u = 0; u < U; u++) {
                 const int b = t0 + u < end ? 8 * (t0 + u) + 2 * quad : blocks;
                 const v4i zero = {0, 0, 0, 0};
+                if (!row_there) { x0[u] = zero; x1[u] = zero; sx[u] = 0; }
                 if (b >= blocks) { w0[u] = zero; x0[u] = zero; sw[u] = 0; sx[u] = 0; }
                 if (b + 1 >= blocks) { w1[u] = zero; x1[u] = zero; sw[u] &= 255u; sx[u] &= 255u; }
                 acc = mfma<0>(w0[u], sw[u], x0[u], sx[u], acc);

@@ -164,6 +164,25 @@ def test_nan_scales_reach_their_sums_alone(mode, K):
     assert torch.equal(torch.isnan(out).cpu(), want) and torch.isfinite(out).cpu().logical_or(want).all()
 
 
+@pytest.mark.parametrize("mode", [G, S])
+def test_rows_outside_are_zeros_that_a_nan_of_the_bank_reaches(mode):
+    """0 * NaN: what a row of zeros in A itself gives."""
+    N, K = 40, 1056
+    p = Problem(2, 5, N, K)
+    aq, as_, wq, ws = p.gpu
+    aq[2], as_[2], ws[1, 7, 3] = 0, 0, 255
+    amap = torch.tensor([-1, 2, 5, 1], dtype=torch.int32, device=dev())
+    how = dict(expert_offsets=torch.tensor([0, 0, 4], dtype=torch.int32, device=dev())) if mode == G else dict(
+        slot_ids=torch.ones(4, dtype=torch.int32, device=dev()))
+    out = torch.empty((4, N), device=dev())
+    m.mx4_grouped_gemm(aq, as_, wq, ws, out, mode=mode, a_rows=amap, **how)
+    zeros = torch.zeros(N, device=dev())
+    zeros[7] = float("nan")
+    for r in range(3):
+        assert torch.equal(torch.isnan(out[r]), torch.isnan(zeros)) and (torch.nan_to_num(out[r]) == 0).all()
+    assert torch.isnan(out[3, 7]) and torch.isfinite(out[3]).sum() == N - 1
+
+
 def test_decreasing_offsets_leave_out_untouched():
     p = Problem(3, 20, 64, 256)
     for offs in ([0, 12, 5, 20], [0, 20, 20, 19]):
