@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "mx4_tile.h"
 
@@ -54,11 +55,22 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
     int prod_t = walk.start, prod_left = 0, prod_kt = 0, prod_stage = 0;
     const int row_byte = code_byte(wave, lane);
     // !BUF: each lane's source of every load, and the bytes of a row (0 past the last tile)
-    const char *p_src[BUF ? 1 : C::P_LOADS], *q_src[BUF ? 1 : C::Q_LOADS], *s_src[BUF ? 1 : C::S_LOADS];
+    const char *p_src[BUF ? 1 : C::P_LOADS], *q_src[BUF ? 1 : C::Q_LOADS], *s_src[BUF ? 1 : C::LOADS];
     int64_t prod_bytes = 0;
     // BUF: each lane's offsets; what the step's lanes past the end of k (the last step's second half, or all of them past the
-    // last tile) take instead is or-ed in
-    uint32_t p_off[BUF ? C::P_LOADS : 1], q_off[BUF ? C::Q_LOADS : 1], s_off[BUF ? C::S_LOADS : 1], code_out = 0;
+    // last tile) take instead is or-ed in.  The rows of W that a lane takes differ from one load to the next by as much in every
+    // lane: one offset of the lane's own and a scalar one per load.  (Rows past the last are past the end of the bank, or
+    // the fused form's gate rows past the last some rows of up; their columns are dropped.)
+    uint32_t p_off[BUF ? C::P_LOADS : 1], q_off = 0, code_out = 0;
+    uint32_t sp_off[BUF ? C::P_LOADS : 1], sq_off = 0;
+    auto w_past = [&](int j) __attribute__((always_inline)) {                  // rows from a lane's first to that of load j
+        const int r = j * C::NW * 8;
+        return FUSED ? (r >> 6) * 32 + (r & 31) + (r & 32 ? (int)g.N : 0) : r;
+    };
+    auto w_first = [&](const Tile& ti, int l) __attribute__((always_inline)) {
+        const int r = code_row<C::NW>(0, wave, l);
+        return ti.n0 + (FUSED ? (r & 31) + (r & 32 ? (int)g.N : 0) : r);
+    };
     const bool half_step = BUF && g.K % kStepK != 0;
     v4i a_buf, as_buf, w_buf, ws_buf;
     if constexpr (BUF) {
@@ -84,11 +96,12 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
                 if constexpr (BUF) p_off[j] = m < 0 ? kNowhere : (uint32_t)(m * g.a_stride) + row_byte;
                 else p_src[j] = m < 0 ? nullptr : g.a + m * g.a_stride + row_byte;
             }
+            if constexpr (BUF) {
+                q_off = (uint32_t)w_first(ti, l) * (uint32_t)g.w_stride_n + row_byte;
+            } else {
 #pragma unroll
-            for (int j = 0; j < C::Q_LOADS; j++) {
-                const int64_t at = walk.template w_row<FUSED>(ti, code_row<C::NW>(j, wave, l)) * g.w_stride_n;
-                if constexpr (BUF) q_off[j] = (uint32_t)at + row_byte;
-                else q_src[j] = w + at + row_byte;
+                for (int j = 0; j < C::Q_LOADS; j++)
+                    q_src[j] = w + walk.template w_row<FUSED>(ti, code_row<C::NW>(j, wave, l)) * g.w_stride_n + row_byte;
             }
         }
         if constexpr (BUF) outside();
@@ -98,7 +111,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
         const uint32_t dst = lds + prod_stage * C::CODES + wave * 1024 + j * C::NW * 1024;
         if constexpr (BUF) {
             if (j < C::P_LOADS) buf16(p_off[j] | code_out, a_buf, prod_kt * kRowBytes, dst);
-            else buf16(q_off[j - C::P_LOADS] | code_out, w_buf, prod_kt * kRowBytes, dst);
+            else buf16(q_off | code_out, w_buf, (uint32_t)w_past(j - C::P_LOADS) * (uint32_t)g.w_stride_n + prod_kt * kRowBytes, dst);
         } else {
             const int64_t at = (int64_t)prod_kt * kRowBytes;
             const char* src = j < C::P_LOADS ? p_src[j] : q_src[j - C::P_LOADS];
@@ -134,13 +147,16 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
         sc_c = first_chunk(ti.expert);
         const char* w_s = g.w_s + ti.expert * g.w_s_stride_e;
         if constexpr (BUF) ws_buf = buffer_of(w_s, (bank - 1) * g.w_s_stride_n + blocks);
+        if constexpr (BUF) sq_off = (uint32_t)w_first(ti, l) * (uint32_t)g.w_s_stride_n + sc_word * 4;
 #pragma unroll
-        for (int j = 0; j < C::S_LOADS; j++) {
-            const int r0 = (wave * C::S_LOADS + j) * 8, r = r0 + l / 8;
-            const bool is_a = r0 < C::BP;              // wave-uniform
-            const int64_t m = is_a ? walk.a_row(ti, r) : walk.template w_row<FUSED>(ti, r - C::BP);
-            if constexpr (BUF) s_off[j] = m < 0 ? kNowhere : (uint32_t)(m * (is_a ? g.a_s_stride : g.w_s_stride_n)) + sc_word * 4;
-            else s_src[j] = m < 0 ? nullptr : (is_a ? g.a_s + m * g.a_s_stride : w_s + m * g.w_s_stride_n) + sc_word * 4;
+        for (int j = 0; j < C::LOADS; j++) {
+            if (j < C::P_LOADS) {
+                const int64_t m = walk.a_row(ti, code_row<C::NW>(j, wave, l));
+                if constexpr (BUF) sp_off[j] = m < 0 ? kNowhere : (uint32_t)(m * g.a_s_stride) + sc_word * 4;
+                else s_src[j] = m < 0 ? nullptr : g.a_s + m * g.a_s_stride + sc_word * 4;
+            } else if constexpr (!BUF) {
+                s_src[j] = w_s + walk.template w_row<FUSED>(ti, code_row<C::NW>(j - C::P_LOADS, wave, l)) * g.w_s_stride_n + sc_word * 4;
+            }
         }
     };
     auto request_scales = [&]() __attribute__((always_inline)) {
@@ -149,14 +165,13 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
             aim_scales();
         }
         const bool in = sc_t < walk.tiles && sc_word < words - 2 * kChunk * sc_c;
+        const uint32_t at = (uint32_t)sc_c * (kChunk * kRowScales);
 #pragma unroll
-        for (int j = 0; j < C::S_LOADS; j++) {
-            const uint32_t dst = chunk_at + (wave * C::S_LOADS + j) * 256;
-            const int64_t at = (int64_t)sc_c * (kChunk * kRowScales);
+        for (int j = 0; j < C::LOADS; j++) {
+            const uint32_t dst = chunk_at + (j * C::NW + wave) * 256;                  // (BP / 8 = P_LOADS * NW: W's rows follow)
             if constexpr (BUF) {
-                const uint32_t off = in ? s_off[j] : kNowhere;
-                if ((wave * C::S_LOADS + j) * 8 < C::BP) buf4(off, as_buf, (uint32_t)at, dst);
-                else buf4(off, ws_buf, (uint32_t)at, dst);
+                if (j < C::P_LOADS) buf4(in ? sp_off[j] : kNowhere, as_buf, at, dst);
+                else buf4(in ? sq_off : kNowhere, ws_buf, (uint32_t)w_past(j - C::P_LOADS) * (uint32_t)g.w_s_stride_n + at, dst);
             } else {
                 dma4(in && s_src[j] ? s_src[j] + at : (const char*)&b16::kZeroPiece, dst);
             }
@@ -170,14 +185,14 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
     aim();
     constexpr bool PIPED = C::MP >= 4;                 // a wave's MFMAs are worth the software pipeline
 #pragma unroll 1
-    for (int i = 0; i < S - 1; i++) produce();
+    for (int i = 0; i < (PIPED ? S : S - 1); i++) produce();
 
     CodeFrag fp, fq;
     const int wp = wave / C::WQ, wq = wave % C::WQ;
     fp.set(wp * C::MP, lane);
     fq.set(wq * C::MQ, lane);
-    Scales<C::MP> sp;
-    Scales<C::MQ> sq;
+    Scales<C::MP, C::ROLLED> sp;
+    Scales<C::MQ, C::ROLLED> sq;
     const uint32_t sp_at = chunk_at + scale_lane(wp * C::MP, lane), sq_at = chunk_at + C::BP * kChunk * kRowScales + scale_lane(wq * C::MQ, lane);
 
     int stage = 0;
@@ -213,24 +228,40 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
             }
             sp.read(sp_at, lane);
             sq.read(sq_at, lane);
+            if constexpr (!BUF) {
+                const int left = blocks - c * kChunk * kRowScales;
+                const uint32_t low = scale_mask(left, lane), high = scale_mask(left - 2 * kRowScales, lane);
+                sp.mask(low, high);
+                sq.mask(low, high);
+            }
             const int n_steps = min(kChunk, steps - c * kChunk);
-#pragma unroll 1
-            for (int u = 0; u < n_steps; u++) {
+            auto step = [&](auto number, int u) __attribute__((always_inline)) {
+                constexpr int U = decltype(number)::value;
                 const uint32_t at = lds + stage * C::CODES;
                 stage = stage + 1 == S ? 0 : stage + 1;
-                const uint32_t mask = BUF ? 0u : scale_mask(blocks - (c * kChunk + u) * kRowScales, lane);
-                sp.template step<!BUF>(u, mask);
-                sq.template step<!BUF>(u, mask);
                 if constexpr (PIPED) {
                     if (u == 1) request_scales();
-                    step_pipelined<C>(acc, f, fp, fq, sp, sq, at, lds + stage * C::CODES, part);
+                    step_pipelined<C, U>(acc, f, fp, fq, sp, sq, at, lds + stage * C::CODES, part);
                     advance();
                 } else {
                     if (u > 0) arrive<S, LPS>();
                     if (u == 1) request_scales();
                     produce();                         // into the stage that the step before this one read
-                    step_plain<C>(acc, fp, fq, sp, sq, at);
+                    step_plain<C, U>(acc, fp, fq, sp, sq, at);
                 }
+            };
+            if constexpr (C::ROLLED) {
+#pragma unroll 1
+                for (int u = 0; u < n_steps; u++) {
+                    sp.take(u);
+                    sq.take(u);
+                    step(std::integral_constant<int, 0>{}, u);
+                }
+            } else {
+                step(std::integral_constant<int, 0>{}, 0);
+                if (n_steps > 1) step(std::integral_constant<int, 1>{}, 1);
+                if (n_steps > 2) step(std::integral_constant<int, 2>{}, 2);
+                if (n_steps > 3) step(std::integral_constant<int, 3>{}, 3);
             }
             before = n_steps;
             c = c + 1 == chunks ? 0 : c + 1;
@@ -285,8 +316,9 @@ int launch_form(hipStream_t st, GemmArgs g) {
 template <class C, bool FUSED>
 int launch_cfg(hipStream_t st, const GemmArgs& g) {
     const int64_t bank = (FUSED ? 2 : 1) * g.N, scales = g.K / kGroup;
+    // (a tile may name up to BQ rows of W past the bank's last, whose offsets still have to stay below kNowhere)
     const bool buf = g.K % 128 == 0 && std::max({(g.a_n - 1) * g.a_stride + g.K / 2, (g.a_n - 1) * g.a_s_stride + scales,
-                                                 (bank - 1) * g.w_stride_n + g.K / 2, (bank - 1) * g.w_s_stride_n + scales}) < (int64_t)kNowhere;
+                                                 (bank + C::BQ) * g.w_stride_n, (bank + C::BQ) * g.w_s_stride_n}) < (int64_t)kNowhere;
     return buf ? launch_form<C, FUSED, true>(st, g) : launch_form<C, FUSED, false>(st, g);
 }
 

@@ -38,6 +38,7 @@ constexpr int kStepK = 256;                   // k per ring stage
 constexpr int kRowBytes = kStepK / 2;
 constexpr int kRowScales = kStepK / kGroup;
 constexpr int kChunk = 4;                     // steps whose scales are loaded at once
+constexpr int kAhead = 2;                     // groups ahead of its MFMAs that a P fragment is read (step_pipelined)
 
 // BP x BQ tile, WP x WQ waves, S ring stages, WGS workgroups resident on a CU.
 template <int BP_, int BQ_, int WP_, int WQ_, int S_, int WGS_>
@@ -48,10 +49,12 @@ struct Cfg {
     static constexpr int WAVES_PER_EU = NW * WGS_ / 4 > 0 ? NW * WGS_ / 4 : 1;
     static constexpr int CODES = (BP + BQ) * kRowBytes;
     static constexpr int CHUNK = (BP + BQ) * kChunk * kRowScales;            // bytes of a chunk of scales
-    static constexpr int P_LOADS = BP / 8 / NW, Q_LOADS = BQ / 8 / NW;       // 16-byte DMAs of a wave and step
+    static constexpr int P_LOADS = BP / 8 / NW, Q_LOADS = BQ / 8 / NW;       // 16-byte DMAs of a wave and step, eight rows each; a chunk takes as many of 4 bytes
     static constexpr int LOADS = P_LOADS + Q_LOADS;
-    static constexpr int S_LOADS = (BP + BQ) / 8 / NW;                       // 4-byte DMAs of a wave and chunk, eight rows each
-    static constexpr int PER = (LOADS + 2 * MP - 3) / (2 * MP - 2) > 1 ? 2 : 1;   // loads of a group of the pipelined step
+    // One step's code for all of a chunk: with a chunk's four written out, which takes the scales where they are, the largest
+    // tile needs more than its 256 registers (385 us instead of 291 for 8 x 2048 rows to 4096 columns of 8192); the others gain
+    // (128 x 256: 250 -> 236 us for 256 x 96 rows to 2 x 1024 of 4096).
+    static constexpr bool ROLLED = MP > 4;
     static_assert(NW % 2 == 0 && BP % 32 == 0 && BQ % 32 == 0 && (BP / 8) % NW == 0 && (BQ / 8) % NW == 0, "waves cover the rows evenly");
 };
 
@@ -104,36 +107,42 @@ __device__ __forceinline__ uint32_t scale_lane(int sub0, int lane) {
     return (uint32_t)((sub0 * 16 + (lane & 15)) * (kChunk * kRowScales) + (lane >> 5) * (kChunk * 4));
 }
 
-// The scales of M sub-tiles' rows: of a chunk, two steps a word (the lane's pairs, of blocks 2q and 2q + 1), and of the step in
-// the low half of `now`.
-template <int M>
+// The scales of M sub-tiles' rows of a chunk, two steps a word: the lane's pairs, of blocks 2q and 2q + 1.  MFMA ks of step u
+// takes byte 2 (u & 1) + ks of its word, or (ROLLED: one step's code serves all) ks of `now`.
+template <int M, bool ROLLED>
 struct Scales {
-    uint32_t first[M], second[M], now[M];                   // steps 0 and 1, steps 2 and 3
+    uint32_t pair[2][M], now[ROLLED ? M : 1];
+    __device__ __forceinline__ void take(int u) {
+        const int shift = (u & 1) * 16;
+        const uint32_t late = u & 2 ? ~0u : 0u;        // (by bits: a choice between the arrays would put them into memory)
+#pragma unroll
+        for (int m = 0; m < (ROLLED ? M : 0); m++) now[m] = ((pair[1][m] & late) | (pair[0][m] & ~late)) >> shift;
+    }
+    template <int U>
+    __device__ __forceinline__ uint32_t word(int m) const { return ROLLED ? now[ROLLED ? m : 0] : pair[U / 2][m]; }
     __device__ __forceinline__ void read(uint32_t at, int lane) {
         const uint32_t sel = (lane >> 4) & 1 ? 0x07060302u : 0x05040100u;      // the quarter's half of either word
 #pragma unroll
         for (int m = 0; m < M; m++) {
             const v4i w = *(const MOE_LDS v4i*)(uintptr_t)(at + m * 16 * kChunk * kRowScales);
-            first[m] = __builtin_amdgcn_perm((uint32_t)w[1], (uint32_t)w[0], sel);
-            second[m] = __builtin_amdgcn_perm((uint32_t)w[3], (uint32_t)w[2], sel);
+            pair[0][m] = __builtin_amdgcn_perm((uint32_t)w[1], (uint32_t)w[0], sel);
+            pair[1][m] = __builtin_amdgcn_perm((uint32_t)w[3], (uint32_t)w[2], sel);
         }
     }
-    template <bool MASKED>
-    __device__ __forceinline__ void step(int u, uint32_t mask) {
-        const int shift = (u & 1) * 16;
-        const uint32_t late = u & 2 ? ~0u : 0u;        // (by bits: a choice between the arrays would put them into memory)
+    __device__ __forceinline__ void mask(uint32_t low, uint32_t high) {
 #pragma unroll
         for (int m = 0; m < M; m++) {
-            now[m] = ((second[m] & late) | (first[m] & ~late)) >> shift;
-            if constexpr (MASKED) now[m] &= mask;
+            pair[0][m] &= low;
+            pair[1][m] &= high;
         }
     }
 };
 
-// Which of the lane's two scales lie before the end of k, `left` blocks on from the stage's first.
+// Which of the lane's two scales of two steps lie before the end of k, `left` blocks on from the first one's start.
 __device__ __forceinline__ uint32_t scale_mask(int left, int lane) {
     const int b = 2 * (lane >> 4);
-    return (left > b ? 0xFFu : 0u) | (left > b + 1 ? 0xFF00u : 0u);
+    return (left > b ? 0xFFu : 0u) | (left > b + 1 ? 0xFF00u : 0u) | (left > kRowScales + b ? 0xFF0000u : 0u) |
+           (left > kRowScales + b + 1 ? 0xFF000000u : 0u);
 }
 
 template <int KS>
@@ -144,9 +153,9 @@ __device__ __forceinline__ v4f mfma(const v4i& a, uint32_t sa, const v4i& b, uin
 
 // One step of a wave's MP x MQ sub-tiles.  Q is the MFMA's row operand, so lane l holds of sub-tile (m, n) the element
 // p = 16m + l % 16, q = 16n + 4 (l / 16) + 0..3.
-template <class C>
-__device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeFrag& fp, const CodeFrag& fq, const Scales<C::MP>& sp,
-                                           const Scales<C::MQ>& sq, uint32_t at) {
+template <class C, int U>
+__device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeFrag& fp, const CodeFrag& fq, const Scales<C::MP, C::ROLLED>& sp,
+                                           const Scales<C::MQ, C::ROLLED>& sq, uint32_t at) {
     const uint32_t at_q = at + C::BP * kRowBytes;
 #pragma unroll
     for (int ks = 0; ks < 2; ks++) {
@@ -158,7 +167,8 @@ __device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeF
             const v4i p = fp.read(at, m, ks);
 #pragma unroll
             for (int n = 0; n < C::MQ; n++)
-                acc[m][n] = ks == 0 ? mfma<0>(q[n], sq.now[n], p, sp.now[m], acc[m][n]) : mfma<1>(q[n], sq.now[n], p, sp.now[m], acc[m][n]);
+                acc[m][n] = ks == 0 ? mfma<2 * (U & 1)>(q[n], sq.template word<U>(n), p, sp.template word<U>(m), acc[m][n])
+                                    : mfma<2 * (U & 1) + 1>(q[n], sq.template word<U>(n), p, sp.template word<U>(m), acc[m][n]);
         }
     }
 }
@@ -170,46 +180,53 @@ __device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeF
 // end: the compiler would sink the MFMAs past a branch, and the loads before it would go out all at once.
 template <class C>
 struct Frags {
-    v4i p[2], q[2][C::MQ];
+    v4i p[4], q[2][C::MQ];
     __device__ __forceinline__ void first(const CodeFrag& fp, const CodeFrag& fq, uint32_t at) {
 #pragma unroll
         for (int n = 0; n < C::MQ; n++) q[0][n] = fq.read(at + C::BP * kRowBytes, n, 0);
-        p[0] = fp.read(at, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) p[i] = fp.read(at, i, 0);
     }
 };
 
-template <class C, class Part>
+template <class C, int U, class Part>
 __device__ __forceinline__ void step_pipelined(v4f (&acc)[C::MP][C::MQ], Frags<C>& f, const CodeFrag& fp, const CodeFrag& fq,
-                                               const Scales<C::MP>& sp, const Scales<C::MQ>& sq, uint32_t at, uint32_t next,
+                                               const Scales<C::MP, C::ROLLED>& sp, const Scales<C::MQ, C::ROLLED>& sq, uint32_t at, uint32_t next,
                                                const Part& part) {
-    constexpr int MP = C::MP, MQ = C::MQ, G = 2 * MP, PARTS = C::LOADS, PER = C::PER;
-    static_assert((G - 2) * PER >= PARTS, "all loads of a step go out before the workgroup meets");
+    constexpr int MP = C::MP, MQ = C::MQ, G = 2 * MP, PARTS = C::LOADS, MEET = G - kAhead;
+    constexpr int PER = (PARTS + kAhead - 1) / kAhead;
     constexpr int Q1 = MP > MQ ? MP - 1 - MQ : 0;         // from this group on, one fragment of Q's second half each
-    static_assert(MP >= 4 && MP >= MQ, "Q's second half is read before its first group");
-    const uint32_t at_q = at + C::BP * kRowBytes;
+    constexpr int Q0 = (MQ + kAhead - 1) / kAhead;        // from the meeting on, fragments of the next stage's Q each
+    static_assert(MP >= 4 && MP >= MQ && kAhead < MP, "Q's second half is read before its first group");
+    const uint32_t at_q = at + C::BP * kRowBytes, next_q = next + C::BP * kRowBytes;
 #pragma unroll
     for (int i = 0; i < G; i++) {
         const int m = i % MP, ks = i / MP;
-        if (i == G - 1) {
+        if (i == MEET) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             arrive<C::S, PARTS>();
         }
 #pragma unroll
         for (int u = 0; u < PER; u++) {
-            const int j = i * PER + u;
-            if (j < PARTS) part(j);
+            const int j = (i - MEET) * PER + u;
+            if (j >= 0 && j < PARTS) part(j);
         }
-        if (i < G - 1) {
-            if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(at_q, i - Q1, 1);
-            f.p[(i + 1) % 2] = fp.read(at, (i + 1) % MP, (i + 1) / MP);
+        if (i >= Q1 && i - Q1 < MQ) f.q[1][i - Q1] = fq.read(at_q, i - Q1, 1);
+        if (i < MEET) {
+            f.p[(i + kAhead) % 4] = fp.read(at, (i + kAhead) % MP, (i + kAhead) / MP);
         } else {
-            f.first(fp, fq, next);
+#pragma unroll
+            for (int u = 0; u < Q0; u++) {
+                const int n = (i - MEET) * Q0 + u;
+                if (n < MQ) f.q[0][n] = fq.read(next_q, n, 0);
+            }
+            f.p[(i + kAhead) % 4] = fp.read(next, i - MEET, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < MQ; n++)
-            acc[m][n] = ks == 0 ? mfma<0>(f.q[0][n], sq.now[n], f.p[i % 2], sp.now[m], acc[m][n])
-                                : mfma<1>(f.q[1][n], sq.now[n], f.p[i % 2], sp.now[m], acc[m][n]);
+            acc[m][n] = ks == 0 ? mfma<2 * (U & 1)>(f.q[0][n], sq.template word<U>(n), f.p[i % 4], sp.template word<U>(m), acc[m][n])
+                                : mfma<2 * (U & 1) + 1>(f.q[1][n], sq.template word<U>(n), f.p[i % 4], sp.template word<U>(m), acc[m][n]);
         __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
