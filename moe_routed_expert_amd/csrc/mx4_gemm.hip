@@ -324,15 +324,15 @@ int launch_cfg(hipStream_t st, const GemmArgs& g) {
 
 // Which tile.  A round of tiles, one on every slot of the card, takes a step's time for each 256 of k and a time for its ends;
 // both in microseconds, fitted to 516 products timed with all five (1 to 256 experts of 1 to 4096 rows, even and dealt at
-// random; N x K from 512 x 2048 to 4096 x 8192).  The rule loses 1.4 % to the best tile on average and 37 % at most.  Two
-// sides: 8 x 256 rows to 4096 columns of 8192 take 51 us by 128 x 256 and 83 by 256 x 256, 128 x 512 rows 1661 and 1568;
-// 8 x 32 rows 30.5 by 64 x 64 and 45.7 by 128 x 256.
+// random; N x K from 512 x 2048 to 4096 x 8192).  The rule loses 1.2 % to the best tile on average and 43 % at most.  Two
+// sides: 8 x 256 rows to 4096 columns of 8192 take 49 us by 128 x 256 and 83 by 256 x 256, 128 x 512 rows 1378 and 1260;
+// 8 x 32 rows 29 by 64 x 64 and 42 by 128 x 256.
 struct TileCost {
     int bp, bq, slots;
     double step, ends;
 };
-constexpr TileCost kCosts[] = {{32, 64, 1024, 0.64, 4.6}, {64, 64, 512, 0.46, 2.3}, {64, 256, 256, 0.73, 3.6},
-                               {128, 256, 256, 0.85, 3.6}, {256, 256, 256, 1.41, 6.0}};
+constexpr TileCost kCosts[] = {{32, 64, 1024, 0.46, 6.4}, {64, 64, 512, 0.42, 2.2}, {64, 256, 256, 0.77, 1.6},
+                               {128, 256, 256, 0.95, 3.6}, {256, 256, 256, 1.75, 6.4}};
 
 int pick_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     const double E = (double)n_experts, R = (double)m_rows, steps = (double)ceil_div(K, kStepK);
@@ -342,9 +342,9 @@ int pick_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     for (int i = 0; i < 5; i++) {
         const TileCost& c = kCosts[i];
         const double x = R / used / c.bp;
-        const double per = n_experts == 1 ? std::ceil(x) : std::max(1.0, x + 0.25 * std::min(1.0, x));    // M tiles of one
+        const double per = n_experts == 1 ? std::ceil(x) : std::max(1.0, x + 0.33 * std::min(1.0, x));    // M tiles of one
         const double full = used * per * (double)ceil_div(N, c.bq) / c.slots;
-        const double rounds = 0.4 * std::ceil(full - 1e-9) + 0.6 * std::max(1.0, full);                   // (loads differ)
+        const double rounds = 0.5 * std::ceil(full - 1e-9) + 0.5 * std::max(1.0, full);                   // (loads differ)
         const double t = rounds * (steps * c.step + c.ends);
         if (i == 0 || t < least) {
             least = t;
