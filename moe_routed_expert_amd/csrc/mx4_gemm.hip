@@ -19,21 +19,14 @@ namespace moe {
 namespace mx4 {
 namespace {
 
+// A workgroup's tiles of `walk`: start, start + G, ... below `tiles`.
 // BUF: the operands are read as buffers (every extent below kNowhere bytes, K a multiple of 128: scale words are whole); else
 // by 64-bit addresses, with the last words' scales masked.
-template <class C, bool FUSED, bool BUF>
-__global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(const GemmArgs g) {
+template <class C, bool FUSED, bool BUF, class W>
+__device__ __forceinline__ void run_tiles(const GemmArgs& g, const W& walk, uint8_t* ring, int lane, int wave) {
     constexpr int S = C::S, LPS = C::LOADS;
     constexpr int COLS = FUSED ? C::BQ / 2 : C::BQ;    // output columns of a tile
     static_assert(C::MQ == 4, "a wave holds 32 gate and 32 up columns, or 64 columns");
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::CODES + C::CHUNK];
-    __shared__ int first_tile[kMaxExperts];
-
-    const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    Walk<C, COLS> walk(g, first_tile, reinterpret_cast<uint32_t*>(ring), tid, lane, wave);
-    if (walk.start >= walk.tiles) return;
-
     const uint32_t lds = lds_offset(ring), chunk_at = lds + S * C::CODES;
     const int steps = (int)((g.K + kStepK - 1) / kStepK), blocks = (int)(g.K / kGroup), words = (blocks + 3) / 4;
     const int chunks = (steps + kChunk - 1) / kChunk;
@@ -277,7 +270,33 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(c
     wait_loads<0>();                                   // no load may write LDS after the workgroup has left it
 }
 
-template <class C, bool FUSED, bool BUF>
+// The tiles of C, a round of one on every workgroup after the other.  HALF: a last round that would leave half of the card
+// idle or more is done by tiles of half the rows (C itself: it is not), each the only one of its workgroup.  16384 rows of
+// eight uneven experts, 1088 tiles for 256 workgroups, take 329 us to 4096 columns of 8192, 358 with whole tiles, and 295
+// where the rows make 1024 tiles.
+template <class C, class HALF, bool FUSED, bool BUF>
+__global__ void __launch_bounds__(C::THREADS, C::WAVES_PER_EU) mx4_gemm_kernel(const GemmArgs g) {
+    constexpr bool SPLIT = !std::is_same<C, HALF>::value;
+    static_assert(!SPLIT || (HALF::BP * 2 == C::BP && HALF::BQ == C::BQ && HALF::NW == C::NW), "a half has C's columns and waves");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS > HALF::LDS ? C::LDS : HALF::LDS];
+    __shared__ int first_tile[kMaxExperts];
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    Walk<C, FUSED ? C::BQ / 2 : C::BQ> walk(g, first_tile, reinterpret_cast<uint32_t*>(ring), tid, lane, wave);
+    const int rest = walk.tiles % walk.G;
+    const bool split = SPLIT && rest * 2 <= walk.G;
+    if (split) walk.tiles -= rest;
+    if (walk.start < walk.tiles) run_tiles<C, FUSED, BUF>(g, walk, ring, lane, wave);
+    if constexpr (SPLIT) {
+        if (!split || walk.start >= rest * 2) return;
+        block_barrier();                               // everyone has done with the ring
+        const Halves<HALF, decltype(walk)> halves{walk, walk.tiles, walk.start, rest * 2, walk.G};
+        if (halves.locate(walk.start, lane).rows > 0) run_tiles<HALF, FUSED, BUF>(g, halves, ring, lane, wave);
+    }
+}
+
+template <class C, class HALF, bool FUSED, bool BUF>
 int resident_blocks() {
     static std::atomic<int> cached[64];   // concurrent first calls may both fill it, with the same value
     int dev = 0;
@@ -285,7 +304,7 @@ int resident_blocks() {
     int c = cached[dev].load(std::memory_order_relaxed);
     if (c == 0) {
         int per_cu = 0, cus = 0;
-        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, mx4_gemm_kernel<C, FUSED, BUF>, C::THREADS, 0) != hipSuccess ||
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, (mx4_gemm_kernel<C, HALF, FUSED, BUF>), C::THREADS, 0) != hipSuccess ||
             hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
             return 0;
         c = per_cu * cus;
@@ -300,39 +319,40 @@ using Tile64 = Cfg<64, 256, 2, 4, 3, 1>;
 using Tile64x64 = Cfg<64, 64, 4, 1, 3, 2>;
 using Tile32x64 = Cfg<32, 64, 2, 1, 4, 2>;
 
-template <class C, bool FUSED, bool BUF>
+template <class C, class HALF, bool FUSED, bool BUF>
 int launch_form(hipStream_t st, GemmArgs g) {
     const int64_t n_tiles = ceil_div(g.N, FUSED ? C::BQ / 2 : C::BQ);
     const int64_t most = (g.m_rows / C::BP + std::min<int64_t>(g.n_experts, g.m_rows)) * n_tiles;
     if (most > 0x7FFFFFFF - (1 << 20)) return MOE_ERR_SHAPE;
-    int wgs = resident_blocks<C, FUSED, BUF>() / kXcds * kXcds;
+    int wgs = resident_blocks<C, HALF, FUSED, BUF>() / kXcds * kXcds;
     if (wgs < kXcds) return MOE_ERR_HIP;
     wgs = (int)std::min<int64_t>(wgs, ceil_div(most, kXcds) * kXcds);
     g.n_tiles = (int)n_tiles;
-    hipLaunchKernelGGL((mx4_gemm_kernel<C, FUSED, BUF>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
+    hipLaunchKernelGGL((mx4_gemm_kernel<C, HALF, FUSED, BUF>), dim3((unsigned)wgs), dim3(C::THREADS), 0, st, g);
     return launch_status();
 }
 
-template <class C, bool FUSED>
+template <class C, class HALF, bool FUSED>
 int launch_cfg(hipStream_t st, const GemmArgs& g) {
     const int64_t bank = (FUSED ? 2 : 1) * g.N, scales = g.K / kGroup;
     // (a tile may name up to BQ rows of W past the bank's last, whose offsets still have to stay below kNowhere)
     const bool buf = g.K % 128 == 0 && std::max({(g.a_n - 1) * g.a_stride + g.K / 2, (g.a_n - 1) * g.a_s_stride + scales,
                                                  (bank + C::BQ) * g.w_stride_n, (bank + C::BQ) * g.w_s_stride_n}) < (int64_t)kNowhere;
-    return buf ? launch_form<C, FUSED, true>(st, g) : launch_form<C, FUSED, false>(st, g);
+    return buf ? launch_form<C, HALF, FUSED, true>(st, g) : launch_form<C, HALF, FUSED, false>(st, g);
 }
 
 // Which tile.  A round of tiles, one on every slot of the card, takes a step's time for each 256 of k and a time for its ends;
 // both in microseconds, fitted to 516 products timed with all five (1 to 256 experts of 1 to 4096 rows, even and dealt at
-// random; N x K from 512 x 2048 to 4096 x 8192).  The rule loses 1.2 % to the best tile on average and 43 % at most.  Two
-// sides: 8 x 256 rows to 4096 columns of 8192 take 49 us by 128 x 256 and 83 by 256 x 256, 128 x 512 rows 1378 and 1260;
-// 8 x 32 rows 29 by 64 x 64 and 42 by 128 x 256.
+// random; N x K from 512 x 2048 to 4096 x 8192).  The rule loses 1.2 % to the best tile on average and 29 % at most.  Two
+// sides, to 4096 columns of 8192: 128 x 512 rows take 1408 us by 128 x 256 and 1302 by 256 x 256, 32 x 512 dealt at random
+// 390 and 395; 8 x 32 rows 31 by 64 x 64 and 43 by 128 x 256.
 struct TileCost {
     int bp, bq, slots;
     double step, ends;
 };
-constexpr TileCost kCosts[] = {{32, 64, 1024, 0.46, 6.4}, {64, 64, 512, 0.42, 2.2}, {64, 256, 256, 0.77, 1.6},
-                               {128, 256, 256, 0.95, 3.6}, {256, 256, 256, 1.75, 6.4}};
+constexpr TileCost kCosts[] = {{32, 64, 1024, 0.40, 6.8}, {64, 64, 512, 0.40, 2.5}, {64, 256, 256, 0.76, 1.6},
+                               {128, 256, 256, 0.96, 3.8}, {256, 256, 256, 1.74, 6.7}};
+constexpr int kFirstSplit = 3;                    // from this one on a last round of half the slots or fewer takes the tile before
 
 int pick_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     const double E = (double)n_experts, R = (double)m_rows, steps = (double)ceil_div(K, kStepK);
@@ -342,10 +362,12 @@ int pick_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
     for (int i = 0; i < 5; i++) {
         const TileCost& c = kCosts[i];
         const double x = R / used / c.bp;
-        const double per = n_experts == 1 ? std::ceil(x) : std::max(1.0, x + 0.33 * std::min(1.0, x));    // M tiles of one
-        const double full = used * per * (double)ceil_div(N, c.bq) / c.slots;
-        const double rounds = 0.5 * std::ceil(full - 1e-9) + 0.5 * std::max(1.0, full);                   // (loads differ)
-        const double t = rounds * (steps * c.step + c.ends);
+        const double per = n_experts == 1 ? std::ceil(x) : std::max(1.0, x + 0.32 * std::min(1.0, x));    // M tiles of one
+        const double rounds = used * per * (double)ceil_div(N, c.bq) / c.slots, whole = std::floor(rounds + 1e-9), part = rounds - whole;
+        auto cost = [&](int j) { return steps * kCosts[j].step + kCosts[j].ends; };
+        auto at_most = [&](double f) { return i >= kFirstSplit && f <= 0.5 ? cost(i - 1) : cost(i); };    // a round of f of the slots
+        const double even = whole * cost(i) + (part > 1e-9 ? at_most(part) : 0.0);
+        const double t = 0.42 * even + 0.58 * std::max(rounds * cost(i), at_most(rounds));                  // (loads differ)
         if (i == 0 || t < least) {
             least = t;
             best = i;
@@ -358,11 +380,11 @@ int pick_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K) {
 template <bool FUSED>
 int grouped_launch(hipStream_t st, const GemmArgs& g) {
     switch (pick_tile(g.m_rows, g.n_experts, FUSED ? 2 * g.N : g.N, g.K)) {
-        case 0: return launch_cfg<Tile32x64, FUSED>(st, g);
-        case 1: return launch_cfg<Tile64x64, FUSED>(st, g);
-        case 2: return launch_cfg<Tile64, FUSED>(st, g);
-        case 3: return launch_cfg<Tile128, FUSED>(st, g);
-        default: return launch_cfg<Tile256, FUSED>(st, g);
+        case 0: return launch_cfg<Tile32x64, Tile32x64, FUSED>(st, g);
+        case 1: return launch_cfg<Tile64x64, Tile64x64, FUSED>(st, g);
+        case 2: return launch_cfg<Tile64, Tile64, FUSED>(st, g);
+        case 3: return launch_cfg<Tile128, Tile64, FUSED>(st, g);
+        default: return launch_cfg<Tile256, Tile128, FUSED>(st, g);
     }
 }
 

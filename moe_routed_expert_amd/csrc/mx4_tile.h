@@ -49,6 +49,7 @@ struct Cfg {
     static constexpr int WAVES_PER_EU = NW * WGS_ / 4 > 0 ? NW * WGS_ / 4 : 1;
     static constexpr int CODES = (BP + BQ) * kRowBytes;
     static constexpr int CHUNK = (BP + BQ) * kChunk * kRowScales;            // bytes of a chunk of scales
+    static constexpr int LDS = S * CODES + CHUNK;
     static constexpr int P_LOADS = BP / 8 / NW, Q_LOADS = BQ / 8 / NW;       // 16-byte DMAs of a wave and step, eight rows each; a chunk takes as many of 4 bytes
     static constexpr int LOADS = P_LOADS + Q_LOADS;
     // One step's code for all of a chunk: with a chunk's four written out, which takes the scales where they are, the largest
@@ -385,6 +386,24 @@ struct Walk {
         const int c = min(ti.n0 + (r >> 6) * 32 + (r & 31), (int)g.N - 1);
         return c + (r & 32 ? g.N : 0);
     }
+};
+
+// The tiles of W from `first` on in halves of C::BP rows, the second of which may have none.
+template <class C, class W>
+struct Halves {
+    const W& whole;
+    int first, start, tiles, G;
+
+    __device__ __forceinline__ Tile locate(int t, int lane) const {
+        Tile ti = whole.locate(first + t / 2, lane);
+        const int past = (t & 1) * C::BP;
+        ti.row0 += past;
+        ti.rows = min(ti.rows - past, C::BP);
+        return ti;
+    }
+    __device__ __forceinline__ int64_t a_row(const Tile& ti, int r) const { return whole.a_row(ti, r); }
+    template <bool FUSED>
+    __device__ __forceinline__ int64_t w_row(const Tile& ti, int r) const { return whole.template w_row<FUSED>(ti, r); }
 };
 
 }  // namespace mx4

@@ -81,9 +81,32 @@ def test_every_tile():
         every_tile(*case)
 
 
-def every_tile(R, E, N, K):
+def last_round_cases():
+    """Of the large tiles: launches whose last round leaves less and more than half of the card idle, or is their only one."""
+    slots = torch.cuda.get_device_properties(0).multi_processor_count // 8 * 8
+    found = {}
+    for counts in [(700,), (2348, 1900), (3000,), (5000,), (1500, 1400, 700, 900), (6000, 2000), (4096, 300), (1290, 0, 130)]:
+        for N in (520, 1032, 2056, 4360, 6152, 8200):
+            for K in (544, 640):
+                bp, bq = m.mx4_grouped_tile(sum(counts), len(counts), N, K)
+                tiles = sum(-(-c // bp) for c in counts) * -(-N // bq)
+                what, work = (bp, K % 128, tiles > slots, 0 < tiles % slots * 2 <= slots), sum(counts) * N * K
+                if bp >= 128 and (what not in found or work < found[what][0]):
+                    found[what] = (work, (counts, N, K))
+    assert {(256, 0, True, True), (256, 0, True, False), (128, 0, True, True), (256, 32, True, True)} <= set(found) or slots != 256
+    return [case for _, case in found.values()]
+
+
+def test_last_rounds():
+    for counts, N, K in last_round_cases():
+        every_tile(sum(counts), len(counts), N, K, counts)
+        if N % 64 == 8:
+            fused_in_every_tile(sum(counts), len(counts), N, K, counts)
+
+
+def every_tile(R, E, N, K, counts=None):
     rng = np.random.default_rng(R)
-    counts = rng.multinomial(R, rng.dirichlet(np.ones(E)))
+    counts = rng.multinomial(R, rng.dirichlet(np.ones(E))) if counts is None else counts
     p = Problem(E, R, N, K)
     out = torch.empty((R, N), dtype=torch.float32, device=dev())
     print("mx4 tile", R, E, N, K, m.mx4_grouped_tile(R, E, N, K), flush=True)
@@ -264,9 +287,9 @@ def test_fused_in_every_tile():
         fused_in_every_tile(*case)
 
 
-def fused_in_every_tile(R, E, N, K):
+def fused_in_every_tile(R, E, N, K, counts=None):
     I = -(-N // 64) * 32
-    counts = np.random.default_rng(R).multinomial(R, np.ones(E) / E)
+    counts = np.random.default_rng(R).multinomial(R, np.ones(E) / E) if counts is None else counts
     p = Problem(E, R, 2 * I, K)
     offs = torch.from_numpy(offsets_of(counts)).to(dev())
     c1 = torch.empty((R, 2 * I), device=dev())
