@@ -3,14 +3,22 @@
 // are applied inside the MFMA, so the accumulators run through the whole reduction; its sums of 128 scaled products and
 // the accumulator were within 2^-23 of the sum of magnitudes, whatever the scales (checked on the device).
 //
-// A workgroup owns a BP x BQ tile and walks k in steps of 256 elements: 128 bytes of codes and 8 scale bytes a row.  Both
-// go from global memory straight into a stage of an LDS ring (S - 1 steps in flight): codes by 16-byte pieces as in
-// b16_tile.h, whose slot swizzle and waits are used here, scales by words.  A step is two MFMAs per pair of 16-row
-// sub-tiles.  Lane l of an MFMA holds row l % 16 and 32 k of its own, and any four blocks of 32 may meet in one MFMA as
-// long as both operands take the same ones: quarter q = l / 16 takes blocks 2q (first MFMA) and 2q + 1 (second), so its
-// two scales are one 16-bit word of the row's eight and the MFMA picks the byte (op_sel) - no shift, no unpacking.
-// Pieces past the end of k come from a page of zeros, and so do scale words wholly past it; the scale bytes of a word
-// that straddles the end are masked to 0, since a scale byte of 255 there would make a NaN of the zeros.
+// A workgroup owns a BP x BQ tile and walks k in steps of 256 elements, 128 bytes of codes a row, which go from global memory
+// straight into a stage of an LDS ring by 16-byte pieces.  A step is two MFMAs per pair of 16-row sub-tiles.  Lane l of an
+// MFMA holds row l % 16 and 32 k of its own, and any four blocks of 32 may meet in one MFMA as long as both operands take the
+// same ones: quarter q = l / 16 takes blocks 2q (first MFMA) and 2q + 1 (second), so its two scales are one 16-bit word of the
+// row's eight bytes and the MFMA picks the byte (op_sel) - no shift, no unpacking.
+// Scales are loaded for a chunk of four steps at a time, 32 bytes a row: a load costs the CU's address path a cycle per line
+// it touches, however little of it (with the scales of one step at a time a layer of 256 experts took 444 us instead of 405).
+// From LDS a chunk goes to registers, a pair of 16-bit words each.
+// Pieces past the end of k read as zeros, and so do scale words wholly past it; the scale bytes of a word that straddles the
+// end are masked to 0, since a scale byte of 255 there would make a NaN of the zeros.
+//
+// What bounds it (8 x 2048 rows to 4096 columns of 8192, 1.1 TFLOP): the MFMAs are busy in 42 % of the cycles at 295 us
+// (3.7 PFLOP/s) once the clock has come up; with operands of zeros 268, so 10 % is power.  Timed without the loads 243 (zeros):
+// of it 165 the steps, 30 the change of tiles, 22 each the epilogues and the chunks of scales.  Tried and not kept: four waves
+// of 128 x 128, which halve the reads of LDS but leave one wave a SIMD (398 us against 337), loads spread over all of a
+// step, reads three groups ahead (the same), lines asked for ahead of their loads (8 us more).
 #pragma once
 
 #include "b16_tile.h"
@@ -175,10 +183,12 @@ __device__ __forceinline__ void step_plain(v4f (&acc)[C::MP][C::MQ], const CodeF
 }
 
 // The same step as a software pipeline (b16::step_pipelined), for tiles whose MFMAs are the bound: 2 MP groups of MQ MFMAs,
-// each group's P fragment read while the group before it is multiplied; the workgroup meets before the last group, which
-// covers the first reads of the next stage; the loads of the stage that takes the last one's place are spread over the first
-// groups, PER each.  No branch lies within a step (the producer moves on between steps) and the accumulators are named at its
-// end: the compiler would sink the MFMAs past a branch, and the loads before it would go out all at once.
+// each group's P fragment read kAhead groups before.  Ahead of the last kAhead groups all of the stage is in registers and the
+// workgroup meets: the next stage has landed for every wave and this one is free, so these groups read the first fragments of
+// the next one and ask for the stage that takes this one's place (a step earlier than spread over the step to come: 250 ->
+// 235 us for 256 x 96 rows, with the chunks written out).  No branch lies within a step (the producer moves on between steps)
+// and the accumulators are named at its end: the compiler would sink the MFMAs past a branch, and the loads before it would go
+// out all at once.
 template <class C>
 struct Frags {
     v4i p[4], q[2][C::MQ];
