@@ -62,3 +62,30 @@ def test_large_biases(big):
     bias[::7] = big
     bias[5] = -big
     check(rng.standard_normal((21, 130)).astype(np.float32), 25, SIGMOID, bias)
+
+
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("masked", [0.0, 0.6])
+@pytest.mark.parametrize("T,E,topk,G,keep", [(30, 64, 8, 8, 3), (90, 256, 6, 8, 4), (20, 512, 8, 16, 5), (9, 1024, 9, 32, 7)])
+def test_groups_of_nearly_equal_sums(score, with_bias, masked, T, E, topk, G, keep):
+    """Groups in pairs that hold the same logits in another order, one of them off by an ulp or two or none; masked: groups of
+    one choosable expert too."""
+    rng = np.random.default_rng(E + T)
+    size = E // G
+    base = rng.standard_normal((T, G // 2, size)).astype(np.float32)
+    base[rng.random(base.shape) < masked] = -np.inf
+    b = rng.standard_normal((G // 2, size)).astype(np.float32) * 0.1
+    x, bias = np.empty((T, G, size), np.float32), np.empty((G, size), np.float32)
+    for p in range(G // 2):
+        order = rng.permutation(size)
+        x[:, 2 * p], bias[2 * p] = base[:, p], b[p]
+        x[:, 2 * p + 1], bias[2 * p + 1] = base[:, p][:, order], b[p][order]
+    off = rng.integers(-2, 3, T)
+    top = x[:, 1].argmax(axis=1)
+    for t in range(T):
+        v = x[t, 1, top[t]]
+        for _ in range(abs(off[t])):
+            v = np.nextafter(v, np.float32(np.inf if off[t] > 0 else -np.inf))
+        x[t, 1, top[t]] = v if np.isfinite(x[t, 1, top[t]]) else -np.inf
+    check(x.reshape(T, E), topk, score, bias.reshape(E) if with_bias else None, G, keep, 2)
