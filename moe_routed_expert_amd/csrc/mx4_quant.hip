@@ -2,7 +2,9 @@
 //
 // MI355X design: HBM-bound passes.  A lane owns 8 consecutive columns (16-byte loads of 2-byte types, 4 bytes of codes), 4
 // lanes share a group of 32 and its maximum (two DPP moves over the bits of |v|), and a wave covers 512 columns of a row.
-// The conversions to and from E2M1 are gfx950's, two elements an instruction with the scale applied inside.
+// The conversions to and from E2M1 are gfx950's, two elements an instruction with the scale applied inside.  24576 x 4096 bf16
+// take 48 us (5.3 TB/s; a copy reaches 4.6) and back 40 (6.4); fp32 10000 x 4096 34 and 29 (back 60 by eight columns a lane,
+// whose stores fill half a line each).
 #include <algorithm>
 
 #include "cols8.h"
@@ -33,6 +35,44 @@ __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
     return v > o ? v : o;
 }
 
+// Whole pieces of eight columns in rows that begin anywhere: the same wide accesses, which the memory takes at any byte; an
+// element at a time is left for a row's last piece.  (23977 rows of 1924 fp16 there and back: 130 us by elements, 80 so.)
+typedef uint32_t words4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t word_any __attribute__((aligned(1)));
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void* __restrict__ base, int64_t off, int valid, float (&v)[kCols]) {
+    if (!VEC && valid == kCols) {
+        const words4_any* p = reinterpret_cast<const words4_any*>((const char*)base + off * (DT == kF32 ? 4 : 2));
+        RawCols8<DT> r;
+#pragma unroll
+        for (int i = 0; i < (DT == kF32 ? 2 : 1); i++) {
+            const words4_any w = p[i];
+            r.w[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        r.get(v);
+    } else {
+        load_cols<DT, VEC>(base, off, valid, v);
+    }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void store8(void* __restrict__ base, int64_t off, int valid, const float (&v)[kCols]) {
+    if (!VEC && valid == kCols) {
+        words4_any* p = reinterpret_cast<words4_any*>((char*)base + off * (DT == kF32 ? 4 : 2));
+        if constexpr (DT == kF32) {
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                p[i] = words4_any{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                  __float_as_uint(v[4 * i + 3])};
+        } else {
+            p[0] = words4_any{pk16<DT>(v[0], v[1]), pk16<DT>(v[2], v[3]), pk16<DT>(v[4], v[5]), pk16<DT>(v[6], v[7])};
+        }
+    } else {
+        store_cols<DT, VEC>(base, off, valid, v);
+    }
+}
+
 // grid: (512-column segments, rows / waves per block); a wave takes rows blockIdx.y * 4 + wave, then on in strides.
 template <int DT, int ACT, bool VEC>
 __global__ void __launch_bounds__(64 * kWavesPerBlock) quant_kernel(const QuantArgs a) {
@@ -42,10 +82,10 @@ __global__ void __launch_bounds__(64 * kWavesPerBlock) quant_kernel(const QuantA
     for (int64_t r = (int64_t)blockIdx.y * kWavesPerBlock + wave; r < a.rows; r += (int64_t)gridDim.y * kWavesPerBlock) {
         float v[kCols] = {};
         if (valid > 0) {
-            load_cols<DT, VEC>(a.in, r * a.in_stride + c, valid, v);
+            load8<DT, VEC>(a.in, r * a.in_stride + c, valid, v);
             if constexpr (ACT != 0) {
                 float u[kCols];
-                load_cols<DT, VEC>(a.in, r * a.in_stride + a.n + c, valid, u);
+                load8<DT, VEC>(a.in, r * a.in_stride + a.n + c, valid, u);
 #pragma unroll
                 for (int i = 0; i < kCols; i++) v[i] = i < valid ? gated<ACT>(v[i], u[i]) : 0.0f;
             }
@@ -59,6 +99,8 @@ __global__ void __launch_bounds__(64 * kWavesPerBlock) quant_kernel(const QuantA
             uint8_t* q = a.q + r * a.q_stride + c / 2;
             if constexpr (VEC) {
                 *reinterpret_cast<uint32_t*>(q) = codes;
+            } else if (valid == kCols) {
+                *reinterpret_cast<word_any*>(q) = codes;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -81,6 +123,20 @@ struct DequantArgs {
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(64 * kWavesPerBlock) dequant_kernel(const DequantArgs a) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    if constexpr (VEC && DT == kF32) {           // whole lines a store: four columns a lane, two of such pieces
+        for (int64_t r = (int64_t)blockIdx.y * kWavesPerBlock + wave; r < a.rows; r += (int64_t)gridDim.y * kWavesPerBlock) {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t c = (int64_t)blockIdx.x * kWaveCols + h * (kWaveCols / 2) + lane * 4;
+                if (c >= a.n) continue;
+                const uint32_t w = *reinterpret_cast<const uint16_t*>(a.q + r * a.q_stride + c / 2);
+                const float s = scale_value(a.s[r * a.s_stride + c / kGroup]);
+                const v2f x0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), x1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
+                __builtin_nontemporal_store(v4f{x0[0], x0[1], x1[0], x1[1]}, reinterpret_cast<v4f*>((float*)a.out + r * a.out_stride + c));
+            }
+        }
+        return;
+    }
     const int64_t c = (int64_t)blockIdx.x * kWaveCols + lane * kCols;
     if (c >= a.n) return;
     const int valid = (int)(a.n - c < kCols ? a.n - c : kCols);
@@ -89,6 +145,8 @@ __global__ void __launch_bounds__(64 * kWavesPerBlock) dequant_kernel(const Dequ
         uint32_t w = 0;
         if constexpr (VEC) {
             w = *reinterpret_cast<const uint32_t*>(q);
+        } else if (valid == kCols) {
+            w = *reinterpret_cast<const word_any*>(q);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; i++)
@@ -100,7 +158,7 @@ __global__ void __launch_bounds__(64 * kWavesPerBlock) dequant_kernel(const Dequ
         const v2f x2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), x3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
         v[0] = x0[0]; v[1] = x0[1]; v[2] = x1[0]; v[3] = x1[1];
         v[4] = x2[0]; v[5] = x2[1]; v[6] = x3[0]; v[7] = x3[1];
-        store_cols<DT, VEC>(a.out, r * a.out_stride + c, valid, v);
+        store8<DT, VEC>(a.out, r * a.out_stride + c, valid, v);
     }
 }
 
