@@ -837,83 +837,83 @@ __global__ void __launch_bounds__(256) scan_kernel(const Args a) {
 // Chunk blockIdx.x's routes to their rows.
 template <bool SCANNED>
 __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const Args a) {
-    __shared__ int total[kMaxE], base[kMaxE];
+    static_assert(kScatterThreads >= kMaxE, "a thread an expert");
+    __shared__ int base[kMaxE];
     __shared__ uint64_t mask[kMaxE];
     __shared__ int sums[kScatterThreads / kWave];
     __shared__ uint4 sum4[SCANNED ? 1 : kScatterThreads];
-    const int rw = row_bytes(a.E), c = blockIdx.x;
+    const int rw = row_bytes(a.E), c = blockIdx.x, e = threadIdx.x;
     const int t0 = c * a.chunk, n_tok = min(a.chunk, a.T - t0), n = n_tok * a.topk;
     const int32_t* ids = a.ids + (int64_t)t0 * a.topk;
-    for (int e = threadIdx.x; e < a.E; e += kScatterThreads) {
-        if constexpr (SCANNED) {
-            total[e] = a.before[(int64_t)a.nc * rw + e];
-            base[e] = a.before[(int64_t)c * rw + e];
+    const int id0 = (int)threadIdx.x < n ? ids[threadIdx.x] : -1;      // asked for before the counts
+    mask[e] = 0ull;
+    int all = 0, early = 0;                            // expert e's routes, and those of the chunks before this one
+    if constexpr (SCANNED) {
+        if (e < a.E) {
+            all = a.before[(int64_t)a.nc * rw + e];
+            early = a.before[(int64_t)c * rw + e];
         }
-        mask[e] = 0ull;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kScatterThreads) {
-        const int e = ids[i];
-        if (e >= 0) atomicOr((unsigned long long*)&mask[e], 1ull << (i / a.topk));
-    }
-    if constexpr (!SCANNED) {
-        // Four experts a thread (a word of a chunk's counts), the chunks dealt over the parts of the workgroup; sums of bytes as
-        // 16-bit pairs (at most 512 chunks of at most 64 tokens), added up over the parts through LDS.
+        __syncthreads();
+    } else {
+        // Four experts a thread (a word of a chunk's counts), the chunks dealt over the parts of the workgroup, kAsk of them asked
+        // for at once; sums of bytes as 16-bit pairs (at most 512 chunks of 16 tokens), added up over the parts through LDS.
+        constexpr int kAsk = 16;
         const int quads = rw / 4, parts = kScatterThreads / quads;
-        const int qd = threadIdx.x % quads, part = threadIdx.x / quads;
+        const int part = threadIdx.x / quads, qd = threadIdx.x - part * quads;
         uint32_t even = 0, odd = 0, even_b = 0, odd_b = 0;
         if (part < parts) {
-#pragma unroll 16
-            for (int cc = part; cc < a.nc; cc += parts) {
-                const uint32_t v = *reinterpret_cast<const uint32_t*>(a.counts + (int64_t)cc * rw + qd * 4);
-                const uint32_t early = cc < c ? 0x00FF00FFu : 0u;
-                even += v & 0x00FF00FFu;
-                odd += v >> 8 & 0x00FF00FFu;
-                even_b += v & early;
-                odd_b += v >> 8 & early;
+            const uint8_t* counts = a.counts + qd * 4;
+            for (int c0 = part; c0 < a.nc; c0 += kAsk * parts) {
+                uint32_t w[kAsk];
+#pragma unroll
+                for (int k = 0; k < kAsk; k++) w[k] = *reinterpret_cast<const uint32_t*>(counts + (int64_t)min(c0 + k * parts, a.nc - 1) * rw);
+#pragma unroll
+                for (int k = 0; k < kAsk; k++) {
+                    const int cc = c0 + k * parts;
+                    const uint32_t v = cc < a.nc ? w[k] : 0u, before = cc < c ? v : 0u;
+                    even += v & 0x00FF00FFu;
+                    odd += v >> 8 & 0x00FF00FFu;
+                    even_b += before & 0x00FF00FFu;
+                    odd_b += before >> 8 & 0x00FF00FFu;
+                }
             }
             sum4[threadIdx.x] = make_uint4(even, odd, even_b, odd_b);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += kScatterThreads) {
+        if (e < a.E) {
             const int sh = (e & 2) * 8;
-            int all = 0, early = 0;
             for (int p = 0; p < parts; p++) {
                 const uint4 v = sum4[p * quads + e / 4];
                 all += (e & 1 ? v.y : v.x) >> sh & 0xFFFFu;
                 early += (e & 1 ? v.w : v.z) >> sh & 0xFFFFu;
             }
-            total[e] = all;
-            base[e] = early;
         }
     }
+    auto mark = [&](int i, int id) {
+        if (id >= 0) atomicOr((unsigned long long*)&mask[id], 1ull << (i / a.topk));
+    };
+    mark(threadIdx.x, id0);
+    for (int i = threadIdx.x + kScatterThreads; i < n; i += kScatterThreads) mark(i, ids[i]);
+    int run;
+    const int at = block_scan<kScatterThreads>(all, sums, run);
+    base[e] = early + at;
+    if (c == 0 && e < a.E) a.offsets[e] = at;
+    if (c == 0 && e == 0) a.offsets[a.E] = run;
     __syncthreads();
-    int run = 0;
-    for (int e0 = 0; e0 < a.E; e0 += kScatterThreads) {
-        const int e = e0 + threadIdx.x;
-        const int mine = e < a.E ? total[e] : 0;
-        int sum;
-        const int at = run + block_scan<kScatterThreads>(mine, sums, sum);
-        if (e < a.E) {
-            base[e] += at;
-            if (c == 0) a.offsets[e] = at;
-        }
-        run += sum;
-    }
-    if (c == 0 && threadIdx.x == 0) a.offsets[a.E] = run;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kScatterThreads) {
-        const int tt = i / a.topk, e = ids[i];
+    auto place = [&](int i, int id) {
+        const int tt = i / a.topk;
         int row = -1;
-        if (e >= 0) {
-            row = base[e] + __popcll(mask[e] & ((1ull << tt) - 1ull));
+        if (id >= 0) {
+            row = base[id] + __popcll(mask[id] & ((1ull << tt) - 1ull));
             a.dst2src[row] = t0 + tt;
         }
         a.route_rows[(int64_t)t0 * a.topk + i] = row;
-    }
+    };
+    if ((int)threadIdx.x < n) place(threadIdx.x, id0);
+    for (int i = threadIdx.x + kScatterThreads; i < n; i += kScatterThreads) place(i, ids[i]);
     // the rows behind the last route name no token
-    const int64_t all = (int64_t)a.T * a.topk;
-    for (int64_t i = run + (int64_t)c * kScatterThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kScatterThreads)
+    const int64_t routes = (int64_t)a.T * a.topk;
+    for (int64_t i = run + (int64_t)c * kScatterThreads + threadIdx.x; i < routes; i += (int64_t)gridDim.x * kScatterThreads)
         a.dst2src[i] = -1;
 }
 

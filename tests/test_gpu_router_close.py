@@ -3,6 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+import moe_routed_expert_amd as m
+from gpu_util import dev
+
 from test_gpu_router import SIGMOID, SOFTMAX, check
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +92,17 @@ def test_groups_of_nearly_equal_sums(score, with_bias, masked, T, E, topk, G, ke
             v = np.nextafter(v, np.float32(np.inf if off[t] > 0 else -np.inf))
         x[t, 1, top[t]] = v if np.isfinite(x[t, 1, top[t]]) else -np.inf
     check(x.reshape(T, E), topk, score, bias.reshape(E) if with_bias else None, G, keep, 2)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace (allocated by the call), many tokens and few."""
+    rng = np.random.default_rng(5)
+    xs = [torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev()) for s in ((5000, 200), (9000, 300), (64, 64), (700, 1000))]
+    want = [m.router(x, 5) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [m.router(x, 5, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g[:5], w[:5]))
