@@ -10,7 +10,7 @@
 //    value, ties to the lower index".  Without a bias the order is the logits' own, which needs no exponential.  With one (or
 //    with group values that are sums) scores have to be formed in 64 bits, for in 32 about one token in ten thousand has two
 //    choices next to each other that round to the wrong order; but 64-bit exponentials and 64-bit keys for every expert took
-//    86 us where this takes 45 (16384 tokens, 512 experts).  So keys are 32 bits: 22-bit steps over the token's own range, formed
+//    86 us where this takes 39 (16384 tokens, 512 experts).  So keys are 32 bits: 22-bit steps over the token's own range, formed
 //    with 32-bit scores whose error is known in steps.  Where two keys that matter are closer than that, the candidates alone
 //    are ranked again in 64 bits: of experts (refine, one token in a hundred) or groups (exact_groups, one in ten thousand).
 //    What even that leaves open is ranked as a whole (rank_exact).  16-bit logits fit a key as they are.
@@ -21,8 +21,8 @@
 //    counts of all chunks (bytes) for the experts' offsets and of the chunks before its own for its rows.  With more than
 //    kSumChunks chunks those sums come from a scan launched between.
 //  * Bound by instruction issue and the latency of the rounds, not by bytes: 4096 tokens of 256 fp32 logits in 8 groups with
-//    maps take 19.8 us in two launches (770 vector instructions a token), 16384 of 512 bf16 ones with their scores 45.2 us in
-//    two (50 MB: 1.2 TB/s), eight of 64 experts 7.6 us, which is the call.
+//    maps take 20 us in two launches, 16.2 in a graph (790 vector instructions a token), 16384 of 512 bf16 ones with their scores 39 us in
+//    two (50 MB: 1.3 TB/s), eight of 64 experts 7.6 us, which is the call.
 #include <algorithm>
 #include <type_traits>
 
