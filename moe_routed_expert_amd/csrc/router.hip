@@ -16,13 +16,13 @@
 //    What even that leaves open is ranked as a whole (rank_exact).  16-bit logits fit a key as they are.
 //  * Up to 64 experts a token takes 16 lanes of a wave, beyond a whole wave; lanes hold experts lane, lane + LPT, ... .
 //    Every round's largest key is found by lane moves folded into the maximum, then struck out.
-//  * A workgroup takes 16 tokens at a time and counts its routes in LDS, the chunk's loads.  Up to 64 tokens one workgroup
-//    does everything, maps included, in one launch.  Beyond, a second launch scatters: each of its workgroups adds up the
-//    counts of all chunks (bytes) for the experts' offsets and of the chunks before its own for its rows.  With more than
-//    kSumChunks chunks those sums come from a scan launched between.
+//  * A workgroup takes 16 tokens at a time and counts its routes in LDS, the chunk's loads.  Up to 64 tokens (32 of more than
+//    64 experts) one workgroup does everything, maps included, in one launch.  Beyond, a second launch scatters: each of its
+//    workgroups adds up the counts of all chunks (bytes) for the experts' offsets and of the chunks before its own for its
+//    rows.  With more than kSumChunks chunks those sums come from a scan launched between.
 //  * Bound by instruction issue and the latency of the rounds, not by bytes: 4096 tokens of 256 fp32 logits in 8 groups with
-//    maps take 20 us in two launches, 16.2 in a graph (790 vector instructions a token), 16384 of 512 bf16 ones with their scores 39 us in
-//    two (50 MB: 1.3 TB/s), eight of 64 experts 7.6 us, which is the call.
+//    maps take 20 us in two launches, 16.2 in a graph (790 vector instructions a token), 16384 of 512 bf16 ones with their
+//    scores 39 us in two (50 MB: 1.3 TB/s), eight of 64 experts 7.3 us, which is the call (5.9 in a graph).
 #include <algorithm>
 #include <type_traits>
 
@@ -38,7 +38,8 @@ constexpr int kMaxTopk = 64;
 constexpr int kMaxGroups = 64;
 constexpr int kTok = 16;                        // tokens of a workgroup at one time (TOK: of the only one, where a token takes 16 lanes)
 constexpr int kWaves = 16;                      // of a workgroup at most
-constexpr int kSingle = 64;                     // tokens that one workgroup routes alone
+constexpr int kSingle = 64;                     // tokens that one workgroup routes alone, with up to 64 experts
+constexpr int kSingleWide = 32;                 // with more, a wave a token
 constexpr int kSumChunks = 512;                 // chunks whose counts every scattering workgroup adds up itself
 constexpr int kScatterThreads = 1024;
 constexpr int64_t kMaxT = 1 << 27;              // a chunk of 64 tokens is 1024 threads of a grid, which fit 32 bits
@@ -684,7 +685,7 @@ __device__ __forceinline__ int block_scan(int v, int* lds, int& total) {
     return base + x - v;
 }
 
-// SINGLE: one workgroup, T <= kSingle, maps too.  Else chunk blockIdx.x, whose counts are written when maps are wanted.
+// SINGLE: one workgroup, maps too.  Else chunk blockIdx.x, whose counts are written when maps are wanted.
 template <int LPT, int VPL, bool WIDE, bool SOFT, bool GROUPS, bool SINGLE, int TOK>
 __global__ void __launch_bounds__((TOK * LPT)) route_kernel(const Args a) {
     constexpr int THREADS = TOK * LPT;
@@ -922,7 +923,10 @@ __global__ void zero_offsets_kernel(int E, int32_t* offsets) {
     for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = 0;
 }
 
-int chunk_of(int64_t T) { return T <= kSingle ? kSingle : T <= (int64_t)kTok * kSumChunks ? kTok : 64; }
+// One workgroup, one launch.  (256 experts in 8 groups, in a graph: 64 tokens 29 us so and 13.6 in two launches of more, 32
+// tokens 16.8 and 13.5, 16 tokens 10.6; outside of one the second launch costs the caller 4 us.)
+bool single(int64_t T, int64_t E) { return T <= (E <= 64 ? kSingle : kSingleWide); }
+int chunk_of(int64_t T, int64_t E) { return single(T, E) ? kSingle : T <= (int64_t)kTok * kSumChunks ? kTok : 64; }
 
 template <int LPT, int VPL, bool WIDE, bool SOFT, bool GROUPS>
 void launch_route(hipStream_t st, const Args& a) {
@@ -931,7 +935,7 @@ void launch_route(hipStream_t st, const Args& a) {
                            dim3(decltype(tok)::value * LPT), 0, st, a);
     };
     constexpr std::integral_constant<int, kTok> some{};
-    if (a.T > kSingle) return launch(std::false_type{}, some, a.nc);
+    if (!single(a.T, a.E)) return launch(std::false_type{}, some, a.nc);
     // (64 tokens of 64 experts in 8 groups: 14.6 us all at once, 25.3 by sixteens; 8 tokens 6.6 and 5.9)
     if constexpr (LPT == 16) {
         if (a.T > kTok) return launch(std::true_type{}, std::integral_constant<int, kSingle>{}, 1);
@@ -1106,8 +1110,8 @@ bool natural(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % (d
 using namespace moe;
 
 extern "C" size_t moe_router_workspace_size(int64_t T, int64_t E) {
-    if (T <= router::kSingle || T > router::kMaxT || E < 1 || E > router::kMaxE) return 0;
-    const int64_t nc = ceil_div(T, router::chunk_of(T)), rw = router::row_bytes((int)E);
+    if (T > router::kMaxT || E < 1 || E > router::kMaxE || router::single(T, E)) return 0;
+    const int64_t nc = ceil_div(T, router::chunk_of(T, E)), rw = router::row_bytes((int)E);
     const int64_t bytes = nc * rw + (nc > router::kSumChunks ? (nc + 1) * rw * 4 : 0);
     return (size_t)ceil_div(bytes, 256) * 256;
 }
@@ -1138,9 +1142,9 @@ extern "C" int moe_router(const void* logits, int dt, int64_t logits_stride, int
     a.n_group = topk_group < n_group ? (int)n_group : 1;
     a.keep = (int)topk_group; a.group_top = group_top; a.renorm = renorm; a.scale = scale;
     a.ids = expert_ids; a.weights = weights; a.scores = scores; a.dst2src = dst2src; a.route_rows = route_rows; a.offsets = expert_offsets;
-    a.chunk = router::chunk_of(T);
+    a.chunk = router::chunk_of(T, E);
     a.nc = (int)ceil_div(T, a.chunk);
-    if (maps && T > router::kSingle) {
+    if (maps && !router::single(T, E)) {
         if (!workspace) return MOE_ERR_NULL;
         if (ws_bytes < moe_router_workspace_size(T, E)) return MOE_ERR_WORKSPACE;
         if (!aligned16(workspace)) return MOE_ERR_ALIGN;
@@ -1149,7 +1153,7 @@ extern "C" int moe_router(const void* logits, int dt, int64_t logits_stride, int
     }
     if (bias || (a.n_group > 1 && group_top == 2)) router::launch_route_score<true>(st, a);
     else router::launch_route_score<false>(st, a);
-    if (maps && T > router::kSingle) {
+    if (maps && !router::single(T, E)) {
         const dim3 grid((unsigned)a.nc), block(router::kScatterThreads);
         if (a.nc > router::kSumChunks) {
             hipLaunchKernelGGL(router::scan_kernel, dim3((unsigned)ceil_div(router::row_bytes((int)E), 4 * kWave)), dim3(256), 0, st, a);
