@@ -643,7 +643,8 @@ int moe_router(const void* logits, int dt, int64_t logits_stride, int64_t T, int
  *     not renorm:       u[e_j] += scale dw_j
  *   and u[e] += dscores[t, e] unless dscores is NULL; then dl[e] += s_e (u_e - sum_i s_i u_i) (softmax) or
  *   u_e s_e (1 - s_e) (sigmoid).  Masked experts' entries are +0.  bias and groups choose, they have no gradient.
- *   logits as moe_router's;  expert_ids, weights, dweights [T][topk];  dscores fp32 [T][dscores_stride], stride 0: one
+ *   logits as moe_router's;  expert_ids, weights [T][topk] as it wrote them for these logits (an id named twice counts twice),
+ *   dweights [T][topk];  dscores fp32 [T][dscores_stride], stride 0: one
  *   row for all tokens (an auxiliary loss on the batch's mean scores);  dlogits [T][dlogits_stride] of dt, E written.
  *   score, renorm, scale as in the forward call.  fp32 inside.  T == 0 launches nothing.
  */

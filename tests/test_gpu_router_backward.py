@@ -115,6 +115,19 @@ def test_ids_outside_are_left_out():
             assert (np.abs(got - ref) <= (REL + 2.0 ** -24) * mag + 2.0 ** -120).all()
 
 
+def test_an_id_named_twice_counts_twice():
+    for score in (SOFTMAX, SIGMOID):
+        for renorm in (True, False):
+            for aux in ("none", "full"):
+                x, ids, w, dw, ds = case(20, 70, 4, 2, "fp32", score, renorm, 1.5, aux, masked=False)
+                ids = ids.clone()
+                ids[:, 2] = ids[:, 0]
+                ids[7] = ids[7, 1]
+                got = run(x, ids, w, dw, ds, score, renorm, 1.5).cpu().double().numpy()
+                ref, mag = reference(x.double().numpy(), ids.cpu().numpy(), w.cpu().double().numpy(), dw.cpu().double().numpy(), ds, score, renorm, 1.5)
+                assert (np.abs(got - ref) <= (REL + 2.0 ** -24) * mag + 2.0 ** -120).all()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_strides(dt):
     x, ids, w, dw, ds = case(11, 50, 4, 2, dt, SOFTMAX, False, 1.0, "full")
