@@ -15,6 +15,7 @@ from __future__ import annotations
 import collections
 import ctypes
 import os
+from contextlib import nullcontext
 
 import torch
 
@@ -585,7 +586,7 @@ def router(logits, topk, *, score=MOE_SCORE_SOFTMAX, bias=None, n_group=1, topk_
     assert l_1 == 1 or E == 1, _UNIT
     size = router_workspace_size(T, E)
     if out is None or (workspace is None and size):
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(logits.device)):
+        with nullcontext() if stream is None else torch.cuda.stream(stream):    # (the device's current stream owns it otherwise)
             if out is None:
                 new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)  # noqa: E731
                 out = (new((T, topk), _I32T), new((T, topk), _F32)) + (
