@@ -21,7 +21,7 @@
 //    workgroups adds up the counts of all chunks (bytes) for the experts' offsets and of the chunks before its own for its
 //    rows.  With more than kSumChunks chunks those sums come from a scan launched between.
 //  * Bound by instruction issue and the latency of the rounds, not by bytes: 4096 tokens of 256 fp32 logits in 8 groups with
-//    maps take 20 us in two launches, 16.2 in a graph (790 vector instructions a token), 16384 of 512 bf16 ones with their
+//    maps take 16.4 us in two launches (790 vector instructions a token), 16384 of 512 bf16 ones with their
 //    scores 39 us in two (50 MB: 1.3 TB/s), eight of 64 experts 7.3 us, which is the call (5.9 in a graph).
 #include <algorithm>
 #include <type_traits>
