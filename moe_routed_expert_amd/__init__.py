@@ -678,7 +678,8 @@ def mx4_dequant(q, s, out, stream=None):
 
 def _mx4_operands(a_q, a_s, w_q, w_s, mode, expert_offsets, slot_ids, a_rows, rows, a_row_div, N):
     """The operand arguments that both MXFP4 products take, checked; N: output columns (the bank holds N or 2N rows)."""
-    E, _, k2 = w_q.shape
+    bank = w_q.shape
+    E, _, k2 = bank
     w_e, w_r, w_1 = w_q.stride()
     v_e, v_r, v_1 = w_s.stride()
     a_n, a_cols = a_q.shape
@@ -687,21 +688,24 @@ def _mx4_operands(a_q, a_s, w_q, w_s, mode, expert_offsets, slot_ids, a_rows, ro
     groups = k2 // 16
     assert a_q.dtype is _U8 and a_s.dtype is _U8 and w_q.dtype is _U8 and w_s.dtype is _U8, "codes and scales are uint8"
     assert k2 % 16 == 0, "whole groups of 32 expected"
-    assert a_cols == k2 and a_s.shape == (a_n, groups) and w_s.shape == (E, w_q.shape[1], groups), "operands do not match"
+    assert a_cols == k2 and a_s.shape == (a_n, groups) and w_s.shape == (E, bank[1], groups), "operands do not match"
     assert w_1 == 1 and a_1 == 1 and ((s_1 == 1 and v_1 == 1) or groups == 1), _UNIT
     if groups % 4:                      # the kernels read a scale row to its next multiple of four bytes
         for t in (a_s, w_s):
             last = t.storage_offset() + sum((n - 1) * st for n, st in zip(t.shape[:-1], t.stride()[:-1])) + (groups + 3) // 4 * 4
             assert not t.numel() or last <= t.untyped_storage().nbytes(), "scale rows padded to a multiple of four bytes expected"
+    m_p = o_p = s_p = None
     if a_rows is not None:
         _i32(a_rows, rows, "a_rows")
+        m_p = a_rows.data_ptr()
     if mode == MOE_MODE_SLOT:
         _i32(slot_ids, rows, "slot_ids")
+        s_p = slot_ids.data_ptr()
     else:
         _i32(expert_offsets, E + 1, "expert_offsets")
-    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return (a_q.data_ptr(), a_r, a_s.data_ptr(), s_r, a_n, p(a_rows), w_q.data_ptr(), w_e, w_r, w_s.data_ptr(), v_e, v_r, E, N,
-            2 * k2, mode, p(expert_offsets), p(slot_ids), rows, a_row_div)
+        o_p = expert_offsets.data_ptr()
+    return (a_q.data_ptr(), a_r, a_s.data_ptr(), s_r, a_n, m_p, w_q.data_ptr(), w_e, w_r, w_s.data_ptr(), v_e, v_r, E, N, 2 * k2,
+            mode, o_p, s_p, rows, a_row_div)
 
 
 def mx4_grouped_gemm(a_q, a_s, w_q, w_s, out, *, mode, expert_offsets=None, slot_ids=None, a_rows=None, m_rows=None,
