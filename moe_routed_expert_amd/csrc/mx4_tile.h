@@ -64,7 +64,8 @@ struct Cfg {
     // tile needs more than its 256 registers (385 us instead of 291 for 8 x 2048 rows to 4096 columns of 8192); the others gain
     // (128 x 256: 250 -> 236 us for 256 x 96 rows to 2 x 1024 of 4096).
     static constexpr bool ROLLED = MP > 4;
-    static_assert(NW % 2 == 0 && BP % 32 == 0 && BQ % 32 == 0 && (BP / 8) % NW == 0 && (BQ / 8) % NW == 0, "waves cover the rows evenly");
+    static_assert(NW % 2 == 0 && BP % 32 == 0 && BQ % 32 == 0 && (BP / 8) % NW == 0 && (BQ / 8) % NW == 0,
+                  "waves cover the rows evenly");
 };
 
 // Piece c (16 bytes, one block of 32) of tile row r lies in slot slot_of(c) ^ ((r >> 1) & 7) of the row's eight.  The slots
@@ -277,7 +278,8 @@ __device__ __forceinline__ uint32_t max_lanes16_32(uint32_t v) {
     return b[0] > b[1] ? b[0] : b[1];
 }
 
-// The fused epilogue of four of a wave's sub-tiles (two of gate, two of up, from n0 on): rows row0 + 16m + lane % 16 (below `rows`), act columns col0 .. col0 + 31 (below `cols`).
+// The fused epilogue of four of a wave's sub-tiles (two of gate, two of up, from n0 on): rows row0 + 16m + lane % 16 (below
+// `rows`), act columns col0 .. col0 + 31.
 template <int ACT, int MP, int MQ>
 __device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP][MQ], int n0, int64_t row0, int rows, int64_t col0, int lane) {
     const int r = lane & 15, q = lane >> 4;
@@ -318,7 +320,8 @@ struct Tile {
 };
 
 // The tiles of a launch, COLS output columns each: numbered in panels of kPanel M tiles, M fastest, and dealt so that the
-// workgroups of an XCD stand next to each other (b16_gemm.hip).  Built by the whole workgroup from the device's offsets, with 2 NW + 2 words of scratch LDS.
+// workgroups of an XCD stand next to each other (b16_gemm.hip).  Built by the whole workgroup from the device's offsets, with
+// 2 NW + 2 words of scratch LDS.
 template <class C, int COLS>
 struct Walk {
     const GemmArgs& g;
