@@ -155,11 +155,12 @@ __device__ __forceinline__ float sigmoid32(float l) {
     return l >= 0.0f ? r : t * r;
 }
 
-// e^(x - y) for x <= y, the difference as an exact sum of two floats, so that its rounding does not scale with it.
+// e^(x - y) for x <= y, the difference as an exact sum of two floats, so that its rounding does not scale with it.  Below -104
+// (half a step of 2^-149 is e^-103.97) it is 0 by itself: d may have overflowed there, which leaves no number in `rest`.
 __device__ __forceinline__ float exp_of_difference(float x, float y) {
     const float d = x - y, yy = x - d, xx = d + yy;
     const float rest = (x - xx) + (yy - y);
-    return expf(d) * (1.0f + rest);
+    return d < -104.0f ? 0.0f : expf(d) * (1.0f + rest);
 }
 
 // What a lane needs of its experts for every token: their biases and groups.
