@@ -232,10 +232,11 @@ __device__ __forceinline__ uint32_t step_key(const Steps& s, float c, int e) {
     const float q = (c - s.lo) * s.inv;
     return c > -__builtin_inff() ? (((uint32_t)larger(q, 0.0f) + 1u) << 10) | (1023u - (uint32_t)e) : 0u;
 }
-// A 16-bit logit's own order, exact: equal logits are true ties.
+// A 16-bit logit's own order, exact: equal logits are true ties.  (+inf, fp32's largest value here, is above each type's largest
+// finite one: the conversions round it up to the type's infinity, bf16's by half a step, which changes no other value.)
 __device__ __forceinline__ uint32_t half_key(float v, bool bf16, int e) {
     uint32_t u;
-    if (bf16) u = __float_as_uint(v + 0.0f) >> 16;
+    if (bf16) u = (__float_as_uint(v + 0.0f) + 0x8000u) >> 16;
     else u = f32_to_f16(v + 0.0f);
     u = u >> 15 ? 0xFFFFu & ~u : u | 0x8000u;
     return v > -__builtin_inff() ? ((u + 1u) << 10) | (1023u - (uint32_t)e) : 0u;

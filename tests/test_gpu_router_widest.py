@@ -1,4 +1,4 @@
-"""Weights of a token whose chosen logits lie further apart than fp32 reaches."""
+"""Weights of a token whose chosen logits lie further apart than fp32 reaches, and the order of its widest logits."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +10,7 @@ from test_gpu_router import SIGMOID, SOFTMAX, check
 
 pytestmark = pytest.mark.gpu
 INF, LOW, TOP = np.inf, float(np.finfo(np.float32).min), float(np.finfo(np.float32).max)
+BF16_TOP = float(torch.finfo(torch.bfloat16).max)
 
 
 def widest(E):
@@ -40,3 +41,17 @@ def test_two_routes_far_apart(score):
     for renorm in (True, False):
         r = m.router(x, 2, score=score, renorm=renorm)
         assert r.weights.tolist() == [[1.0, 0.0]] * 3 and r.expert_ids.tolist() == [[0, 1], [1, 0], [0, 1]]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("with_groups", [False, True])
+@pytest.mark.parametrize("T,E,topk", [(3, 16, 1), (5, 64, 6), (70, 96, 12), (4, 1024, 3)])
+def test_infinity_goes_before_the_largest_finite_logit(dt, with_groups, T, E, topk):
+    """+inf counts as fp32's largest value, which is above bf16's and fp16's largest finite one (and equal to fp32's)."""
+    top = {"bf16": BF16_TOP, "fp16": 65504.0, "fp32": TOP}[dt]
+    x = np.zeros((T, E), np.float32)
+    x[:, ::2] = top
+    x[:, 3::4] = INF
+    x[T // 2, E // 2:] = INF
+    x[T // 2, :E // 2] = top
+    check(x, topk, SOFTMAX, G=4 if with_groups else 1, keep=2 if with_groups and topk > 1 else 1, top=1, dt=dt)
