@@ -625,8 +625,8 @@ typedef enum { MOE_MX_FLOOR = 0, MOE_MX_CEIL = 1 } moe_mx_rule;
  *   inactive routes have no row: their route_rows entry is -1, and the expert_offsets[E] rows are followed by dst2src
  *   entries of -1 (moe_gather_rows_scales and a_rows take these as rows of zeros).  All three NULL: not wanted.
  *   workspace: moe_router_workspace_size(T, E) bytes, 16-byte aligned, no initialization; 0 bytes (NULL allowed) up to
- *   64 tokens over up to 64 experts, up to 32 over more, and not used without maps.  Scratch within one call: overlapping
- *   calls need their own.
+ *   64 tokens over up to 64 experts, up to 32 over more, and not used without maps.  Never less for more tokens or experts, so
+ *   one sized for the largest batch serves the smaller ones.  Scratch within one call: overlapping calls need their own.
  *   Requirements: T <= 2^27, 1 <= E <= 1024, 1 <= topk <= min(E, 64), T * topk < 2^31; n_group <= 64 divides E,
  *   topk_group * (E / n_group) >= topk; scale positive and finite.  T == 0 with maps writes the zero offsets.
  */

@@ -1101,6 +1101,13 @@ bool sizes_ok(int64_t T, int64_t E, int64_t topk) {
     return T >= 0 && T <= kMaxT && E >= 1 && E <= kMaxE && topk >= 1 && topk <= std::min<int64_t>(E, kMaxTopk) && T <= 0x7FFFFFFF / topk;
 }
 
+// Bytes of workspace that T tokens take with maps: the chunks' counts, and their sums where a scan forms them.
+int64_t workspace_need(int64_t T, int64_t E) {
+    if (single(T, E)) return 0;
+    const int64_t nc = ceil_div(T, chunk_of(T, E)), rw = row_bytes((int)E);
+    return nc * rw + (nc > kSumChunks ? (nc + 1) * rw * 4 : 0);
+}
+
 bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.402823466e38f; }
 
 bool natural(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % (dt == MOE_F32 ? 4 : 2) == 0; }
@@ -1112,9 +1119,9 @@ bool natural(const void* p, int dt) { return reinterpret_cast<uintptr_t>(p) % (d
 using namespace moe;
 
 extern "C" size_t moe_router_workspace_size(int64_t T, int64_t E) {
-    if (T > router::kMaxT || E < 1 || E > router::kMaxE || router::single(T, E)) return 0;
-    const int64_t nc = ceil_div(T, router::chunk_of(T, E)), rw = router::row_bytes((int)E);
-    const int64_t bytes = nc * rw + (nc > router::kSumChunks ? (nc + 1) * rw * 4 : 0);
+    if (T > router::kMaxT || E < 1 || E > router::kMaxE) return 0;
+    // Chunks grow from 16 tokens to 64 past kTok * kSumChunks tokens, which then need less: not fewer bytes than those.
+    const int64_t bytes = std::max(router::workspace_need(T, E), router::workspace_need(std::min<int64_t>(T, router::kTok * router::kSumChunks), E));
     return (size_t)ceil_div(bytes, 256) * 256;
 }
 
@@ -1148,7 +1155,7 @@ extern "C" int moe_router(const void* logits, int dt, int64_t logits_stride, int
     a.nc = (int)ceil_div(T, a.chunk);
     if (maps && !router::single(T, E)) {
         if (!workspace) return MOE_ERR_NULL;
-        if (ws_bytes < moe_router_workspace_size(T, E)) return MOE_ERR_WORKSPACE;
+        if (ws_bytes < (size_t)router::workspace_need(T, E)) return MOE_ERR_WORKSPACE;
         if (!aligned16(workspace)) return MOE_ERR_ALIGN;
         a.counts = (uint8_t*)workspace;
         a.before = (int32_t*)(a.counts + (int64_t)a.nc * router::row_bytes((int)E));
