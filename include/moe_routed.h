@@ -658,8 +658,9 @@ int moe_router_backward(const void* logits, int dt, int64_t logits_stride, const
  *   act = MOE_ACT_IDENTITY: v = in[r, c];  moe_act 1..5: in row is [gate(0:n) | up(n:2n)], v = act(gate) * up in fp32.
  *   Per group of 32 columns (the last may be shorter): scale by `rule` (moe_mx_rule), at least 2^-127 (byte 0, also that
  *   of a group of zeros); codes e2m1_rne(v / scale), the quotient exact, saturating at 6.  Bit-exact for IDENTITY, RELU and
- *   MUL; the transcendental gates are within a few ulp of their fp32 value.  A group that holds an infinity or NaN takes
- *   scale byte 255 (NaN) and codes 0: every value of it reads as NaN.
+ *   MUL; v of the transcendental gates is, whatever dt, within (1.25 |gate| + 16) 2^-24 of its value (SiLU, sigmoid) or
+ *   (1.25 gate^2 + 32) 2^-24 (GELU), and where act(gate) is below 2^-126 within 2^-150 |up| more.  A group that holds an
+ *   infinity or NaN takes scale byte 255 (NaN) and codes 0: every value of it reads as NaN.
  *   in [rows][in_stride] of dt;  out_q [rows][q_stride] bytes, n/2 written;  out_s [rows][s_stride] bytes, ceil(n/32) written.
  *   Requirements: n even; in aligned to its type.  16-byte aligned rows with n % 8 == 0 and 4-byte aligned code rows take
  *   the vector path.  The products want scale rows at multiples of 4 bytes.
