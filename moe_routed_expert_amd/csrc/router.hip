@@ -97,6 +97,9 @@ __device__ __forceinline__ uint64_t mono64(double v) {
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
+__device__ __forceinline__ double from_mono64(uint64_t u) {
+    return __longlong_as_double((long long)(u >> 63 ? u & 0x7FFFFFFFFFFFFFFFull : ~u));
+}
 // The ten lowest bits of a 64-bit value give way to the index, the others rounded to nearest: 43 significant bits.  (Cut off,
 // values that are equal but for their last rounding, such as sums s(x) + s(-x) = 1, would fall on either side of 1.)
 constexpr uint64_t kLow = 1023;
@@ -493,8 +496,8 @@ __device__ __forceinline__ void refine(const Args& a, int64_t row, int l, float 
 // All of a token in 64 bits, for the very few that have a great many close candidates, or a range that has no 22-bit steps: the
 // workgroup takes one at a time, an expert a thread (7 us where one token of 4096 needs it).
 struct ExactLds {
-    uint64_t top1[kMaxGroups], top2[kMaxGroups];     // keys of each group's two largest choices
-    double val1[kMaxGroups], val2[kMaxGroups];       // and, for their sum, the choices
+    uint64_t top1[kMaxGroups], top2[kMaxGroups];     // each group's largest key; for sums its two largest choices, all their bits
+    int32_t owner[kMaxGroups];                       // the expert whose choice the largest is
     uint64_t part[2][kWaves];
     int32_t id[kMaxTopk];
     float logit[kMaxTopk];                           // of the chosen experts
@@ -555,21 +558,25 @@ __device__ __forceinline__ void rank_exact(const Args& a, int t, ExactLds& lds, 
     if (a.n_group > 1) {                        // the best groups stay
         const int size = a.E / a.n_group, g = min(e / size, kMaxGroups - 1);
         const bool two = WIDE && a.group_top == 2;
-        if (e < a.n_group) lds.top1[e] = lds.top2[e] = 0ull;
+        if (e < a.n_group) {
+            lds.top1[e] = lds.top2[e] = 0ull;
+            lds.owner[e] = kMaxE;
+        }
         __syncthreads();
-        if (key) atomicMax((unsigned long long*)&lds.top1[g], (unsigned long long)key);
+        // (a key would leave it to the index which of two choices that are one value in 43 bits enters the sum)
+        const uint64_t entry = key ? (two ? mono64(c) : key) : 0ull;
+        if (entry) atomicMax((unsigned long long*)&lds.top1[g], (unsigned long long)entry);
         __syncthreads();
         if (two) {
-            if (key && key == lds.top1[g]) lds.val1[g] = c;
-            else if (key) atomicMax((unsigned long long*)&lds.top2[g], (unsigned long long)key);
+            if (entry && entry == lds.top1[g]) atomicMin(&lds.owner[g], e);
             __syncthreads();
-            if (key && key == lds.top2[g]) lds.val2[g] = c;
+            if (entry && lds.owner[g] != e) atomicMax((unsigned long long*)&lds.top2[g], (unsigned long long)entry);
             __syncthreads();
         }
         uint64_t gk = 0ull;
         if (e < a.n_group && lds.top1[e]) {
             gk = lds.top1[e];                   // its index orders ties by group as well
-            if (two) gk = value_key(lds.top2[e] ? lds.val1[e] + lds.val2[e] : lds.val1[e], e);
+            if (two) gk = value_key(lds.top2[e] ? from_mono64(lds.top1[e]) + from_mono64(lds.top2[e]) : from_mono64(lds.top1[e]), e);
         }
         uint64_t kept = 0ull;
         for (int n = 0; n < a.keep; n++) {
