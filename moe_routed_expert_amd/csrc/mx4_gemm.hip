@@ -263,7 +263,7 @@ __device__ __forceinline__ void run_tiles(const GemmArgs& g, const W& walk, uint
         const int cols = (int)min(g.N - c0, (int64_t)(COLS / C::WQ));
         const int64_t r0 = ti.row0 + wp * C::MP * 16;
         if (rows > 0 && cols > 0) {
-            if constexpr (FUSED) store_act_of(g, acc, 0, r0, rows, c0, fresh(lane));
+            if constexpr (FUSED) store_act_of(g, acc, r0, rows, c0, fresh(lane));
             else b16::store_wave_dt(g.out, g.out_dt, false, r0 * g.out_stride + c0, g.out_stride, rows, cols, acc, fresh(lane));
         }
     }

@@ -278,10 +278,10 @@ __device__ __forceinline__ uint32_t max_lanes16_32(uint32_t v) {
     return b[0] > b[1] ? b[0] : b[1];
 }
 
-// The fused epilogue of four of a wave's sub-tiles (two of gate, two of up, from n0 on): rows row0 + 16m + lane % 16 (below
-// `rows`), act columns col0 .. col0 + 31.
+// The fused epilogue of a wave's sub-tiles, two of gate and two of up: rows row0 + 16m + lane % 16 (below `rows`), act columns
+// col0 .. col0 + 31.
 template <int ACT, int MP, int MQ>
-__device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP][MQ], int n0, int64_t row0, int rows, int64_t col0, int lane) {
+__device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP][MQ], int64_t row0, int rows, int64_t col0, int lane) {
     const int r = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int m = 0; m < MP; m++) {
@@ -290,7 +290,7 @@ __device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP
 #pragma unroll
         for (int n = 0; n < 2; n++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) h[4 * n + i] = gated<ACT>(acc[m][n0 + n][i], acc[m][n0 + n + 2][i]);
+            for (int i = 0; i < 4; i++) h[4 * n + i] = gated<ACT>(acc[m][n][i], acc[m][n + 2][i]);
         const uint32_t byte = scale_byte(max_lanes16_32(max_bits8(h)), g.ceil != 0);
         const uint32_t codes = encode8(h, byte);
         if (m * 16 + r < rows) {
@@ -304,13 +304,13 @@ __device__ __forceinline__ void store_act(const GemmArgs& g, const v4f (&acc)[MP
 }
 
 template <int MP, int MQ>
-__device__ __forceinline__ void store_act_of(const GemmArgs& g, const v4f (&acc)[MP][MQ], int n0, int64_t row0, int rows, int64_t col0, int lane) {
+__device__ __forceinline__ void store_act_of(const GemmArgs& g, const v4f (&acc)[MP][MQ], int64_t row0, int rows, int64_t col0, int lane) {
     switch (g.act) {
-        case 1: return store_act<1>(g, acc, n0, row0, rows, col0, lane);
-        case 2: return store_act<2>(g, acc, n0, row0, rows, col0, lane);
-        case 3: return store_act<3>(g, acc, n0, row0, rows, col0, lane);
-        case 4: return store_act<4>(g, acc, n0, row0, rows, col0, lane);
-        default: return store_act<5>(g, acc, n0, row0, rows, col0, lane);
+        case 1: return store_act<1>(g, acc, row0, rows, col0, lane);
+        case 2: return store_act<2>(g, acc, row0, rows, col0, lane);
+        case 3: return store_act<3>(g, acc, row0, rows, col0, lane);
+        case 4: return store_act<4>(g, acc, row0, rows, col0, lane);
+        default: return store_act<5>(g, acc, row0, rows, col0, lane);
     }
 }
 
