@@ -607,7 +607,9 @@ typedef enum { MOE_MX_FLOOR = 0, MOE_MX_CEIL = 1 } moe_mx_rule;
 /*
  * moe_router  -- scores, choice, weights and route maps
  *   logits   DEVICE [T][logits_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32), E used.  -inf and NaN mask their expert for that
- *            token (its score is 0); +inf counts as fp32's largest value.
+ *            token (its score is 0); +inf counts as fp32's largest value, and fp32's lowest is a logit like any other.  (As a
+ *            mask -inf is the quick one: fp32 logits ranked without a bias leave the fast path where some lie beyond 1e30, and
+ *            fp32 logits or biased scores where all that are not masked are equal: 6 to 8 us a token, one by one on a CU.)
  *   s        scores of the logits (moe_score).  The masked experts take no part in the softmax.
  *   c        choices s + bias (bias DEVICE fp32 [E]; a bias of -inf or NaN takes its expert from every choice), or, with bias
  *            NULL, the order of the logits themselves.
@@ -618,9 +620,11 @@ typedef enum { MOE_MX_FLOOR = 0, MOE_MX_CEIL = 1 } moe_mx_rule;
  *            expert is left (an inactive route for every other entry point).
  *   weights  [T][topk] fp32: scale * s_j, or scale * s_j / sum_i s_i over the token's routes (renorm = 1; formed as
  *            ratios, so scores that underflow still divide); +0 where the id is -1.
- *   scores   [T][E] fp32: s, for an auxiliary loss; NULL: not wanted.
- *   Ties go to the lower index, of experts and of groups.  Choices and sums of two are formed in 64 bits and rounded to 43
- *   significant bits for the comparison.
+ *   scores   [T][E] fp32: s, for an auxiliary loss; NULL: not wanted.  Formed in fp32 from the hardware's exponential: within
+ *            (2.5 d + 48) 2^-24 of s, d the distance of the logit from the token's largest (sigmoid: from 0); one below 2^-126
+ *            may be 0.  The weights are within 2^-18 of their value where that is 2^-126 or more.
+ *   Ties go to the lower index, of experts and of groups.  Choices and sums of the two largest are formed in 64 bits and each
+ *   rounded once to 43 significant bits for the comparison (those below 2^-1012 to fewer).
  *   dst2src, route_rows [T*topk], expert_offsets [E+1] int32: the route maps of moe_route_prep over the active routes;
  *   inactive routes have no row: their route_rows entry is -1, and the expert_offsets[E] rows are followed by dst2src
  *   entries of -1 (moe_gather_rows_scales and a_rows take these as rows of zeros).  All three NULL: not wanted.
@@ -671,7 +675,8 @@ int moe_mx4_quant(const void* in, int dt, int64_t in_stride, int64_t rows, int64
 /*
  * moe_mx4_dequant  -- MXFP4 rows back to values
  *   out[r, c] = code * scale, rounded once to out_dt: exact in fp32 (subnormals included) and bf16 (scales of 2^-126 and
- *   more); fp16 overflows to infinity past 65504.  NaN under scale byte 255.  Layouts as moe_mx4_quant.
+ *   more); infinity past the type's largest value (fp16: 65504; fp32 and bf16: codes 4 and 6 under scales of 2^126 and 2^127,
+ *   and 2 and 3 under 2^127).  NaN under scale byte 255.  Layouts as moe_mx4_quant.
  */
 int moe_mx4_dequant(const uint8_t* q, int64_t q_stride, const uint8_t* s, int64_t s_stride, int64_t rows, int64_t n,
                     void* out, int out_dt, int64_t out_stride, void* stream);
@@ -705,7 +710,8 @@ int moe_mx4_grouped_tile(int64_t m_rows, int64_t n_experts, int64_t N, int64_t K
  * moe_mx4_grouped_gemm_act_quant  -- the gate/up GEMM with the gated activation and its MXFP4 requant in the epilogue
  *   c1 is the fp32 result of moe_mx4_grouped_gemm with N = 2I (W13 rows 0..I-1 gate, I..2I-1 up), never stored; out_q, out_s
  *   are moe_mx4_quant's of it with `act` (1..5) and `rule`.  The results equal moe_mx4_grouped_gemm with MOE_F32 output
- *   followed by moe_mx4_quant, bit for bit.  Both modes; an inactive route gets codes 0 and scale bytes 0.
+ *   followed by moe_mx4_quant, bit for bit, in both modes.  Slot mode: an inactive route gets codes 0 and scale bytes 0.
+ *   Grouped mode: rows from expert_offsets[n_experts] on, where moe_router leaves the inactive routes, stay as they were.
  *   Requirements: I % 32 == 0; out_q and q_stride even; slot mode: m_rows * I / 32 < 2^22; the rest as
  *   moe_mx4_grouped_gemm with N = 2I.
  */

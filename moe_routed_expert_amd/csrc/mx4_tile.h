@@ -78,7 +78,8 @@ __device__ __forceinline__ int slot_of(int c) { return (c & 4) | ((c & 1) << 1) 
 // all of them before any LDS read.
 //   dma16 / dma4  from an address of each lane's own: operands of any extent.
 //   buf16 / buf4  from a buffer (base and extent in scalar registers) at a 32-bit offset of each lane's own plus a scalar one:
-//                 no vector instruction per load, and an offset of kNowhere or more is out of range, which reads as zeros.
+//                 no vector instruction per load, and an offset of kNowhere or more is out of range, which reads as zeros.  Both
+//                 offsets count in the range check, also where the scalar one alone is past the extent (checked on the device).
 __device__ __forceinline__ void dma4(const void* src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }

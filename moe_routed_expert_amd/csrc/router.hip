@@ -13,7 +13,8 @@
 //    86 us where this takes 39 (16384 tokens, 512 experts).  So keys are 32 bits: 22-bit steps over the token's own range, formed
 //    with 32-bit scores whose error is known in steps.  Where two keys that matter are closer than that, the candidates alone
 //    are ranked again in 64 bits: of experts (refine, one token in a hundred) or groups (exact_groups, one in ten thousand).
-//    What even that leaves open is ranked as a whole (rank_exact).  16-bit logits fit a key as they are.
+//    What even that leaves open, and tokens whose range has no such steps, are ranked as a whole, one after the other
+//    (rank_exact).  16-bit logits fit a key as they are.
 //  * Up to 64 experts a token takes 16 lanes of a wave, beyond a whole wave; lanes hold experts lane, lane + LPT, ... .
 //    Every round's largest key is found by lane moves folded into the maximum, then struck out.
 //  * A workgroup takes 16 tokens at a time and counts its routes in LDS, the chunk's loads.  Up to 64 tokens (32 of more than
@@ -147,7 +148,8 @@ __device__ __forceinline__ double sigmoid64(double l) {
     const double t = exp(-fabs(l)), r = 1.0 / (1.0 + t);
     return l >= 0.0 ? r : t * r;
 }
-// From the hardware exp2 and reciprocal, within an ulp each: e^x for x <= 0 is within (1.5 |x| + 2) 2^-24 of itself.
+// From the hardware exp2 and reciprocal, within an ulp each: e^x for x <= 0 is within (1.25 |x| + 2) 2^-24 of itself (a
+// difference as x adds |x| by its rounding).
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 __device__ __forceinline__ float fast_score(float l) {
     const float t = fast_exp(-__builtin_fabsf(l)), r = __builtin_amdgcn_rcpf(1.0f + t);
@@ -338,10 +340,10 @@ __device__ __forceinline__ bool rank_fast(const Args& a, int64_t row, const Lane
             c[i] = (softmax ? fast_exp(s.v[i] - s.top) * inv : fast_score(s.v[i])) + x.bias[i];
             c[i] = s.v[i] > -kInf && c[i] > -kInf ? c[i] : -kInf;
         }
-        // In units of 2^-24, with the hardware exp2 and reciprocal: a sigmoid is off by t (1.5 |x| + 2) / (1 + t)^2 < 1 for t, 1
-        // for 1 + t, 2 for its reciprocal, 1 for the product.  A softmax score is inv at most and off by inv times: e^-d (1.5 d +
-        // 2) < 3, 2 for the reciprocal, 1 for the product, and for the sum 1.5 ln E + 2 < 13 and 22 additions.  Then the bias's
-        // addition rounds.
+        // In units of 2^-24, with the hardware exp2 and reciprocal: a sigmoid is off by t (1.25 |x| + 2) / (1 + t)^2 < 1 for t, 1
+        // for 1 + t, 2 for its reciprocal, 1 for the product.  A softmax score is inv at most and off by inv times: e^-d (2.25 d +
+        // 2) < 3, 2 for the reciprocal, 1 for the product, and for the sum 2.25 ln E + 2 < 18 and 22 additions: 46 of the 64 that
+        // are allowed.  Then the bias's addition rounds.
         const Steps st = steps_of<LPT, VPL>(c, GROUPS || LPT == 16, softmax ? 0x1p-18f * inv : 0x1p-21f);
 #pragma unroll
         for (int i = 0; i < VPL; i++) key[i] = step_key(st, c[i], i * LPT + l);
@@ -493,8 +495,11 @@ __device__ __forceinline__ void refine(const Args& a, int64_t row, int l, float 
         if (mine[q]) mine[q] = lds.top1[q * LPT + l];   // (the keys there are lead)
 }
 
-// All of a token in 64 bits, for the very few that have a great many close candidates, or a range that has no 22-bit steps: the
-// workgroup takes one at a time, an expert a thread (7 us where one token of 4096 needs it).
+// All of a token in 64 bits, where it has a great many close candidates or its range has no 22-bit steps: the workgroup takes one
+// at a time, an expert a thread, 6 to 8 us each.  Hardly a token of random logits needs it, but whole batches can:
+// fp32 logits (or biased scores) that are all equal, one choosable expert a token, and logits ranked without a bias among which
+// some are the type's lowest value in place of -inf.  Then 4096 tokens of 256 experts take 96 to 135 us instead of 14, 64 of 64
+// (one workgroup) 340 to 460 instead of 10; -inf as the mask, and 16-bit logits, stay with the 32-bit keys.
 struct ExactLds {
     uint64_t top1[kMaxGroups], top2[kMaxGroups];     // each group's largest key; for sums its two largest choices, all their bits
     int32_t owner[kMaxGroups];                       // the expert whose choice the largest is
@@ -867,7 +872,7 @@ __global__ void __launch_bounds__(kScatterThreads) scatter_kernel(const Args a) 
         __syncthreads();
     } else {
         // Four experts a thread (a word of a chunk's counts), the chunks dealt over the parts of the workgroup, kAsk of them asked
-        // for at once; sums of bytes as 16-bit pairs (at most 512 chunks of 16 tokens), added up over the parts through LDS.
+        // for at once; sums of bytes as 16-bit pairs (at most 512 chunks of 64 tokens: 32768), added up over the parts through LDS.
         constexpr int kAsk = 16;
         const int quads = rw / 4, parts = kScatterThreads / quads;
         const int part = threadIdx.x / quads, qd = threadIdx.x - part * quads;
@@ -933,7 +938,12 @@ __global__ void zero_offsets_kernel(int E, int32_t* offsets) {
 }
 
 // One workgroup, one launch.  (256 experts in 8 groups, in a graph: 64 tokens 29 us so and 13.6 in two launches of more, 32
-// tokens 16.8 and 13.5, 16 tokens 10.6; outside of one the second launch costs the caller 4 us.)
+// tokens 16.8 and 13.5, 16 tokens 10.6; outside of one the second launch costs the caller 4 us.  So 17 to 32 tokens of more than
+// 64 experts are the quicker in one launch as eager calls, and up to 3 us slower in a graph.)
+// Chunks: 16 tokens up to 512 chunks, then 64.  Without groups, over 256 experts, 8192 tokens take 25.0 us, 8193 25.7, 16384 26.9,
+// 24576 49.8 and 32768 51.2; in 8 groups 31.1, 37.2, 36.1, 69.4 and 70.1.  A CU holds one workgroup, so chunks of 64 leave half of
+// the card idle just past 8192.  Past 32768 the scan, one workgroup for 256 experts, takes nearly half of the time: 32769 tokens
+// 93.7 us, 131072 344.
 bool single(int64_t T, int64_t E) { return T <= (E <= 64 ? kSingle : kSingleWide); }
 int chunk_of(int64_t T, int64_t E) { return single(T, E) ? kSingle : T <= (int64_t)kTok * kSumChunks ? kTok : 64; }
 
@@ -966,6 +976,9 @@ void launch_route_groups(hipStream_t st, const Args& a) {
     else launch_route_e<WIDE, SOFT, false>(st, a);
 }
 
+// The kernels of 513 to 1024 experts spill 96 to 113 vector registers with groups and choices, 55 with groups alone, 2 to 19
+// without; those of 257 to 512 experts 8 to 20 with groups and choices, the others none.  (1024 experts, 4096 tokens: 24.2 us,
+// with a bias and 32 groups 55.9.)
 // What a kernel knows: whether choices (scores formed) or logits are ranked, the scores' form, whether there are groups.  (With
 // all of it in one kernel the registers of the groups' part spill in the others': 16384 tokens over 512 experts 50.9 us
 // instead of 46.)
