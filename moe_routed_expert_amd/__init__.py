@@ -659,6 +659,8 @@ def mx4_quant(x, out_q, out_s, act=MOE_ACT_IDENTITY, rule=MOE_MX_FLOOR, stream=N
     assert out_q.dtype is _U8 and out_s.dtype is _U8, "codes and scales are uint8"
     assert out_q.shape == (rows, n // 2) and out_s.shape == (rows, (n + 31) // 32), "outputs do not match"
     assert x_1 == 1 and q_1 == 1 and (s_1 == 1 or n <= 32), _UNIT
+    if rows == 1:                       # a single row's stride says nothing about it (a transposed column's is 1)
+        x_r, q_r, s_r = width, n // 2, (n + 31) // 32
     _call("moe_mx4_quant", (x, out_q, out_s), (
         x.data_ptr(), _DT[x.dtype], x_r, rows, n, act, rule, out_q.data_ptr(), q_r, out_s.data_ptr(), s_r), stream)
 
@@ -672,6 +674,8 @@ def mx4_dequant(q, s, out, stream=None):
     assert q.dtype is _U8 and s.dtype is _U8, "codes and scales are uint8"
     assert n % 2 == 0 and q.shape == (rows, n // 2) and s.shape == (rows, (n + 31) // 32), "operands do not match"
     assert o_1 == 1 and q_1 == 1 and (s_1 == 1 or n <= 32), _UNIT
+    if rows == 1:
+        o_r, q_r, s_r = n, n // 2, (n + 31) // 32
     _call("moe_mx4_dequant", (q, s, out), (q.data_ptr(), q_r, s.data_ptr(), s_r, rows, n, out.data_ptr(), _DT[out.dtype], o_r),
           stream)
 
@@ -694,6 +698,8 @@ def _mx4_operands(a_q, a_s, w_q, w_s, mode, expert_offsets, slot_ids, a_rows, ro
         for t in (a_s, w_s):
             last = t.storage_offset() + sum((n - 1) * st for n, st in zip(t.shape[:-1], t.stride()[:-1])) + (groups + 3) // 4 * 4
             assert not t.numel() or last <= t.untyped_storage().nbytes(), "scale rows padded to a multiple of four bytes expected"
+    if a_n == 1:                        # a single row's stride says nothing about it
+        a_r, s_r = k2, (groups + 3) // 4 * 4
     m_p = o_p = s_p = None
     if a_rows is not None:
         _i32(a_rows, rows, "a_rows")
@@ -717,6 +723,8 @@ def mx4_grouped_gemm(a_q, a_s, w_q, w_s, out, *, mode, expert_offsets=None, slot
     o_r, o_1 = out.stride()
     rows = o_rows if m_rows is None else m_rows
     assert w_q.shape[1] == N and o_1 == 1 and 0 <= rows <= o_rows, "out does not match"
+    if o_rows == 1:
+        o_r = N
     args = _mx4_operands(a_q, a_s, w_q, w_s, mode, expert_offsets, slot_ids, a_rows, rows, a_row_div, N)
     _call("moe_mx4_grouped_gemm", (a_q, a_s, w_q, w_s, out, expert_offsets, slot_ids, a_rows),
           args + (out.data_ptr(), _DT[out.dtype], o_r), stream)
@@ -740,6 +748,8 @@ def mx4_grouped_gemm_act_quant(a_q, a_s, w13_q, w13_s, out_q, out_s, *, mode, ex
     assert out_q.dtype is _U8 and out_s.dtype is _U8, "codes and scales are uint8"
     assert i2 % 16 == 0 and out_s.shape == (o_rows, i2 // 16) and w13_q.shape[1] == 4 * i2 and 0 <= rows <= o_rows, "outputs do not match"
     assert q_1 == 1 and (s_1 == 1 or i2 == 16), _UNIT
+    if o_rows == 1:
+        q_r, s_r = i2, i2 // 16
     args = _mx4_operands(a_q, a_s, w13_q, w13_s, mode, expert_offsets, slot_ids, a_rows, rows, a_row_div, 2 * i2)
     _call("moe_mx4_grouped_gemm_act_quant", (a_q, a_s, w13_q, w13_s, out_q, out_s, expert_offsets, slot_ids, a_rows),
           args + (act, rule, out_q.data_ptr(), q_r, out_s.data_ptr(), s_r), stream)
