@@ -608,8 +608,8 @@ typedef enum { MOE_MX_FLOOR = 0, MOE_MX_CEIL = 1 } moe_mx_rule;
  * moe_router  -- scores, choice, weights and route maps
  *   logits   DEVICE [T][logits_stride] of dt (MOE_BF16, MOE_F16 or MOE_F32), E used.  -inf and NaN mask their expert for that
  *            token (its score is 0); +inf counts as fp32's largest value, and fp32's lowest is a logit like any other.  (As a
- *            mask -inf is the quick one: fp32 logits ranked without a bias leave the fast path where some lie beyond 1e30, and
- *            fp32 logits or biased scores where all that are not masked are equal: 6 to 8 us a token, one by one on a CU.)
+ *            mask -inf is the quick one, in a bias too: fp32 logits ranked without a bias, and biased scores, leave the fast
+ *            path where some lie beyond 1e30 or all that are not masked are equal: 6 to 8 us a token, one by one on a CU.)
  *   s        scores of the logits (moe_score).  The masked experts take no part in the softmax.
  *   c        choices s + bias (bias DEVICE fp32 [E]; a bias of -inf or NaN takes its expert from every choice), or, with bias
  *            NULL, the order of the logits themselves.

@@ -497,9 +497,10 @@ __device__ __forceinline__ void refine(const Args& a, int64_t row, int l, float 
 
 // All of a token in 64 bits, where it has a great many close candidates or its range has no 22-bit steps: the workgroup takes one
 // at a time, an expert a thread, 6 to 8 us each.  Hardly a token of random logits needs it, but whole batches can:
-// fp32 logits (or biased scores) that are all equal, one choosable expert a token, and logits ranked without a bias among which
-// some are the type's lowest value in place of -inf.  Then 4096 tokens of 256 experts take 96 to 135 us instead of 14, 64 of 64
-// (one workgroup) 340 to 460 instead of 10; -inf as the mask, and 16-bit logits, stay with the 32-bit keys.
+// fp32 logits (or biased scores) that are all equal, one choosable expert a token, and fp32 logits ranked without a bias, or
+// biases, among which some are the type's lowest value in place of -inf.  Then 4096 tokens of 256 experts take 96 to 135 us
+// instead of 14, 64 of 64 (one workgroup) 340 to 460 instead of 10; -inf as the mask, and 16-bit logits without a bias, stay with
+// the 32-bit keys.
 struct ExactLds {
     uint64_t top1[kMaxGroups], top2[kMaxGroups];     // each group's largest key; for sums its two largest choices, all their bits
     int32_t owner[kMaxGroups];                       // the expert whose choice the largest is
